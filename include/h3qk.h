@@ -73,7 +73,8 @@ typedef enum h3qk_dtype {
     H3QK_DTYPE_DEFAULT = 0, /* in h3qk_opts.in_dtype only: see there */
     H3QK_FP16 = 1,          /* IEEE binary16 */
     H3QK_BF16 = 2,          /* bfloat16 */
-    H3QK_E4M3 = 3           /* OCP 8-bit E4M3FN codes (output only) */
+    H3QK_E4M3 = 3,          /* OCP 8-bit E4M3FN codes (output only) */
+    H3QK_FP32 = 4           /* IEEE binary32 (layer norm only) */
 } h3qk_dtype;
 
 typedef enum h3qk_scale_mode {
@@ -385,6 +386,82 @@ h3qk_status h3qk_silu_and_mul(const void* x, h3qk_dtype dtype, int64_t rows, int
 h3qk_status h3qk_scaled_residual(const float* residual, const void* branch, h3qk_dtype branch_dtype,
                                  const float* scale, int64_t rows, int32_t channels, int32_t scale_len,
                                  float* out, h3qk_stream_t stream);
+
+/*
+ * The attention block around the path: layer norm before the projection,
+ * the gradient of h3qk_prepare, and attention on what it writes.  These are
+ * defined by their formulas and checked against binary64; unlike the path
+ * above their results are not pinned bit for bit to the oracle, but the same
+ * call gives the same bits on every run (sums are added in a fixed order,
+ * without atomics).  Pointers, checks, asynchrony and errors as for
+ * h3qk_prepare: device memory owned by the caller, every argument checked on
+ * the host before anything is enqueued, nothing allocated, no
+ * synchronisation.
+ */
+
+/*
+ * h3qk_layer_norm: per row of `width` values,
+ *   mean = sum x / C,  rstd = 1 / sqrt(sum (x - mean)^2 / C + eps),
+ *   out = (x - mean) rstd w + b,  stats = (mean, rstd),
+ * in binary32, rounded once to the row type.
+ *   x          [rows, row_stride] of dtype (FP16, BF16 or FP32), row_stride
+ *              >= width elements (0: width).  Element alignment is enough;
+ *              rows that start on 16-byte boundaries are read fastest.
+ *   width      1 to 16384.
+ *   weight, bias  float [groups, width], each NULL for 1 and 0.  Rows are
+ *              cut into `groups` equal runs, run g using row g (an adaptive
+ *              norm with a scale and shift per item); groups 1 shares one.
+ *   out        [rows, width] contiguous, of dtype; may not overlap an input.
+ *   stats      float [rows, 2], 8-byte aligned.
+ */
+h3qk_status h3qk_layer_norm(const void* x, h3qk_dtype dtype, int64_t rows, int32_t width, int64_t row_stride,
+                            const float* weight, const float* bias, int64_t groups, float eps, void* out,
+                            float* stats, h3qk_stream_t stream);
+
+/*
+ * h3qk_layer_norm_backward: with xh = (x - mean) rstd and g = grad_out w,
+ *   grad_x = rstd (g - mean(g) - xh mean(g xh)),
+ *   grad_weight = sum of grad_out xh, grad_bias = sum of grad_out, over the
+ *   rows of each group (float [groups, width], each NULL when not wanted).
+ * grad_out [rows, grad_stride] (0: width) and x [rows, row_stride] of dtype,
+ * stats as h3qk_layer_norm wrote them, grad_x [rows, width] contiguous.
+ * workspace: device memory of at least
+ * h3qk_layer_norm_backward_workspace_bytes(rows, width, groups) bytes,
+ * 16-byte aligned (unused, may be NULL, when both weight gradients are
+ * NULL); it holds partial sums during the call.  No output may overlap an
+ * input or another output.
+ */
+size_t h3qk_layer_norm_backward_workspace_bytes(int64_t rows, int32_t width, int64_t groups);
+h3qk_status h3qk_layer_norm_backward(const void* grad_out, int64_t grad_stride, const void* x, h3qk_dtype dtype,
+                                     int64_t rows, int32_t width, int64_t row_stride, const float* weight,
+                                     int64_t groups, const float* stats, void* grad_x, float* grad_weight,
+                                     float* grad_bias, void* workspace, size_t workspace_bytes,
+                                     h3qk_stream_t stream);
+
+/*
+ * h3qk_prepare_backward: the gradient of a 16-bit h3qk_prepare call.  From
+ * grad_q, grad_k, grad_v (the layout opts->out_layout names, of the input
+ * type) and the call's own inputs it writes grad_qkv [tokens, 3*heads*head_dim]
+ * contiguous (the input type) and the weight gradients grad_wq, grad_wk
+ * (float[head_dim], each NULL when not wanted):
+ *   dn = R^T dy (the rotation by minus the angle of the forward call),
+ *   grad_w = sum over rows and heads of dn x inv,
+ *   grad_x = inv dn w - x inv^3 (sum_d dn w x) / D,  inv = (sum x^2 / D + eps)^-1/2;
+ * the V part of grad_qkv is grad_v.  The forward's 16-bit rounding points
+ * count as the identity.  Rows past the valid prefix get zeros and their
+ * gradients are not read.
+ * opts as for h3qk_prepare (in_dtype DEFAULT means BF16; static_scales,
+ * workspace and sat_counts are ignored).  workspace: device memory of at
+ * least h3qk_prepare_backward_workspace_bytes(head_dim) bytes on the current
+ * device, 16-byte aligned.  No output may overlap an input or another output.
+ */
+size_t h3qk_prepare_backward_workspace_bytes(int32_t head_dim);
+h3qk_status h3qk_prepare_backward(const void* grad_q, const void* grad_k, const void* grad_v, const void* qkv,
+                                  const float* norm_wq, const float* norm_wk, const int32_t* positions,
+                                  int64_t tokens, int32_t heads, int32_t head_dim, int32_t rotary_dim,
+                                  int64_t valid_len, void* grad_qkv, float* grad_wq, float* grad_wk,
+                                  void* workspace, size_t workspace_bytes, const h3qk_opts* opts,
+                                  h3qk_stream_t stream);
 
 /* A static, human-readable name of a status. */
 const char* h3qk_status_string(h3qk_status status);

@@ -1,0 +1,218 @@
+"""Python binding of the attention block's operators: layer norm and its
+gradient, and the gradient of the fused QK preparation.
+
+As in ``h3qk``, this only checks tensors and passes their addresses: each
+operator runs in the library's CUDA kernels on the caller's stream, and
+workspaces come from torch's allocator unless the caller passes one.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import h3qk
+from .h3qk import BF16, FP16, OK, H3QKError, _need, _need_common, _opts_for, _ptr
+
+FP32 = 4
+_DTYPES = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
+_P, _I32, _I64, _SZ, _F, _INT = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float,
+                                 ctypes.c_int)
+
+_SIGNATURES = {
+    "h3qk_layer_norm": (_INT, [_P, _INT, _I64, _I32, _I64, _P, _P, _I64, _F, _P, _P, _P]),
+    "h3qk_layer_norm_backward_workspace_bytes": (_SZ, [_I64, _I32, _I64]),
+    "h3qk_layer_norm_backward": (_INT, [_P, _I64, _P, _INT, _I64, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "h3qk_prepare_backward_workspace_bytes": (_SZ, [_I32]),
+    "h3qk_prepare_backward": (_INT, [_P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _SZ,
+                                     ctypes.POINTER(h3qk.Opts), _P]),
+}
+
+
+def _fn(name):
+    f = getattr(h3qk.lib(), name)
+    if f.argtypes is None:
+        f.restype, f.argtypes = _SIGNATURES[name]
+    return f
+
+
+def _stream(stream, dev):
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _call(name, dev, *args):
+    """A library call with the tensors' device current (the library keys its
+    caches on it)."""
+    f = _fn(name)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args)
+    if st != OK:
+        raise H3QKError(st, h3qk.status_string(st), int(h3qk.lib().h3qk_last_cuda_error()), name)
+
+
+def _size(name, dev, *args):
+    """A workspace size, asked with the tensors' device current."""
+    if dev.index == torch.cuda.current_device():
+        return _fn(name)(*args)
+    with torch.cuda.device(dev):
+        return _fn(name)(*args)
+
+
+def _workspace(workspace, nbytes, dev):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+    _need(workspace, "workspace", device=dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _need_rows(x, name, dtypes):
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D [rows, width] with unit inner stride")
+    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows")
+
+
+def _row_stride(x):
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _need_affine(w, name, width, batch, dev):
+    """The groups a weight stands for: [width] is shared, [batch, width] has a row per item."""
+    if w.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {w.dtype}")
+    if tuple(w.shape) not in ((width,), (batch, width)):
+        raise ValueError(f"{name} must have shape ({width},) or ({batch}, {width}), got {tuple(w.shape)}")
+    if not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if w.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {w.device}")
+    return 1 if w.dim() == 1 else batch
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6, batch: int = 1, out=None, stats=None, stream=None):
+    """Layer norm of the rows of x [rows, width] (float16, bfloat16 or
+    float32; any row stride >= width).  ``weight`` and ``bias`` are float32
+    [width], or [batch, width] with one row per item of rows / batch rows (an
+    adaptive norm).  Returns (y, stats): y [rows, width] of x's type, stats
+    float32 [rows, 2] with each row's mean and reciprocal deviation, which
+    ``layer_norm_backward`` reads (h3qk_layer_norm)."""
+    _need_rows(x, "x", tuple(_DTYPES))
+    rows, width = x.shape
+    dev = x.device
+    if batch < 1 or rows % batch:
+        raise ValueError("rows must be a multiple of batch")
+    groups = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            g = _need_affine(t, name, width, batch, dev)
+            if groups is not None and g != groups:
+                raise ValueError("weight and bias must have the same shape")
+            groups = g
+    if out is None:
+        out = torch.empty((rows, width), dtype=x.dtype, device=dev)
+    else:
+        _need(out, "out", device=dev, dtypes=(x.dtype,), numel=rows * width)
+    if stats is None:
+        stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    else:
+        _need(stats, "stats", device=dev, dtypes=(torch.float32,), numel=2 * rows)
+    _call("h3qk_layer_norm", dev, x.data_ptr(), _DTYPES[x.dtype], rows, width, _row_stride(x), _ptr(weight), _ptr(bias),
+          groups or 1, eps, out.data_ptr(), stats.data_ptr(), _stream(stream, dev))
+    return out, stats
+
+
+def layer_norm_backward(grad_out, x, weight, stats, *, batch: int = 1, need_weight_grad: bool = True, out=None,
+                        grad_weight=None, grad_bias=None, workspace=None, stream=None):
+    """The gradient of ``layer_norm``: grad_out [rows, width] of x's type, x
+    and weight as the forward took them, stats as it returned them.  Returns
+    (grad_x, grad_weight, grad_bias); the last two are float32 of the
+    weight's shape, summed over the rows that share them, or None without a
+    weight or with ``need_weight_grad=False`` (h3qk_layer_norm_backward)."""
+    _need_rows(x, "x", tuple(_DTYPES))
+    _need_rows(grad_out, "grad_out", (x.dtype,))
+    rows, width = x.shape
+    dev = x.device
+    if tuple(grad_out.shape) != (rows, width) or grad_out.device != dev:
+        raise ValueError(f"grad_out must have shape ({rows}, {width}) on {dev}")
+    if batch < 1 or rows % batch:
+        raise ValueError("rows must be a multiple of batch")
+    _need(stats, "stats", device=dev, dtypes=(torch.float32,), numel=2 * rows)
+    groups = 1 if weight is None else _need_affine(weight, "weight", width, batch, dev)
+    if out is None:
+        out = torch.empty((rows, width), dtype=x.dtype, device=dev)
+    else:
+        _need(out, "out", device=dev, dtypes=(x.dtype,), numel=rows * width)
+    sums = weight is not None and need_weight_grad
+    ws_bytes = 0
+    if sums:
+        if grad_weight is None:
+            grad_weight = torch.empty_like(weight)
+        if grad_bias is None:
+            grad_bias = torch.empty_like(weight)
+        for t, name in ((grad_weight, "grad_weight"), (grad_bias, "grad_bias")):
+            _need(t, name, device=dev, dtypes=(torch.float32,), numel=groups * width)
+        workspace, ws_bytes = _workspace(
+            workspace, _size("h3qk_layer_norm_backward_workspace_bytes", dev, rows, width, groups), dev)
+    else:
+        grad_weight = grad_bias = workspace = None
+    _call("h3qk_layer_norm_backward", dev, grad_out.data_ptr(), _row_stride(grad_out), x.data_ptr(), _DTYPES[x.dtype],
+          rows, width, _row_stride(x), _ptr(weight), groups, stats.data_ptr(), out.data_ptr(), _ptr(grad_weight),
+          _ptr(grad_bias), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    return out, grad_weight, grad_bias
+
+
+def prepare_backward(grad_q, grad_k, grad_v, qkv, norm_wq, norm_wk, positions, *, heads: int, head_dim: int,
+                     rotary_dim: int, batch: int = 1, valid_len: int | None = None, n_axes: int | None = None,
+                     axis_dims=None, theta: float = 10000.0, eps: float = 1e-6, out=None, grad_wq=None, grad_wk=None,
+                     workspace=None, stream=None, layout: str = "head_major", valid_lens=None):
+    """The gradient of a 16-bit ``prepare`` call.  grad_q, grad_k, grad_v are
+    contiguous [batch, heads, S, head_dim] (or [batch, S, heads, head_dim]
+    with ``layout="token_major"``) of qkv's type; the other arguments are the
+    forward call's.  Returns (grad_qkv, grad_wq, grad_wk): grad_qkv
+    [tokens, 3*heads*head_dim] of qkv's type, zero in rows past the valid
+    prefix, and the float32 [head_dim] weight gradients
+    (h3qk_prepare_backward)."""
+    if qkv.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("qkv must be float16 or bfloat16")
+    if qkv.dim() != 2 or qkv.stride(1) != 1:
+        raise ValueError("qkv must be 2-D [tokens, row_stride] with unit inner stride")
+    tokens = qkv.shape[0]
+    if tokens % batch:
+        raise ValueError("tokens must be a multiple of batch")
+    seq = tokens // batch
+    if valid_len is None:
+        valid_len = seq
+    if n_axes is None:
+        n_axes = positions.shape[1] if positions is not None and positions.dim() == 2 else 3
+    dev = qkv.device
+    _need_common(qkv, norm_wq, norm_wk, positions, tokens=tokens, heads=heads, head_dim=head_dim,
+                 rotary_dim=rotary_dim, n_axes=n_axes, batch=batch, valid_lens=valid_lens, device=dev)
+    n = tokens * heads * head_dim
+    for t, name in ((grad_q, "grad_q"), (grad_k, "grad_k"), (grad_v, "grad_v")):
+        _need(t, name, device=dev, dtypes=(qkv.dtype,), numel=n)
+    if out is None:
+        out = torch.empty((tokens, 3 * heads * head_dim), dtype=qkv.dtype, device=dev)
+    else:
+        _need(out, "out", device=dev, dtypes=(qkv.dtype,), numel=3 * n)
+    if grad_wq is None:
+        grad_wq = torch.empty(head_dim, dtype=torch.float32, device=dev)
+    if grad_wk is None:
+        grad_wk = torch.empty(head_dim, dtype=torch.float32, device=dev)
+    for t, name in ((grad_wq, "grad_wq"), (grad_wk, "grad_wk")):
+        _need(t, name, device=dev, dtypes=(torch.float32,), numel=head_dim)
+    o = _opts_for(qkv, n_axes=n_axes, axis_dims=axis_dims, theta=theta, eps=eps, batch=batch)
+    o.out_layout = {"head_major": h3qk.HEAD_MAJOR, "token_major": h3qk.TOKEN_MAJOR}[layout]
+    o.valid_lens = _ptr(valid_lens)
+    workspace, ws_bytes = _workspace(workspace, _size("h3qk_prepare_backward_workspace_bytes", dev, head_dim), dev)
+    _call("h3qk_prepare_backward", dev, grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), qkv.data_ptr(),
+          norm_wq.data_ptr(), norm_wk.data_ptr(), _ptr(positions), tokens, heads, head_dim, rotary_dim, valid_len,
+          out.data_ptr(), grad_wq.data_ptr(), grad_wk.data_ptr(), workspace.data_ptr(), ws_bytes, ctypes.byref(o),
+          _stream(stream, dev))
+    return out, grad_wq, grad_wk

@@ -26,8 +26,10 @@ LIB_DEBUG = os.path.join(PKG, "libh3qk_debug.so")
 # The kernel instances of each input type sit in their own translation unit
 # so that the sources compile in parallel.
 SOURCES = [os.path.join(CSRC, f) for f in ("h3qk_api.cu", "h3qk_host.cu", "h3qk_launch_bf16.cu",
-                                           "h3qk_launch_fp16.cu", "h3qk_vae_ops.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("h3qk_kernels.cuh", "h3qk_launch.cuh", "h3qk_internal.h")] + \
+                                           "h3qk_launch_fp16.cu", "h3qk_vae_ops.cu", "h3qk_layer_norm.cu",
+                                           "h3qk_backward.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("h3qk_kernels.cuh", "h3qk_launch.cuh", "h3qk_internal.h",
+                                                      "h3qk_ops.cuh")] + \
     [os.path.join(INCLUDE, "h3qk.h")]
 
 COMPILE_FLAGS = [

@@ -24,8 +24,8 @@ _SCALE_NAMES = {"none": SCALE_NONE, "dynamic": SCALE_DYNAMIC, "static": SCALE_ST
 
 
 class H3QKError(RuntimeError):
-    def __init__(self, status: int, name: str, cuda_error: int = 0):
-        msg = f"h3qk_prepare failed: {name} (status {status})"
+    def __init__(self, status: int, name: str, cuda_error: int = 0, entry: str = "h3qk_prepare"):
+        msg = f"{entry} failed: {name} (status {status})"
         if status == ERR_CUDA:
             msg += f", cudaError {cuda_error}"
         super().__init__(msg)
