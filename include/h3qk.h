@@ -463,6 +463,82 @@ h3qk_status h3qk_prepare_backward(const void* grad_q, const void* grad_k, const 
                                   void* workspace, size_t workspace_bytes, const h3qk_opts* opts,
                                   h3qk_stream_t stream);
 
+/*
+ * h3qk_attention: attention on head rows as h3qk_prepare writes them.
+ * For query row i of an item (batch entry or document), head h, and key j:
+ *   z = scale q_i.k_j;  z = softcap tanh(z / softcap) when softcap > 0;
+ *   z -= slopes[h] |pos_i - j|;  p = exp(z - lse_i) over the keys i sees;
+ *   out_i = sum_j p v_j,  lse_i = ln sum_j exp(z).
+ * Scores, sums and outputs are binary32; p is rounded to the input type for
+ * its product with v; out is rounded once.  Rows that see no key, and rows
+ * past an item's q_lens, get out = 0 and lse = -infinity.
+ *
+ * What row i sees: keys j < kv_len of its item; with causal, of those only
+ * j <= pos_i or j < prefix.  pos_i = start + i, where start is q_starts of
+ * the item, else 0 when q_rows == kv_rows, else kv_len - q_len (the queries
+ * are the last rows of a cache).  With documents, rows and keys of document
+ * d are [doc_offsets[d], doc_offsets[d+1]), positions count from its first
+ * row, and rows past the last offset see nothing.
+ *
+ * Non-finite values in keys and values that no row of an item sees (unwritten
+ * cache rows, other documents) do not reach its results.
+ *
+ * Fill the struct from zeros: a zero scale means 1 / sqrt(head_dim).
+ */
+typedef struct h3qk_strides {
+    int64_t item, head, row;  /* elements; multiples of 8, positive where that
+                                 dimension is larger than 1, row >= head_dim;
+                                 channels are contiguous */
+} h3qk_strides;
+
+typedef struct h3qk_attn {
+    int32_t dtype;            /* H3QK_FP16 or H3QK_BF16, of every 16-bit tensor */
+    int32_t batch, heads;     /* 1 to 65535 each */
+    int32_t kv_heads;         /* divides heads: head h reads K/V head h / (heads / kv_heads) */
+    int32_t head_dim;         /* a multiple of 8 in [8, 128] */
+    int32_t causal;           /* 0 or 1 */
+    int32_t docs;             /* documents packed along the rows (then batch is 1 and
+                                 q_rows == kv_rows); 0: none */
+    int32_t reserved;         /* 0 */
+    float scale;              /* finite, >= 0 */
+    float softcap;            /* finite, >= 0; 0: none */
+    int64_t q_rows, kv_rows;  /* rows of the tensors, below 2^30 */
+    const void *q, *k, *v;    /* [batch, heads, q_rows, head_dim], [batch, kv_heads, kv_rows, head_dim] twice */
+    void* out;                /* as q (h3qk_attention_backward: read) */
+    float* lse;               /* [batch, heads, q_rows] contiguous (backward: read) */
+    const void* grad_out;     /* backward only: as q */
+    void *grad_q, *grad_k, *grad_v;  /* backward only: as q, k, v */
+    const float* slopes;      /* [heads] or NULL */
+    const int32_t* prefix_lens;  /* [docs or batch] or NULL; only with causal */
+    const int32_t* doc_offsets;  /* [docs + 1], ascending from 0, at most q_rows; with docs */
+    const int32_t* q_lens;    /* [batch] or NULL: rows that attend; not with docs */
+    const int32_t* kv_lens;   /* [batch] or NULL: keys that exist; not with docs */
+    const int32_t* q_starts;  /* [batch] or NULL: position of row 0; not with docs */
+    void* workspace;          /* device memory, 16-byte aligned, of the size the functions below give */
+    size_t workspace_bytes;
+    h3qk_strides q_strides, k_strides, v_strides, out_strides;
+    h3qk_strides grad_out_strides, grad_q_strides, grad_k_strides, grad_v_strides;
+} h3qk_attn;
+
+/*
+ * Values of the int32 arrays are read on the device and clamped to the
+ * tensors' sizes.  16-bit tensors start on 16-byte boundaries.  Outputs may
+ * overlap neither inputs nor one another (each tensor's whole span counts).
+ * A workspace may be NULL where its size is 0; calls that may overlap need
+ * their own.  Errors and asynchrony as for h3qk_prepare.
+ *
+ * The tile kernels' waits are bounded: should one ever run out (it cannot in
+ * a working program), the kernel ends, the rows concerned have lse = NaN and
+ * h3qk_attention_stuck() counts the blocks.
+ */
+size_t h3qk_attention_workspace_bytes(const h3qk_attn* call);
+h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t stream);
+
+/* Blocks of attention kernels on the current device that gave up waiting
+ * since the library was loaded (synchronous: waits for the device); -1 when
+ * the count cannot be read. */
+int64_t h3qk_attention_stuck(void);
+
 /* A static, human-readable name of a status. */
 const char* h3qk_status_string(h3qk_status status);
 

@@ -75,3 +75,89 @@ def norm_rope(x, w, ang, eps, rotary):
 def head_major(x, batch):
     """[tokens, heads, D] -> [batch, heads, S, D]."""
     return x.reshape(batch, -1, *x.shape[1:]).transpose(1, 2)
+
+
+def visible(sq, sk, batch, causal=False, prefix_lens=None, doc_offsets=None, q_lens=None, kv_lens=None, q_starts=None,
+            device="cuda"):
+    """(who sees what [batch, sq, sk], |position - key| [batch, sq, sk]) from the definition, by plain loops."""
+    vis = torch.zeros(batch, sq, sk, dtype=torch.bool)
+    dist = torch.zeros(batch, sq, sk, dtype=torch.float64)
+    runs = []
+    if doc_offsets is not None:
+        off = [int(x) for x in doc_offsets]
+        for d in range(len(off) - 1):
+            runs.append((0, off[d], off[d], off[d + 1] - off[d], off[d + 1] - off[d], 0,
+                         int(prefix_lens[d]) if prefix_lens is not None else 0))
+    else:
+        for b in range(batch):
+            n = sq if q_lens is None else min(max(int(q_lens[b]), 0), sq)
+            keys = sk if kv_lens is None else min(max(int(kv_lens[b]), 0), sk)
+            start = int(q_starts[b]) if q_starts is not None else (0 if sq == sk else keys - n)
+            runs.append((b, 0, 0, n, keys, start, int(prefix_lens[b]) if prefix_lens is not None else 0))
+    for b, r0, k0, n, keys, start, prefix in runs:
+        i = torch.arange(n)[:, None] + start
+        j = torch.arange(keys)[None, :]
+        see = torch.ones(n, keys, dtype=torch.bool)
+        if causal:
+            see = (j <= i) | (j < prefix)
+        vis[b, r0:r0 + n, k0:k0 + keys] = see
+        dist[b, r0:r0 + n, k0:k0 + keys] = (i - j).abs().double()
+    return vis.to(device), dist.to(device)
+
+
+def attention(q, k, v, vis, dist, dout=None, scale=None, softcap=0.0, slopes=None):
+    """Attention in binary64: {"out", "lse", and with dout "dq", "dk", "dv"} and under "..._bound" how far the
+    kernels' results may be from each.
+
+    u is the type's unit roundoff.  A score is off by at most eps: the binary32 sum over D products, the hardware's
+    2^x and the tanh built on it, together below 2^-20 (8 + scale sum|q||k| + softcap).  P (and dS) are rounded to
+    the type before their products, so each term of a product's sum is off by 2 (u + eps) of itself; delta takes the
+    rounded output; each result is rounded once."""
+    group = q.shape[1] // k.shape[1]
+    u, tiny = U[q.dtype], TINY[q.dtype]
+    scale = q.shape[3] ** -0.5 if scale is None else scale
+    q, k, v = q.double(), k.double(), v.double()
+    seen = vis.any(1)[:, None, :, None]  # values that nobody sees may be anything
+    k, v = torch.where(seen, k, 0.0), torch.where(seen, v, 0.0)
+    rows = vis.any(2)[:, None, :, None]
+    q = torch.where(rows, q, 0.0)
+    kk, vv = k.repeat_interleave(group, 1), v.repeat_interleave(group, 1)
+    mask = vis[:, None]
+    z = scale * (q @ kk.transpose(2, 3))
+    terms = scale * (q.abs() @ kk.abs().transpose(2, 3))
+    t = torch.tanh(z / softcap) if softcap else None
+    s = softcap * t if softcap else z
+    if slopes is not None:
+        s = s - slopes.double().view(1, -1, 1, 1) * dist[:, None]
+        terms = terms + slopes.double().abs().view(1, -1, 1, 1) * dist[:, None]
+    s = s.masked_fill(~mask, -math.inf)
+    lse = torch.logsumexp(s, 3)
+    p = torch.where(mask, torch.exp(s - torch.where(lse.isinf(), 0.0, lse)[..., None]), 0.0)
+    eps = 2.0 ** -20 * (8 + softcap + torch.where(mask, terms, 0.0).amax(3, keepdim=True))
+    out = p @ vv
+    got = {"out": out, "lse": lse}
+    got["out_bound"] = u * out.abs() + tiny + 2 * (u + eps) * (p @ vv.abs()) + 1e-12
+    got["lse_bound"] = torch.where(lse.isinf(), 0.0, 2 * eps[..., 0] + 2.0 ** -22 * lse.abs())
+    if dout is None:
+        return got
+    do = torch.where(rows, dout.double(), 0.0)
+    dp = do @ vv.transpose(2, 3)
+    dp_terms = do.abs() @ vv.abs().transpose(2, 3)
+    delta = (do * out).sum(3, keepdim=True)
+    bend = (1 - t * t) if softcap else 1.0
+    ds = p * (dp - delta) * bend
+    o_terms = (do.abs() * (u * out.abs() + got["out_bound"])).sum(3, keepdim=True)
+    ds_off = 2 * (u + eps) * ds.abs() + p * (2.0 ** -18 * (dp_terms + delta.abs()) + 2 * o_terms) + \
+        (p * (dp - delta).abs() * 2.0 ** -18 if softcap else 0.0)
+    # fp16's smallest numbers: dS below 2^-14 is held to an absolute 2^-25, P (kept 2^10 larger) to 2^-35
+    if tiny > 1e-10:
+        ds_off = ds_off + torch.where(mask, tiny, 0.0)
+    fold = lambda x: x.view(x.shape[0], -1, group, *x.shape[2:]).sum(2)  # noqa: E731
+    got["dq"] = scale * (ds @ kk)
+    got["dk"] = scale * fold(ds.transpose(2, 3) @ q)
+    got["dv"] = fold(p.transpose(2, 3) @ do)
+    got["dq_bound"] = u * got["dq"].abs() + tiny + scale * (ds_off @ kk.abs()) + 1e-12
+    got["dk_bound"] = u * got["dk"].abs() + tiny + scale * fold(ds_off.transpose(2, 3) @ q.abs()) + 1e-12
+    p_off = 2 * (u + eps) * p + (torch.where(mask, 2.0 ** -34, 0.0) if tiny > 1e-10 else 0.0)
+    got["dv_bound"] = u * got["dv"].abs() + tiny + fold(p_off.transpose(2, 3) @ do.abs()) + 1e-12
+    return got

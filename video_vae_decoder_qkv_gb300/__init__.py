@@ -18,9 +18,10 @@ from .h3qk import (H3QKError, amax, cast, norm_rope_tensor, prepare,  # noqa: F4
                    prepare_dynamic_sharded, prepare_host, prepare_sage, scaled_residual, silu_and_mul)
 
 __all__ = ["prepare", "prepare_host", "prepare_sage", "norm_rope_tensor", "amax", "cast", "prepare_dynamic_sharded",
-           "silu_and_mul", "scaled_residual", "layer_norm", "layer_norm_backward", "prepare_backward", "H3QKError"]
+           "silu_and_mul", "scaled_residual", "layer_norm", "layer_norm_backward", "prepare_backward", "attention",
+           "H3QKError"]
 
-_BLOCK = ("layer_norm", "layer_norm_backward", "prepare_backward")
+_BLOCK = ("layer_norm", "layer_norm_backward", "prepare_backward", "attention")
 
 
 def __getattr__(name):

@@ -1,5 +1,5 @@
 """Python binding of the attention block's operators: layer norm and its
-gradient, and the gradient of the fused QK preparation.
+gradient, the gradient of the fused QK preparation, and attention.
 
 As in ``h3qk``, this only checks tensors and passes their addresses: each
 operator runs in the library's CUDA kernels on the caller's stream, and
@@ -8,6 +8,7 @@ workspaces come from torch's allocator unless the caller passes one.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -23,6 +24,9 @@ _SIGNATURES = {
     "h3qk_layer_norm": (_INT, [_P, _INT, _I64, _I32, _I64, _P, _P, _I64, _F, _P, _P, _P]),
     "h3qk_layer_norm_backward_workspace_bytes": (_SZ, [_I64, _I32, _I64]),
     "h3qk_layer_norm_backward": (_INT, [_P, _I64, _P, _INT, _I64, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "h3qk_attention_workspace_bytes": (_SZ, [ctypes.c_char_p]),
+    "h3qk_attention": (_INT, [ctypes.c_char_p, _P]),
+    "h3qk_attention_stuck": (_I64, []),
     "h3qk_prepare_backward_workspace_bytes": (_SZ, [_I32]),
     "h3qk_prepare_backward": (_INT, [_P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _SZ,
                                      ctypes.POINTER(h3qk.Opts), _P]),
@@ -216,3 +220,118 @@ def prepare_backward(grad_q, grad_k, grad_v, qkv, norm_wq, norm_wk, positions, *
           out.data_ptr(), grad_wq.data_ptr(), grad_wk.data_ptr(), workspace.data_ptr(), ws_bytes, ctypes.byref(o),
           _stream(stream, dev))
     return out, grad_wq, grad_wk
+
+
+# h3qk_attn (include/h3qk.h), packed in one step
+_ATTN = struct.Struct("@8i2f2q16PN24q")
+_NO_STRIDES = (0, 0, 0)
+
+
+def _need_heads(t, name, shape, dtype, dev):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    st = t.stride()
+    if st[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{name} must have unit stride along head_dim")
+    return st[:3]
+
+
+def _need_lens(t, name, n, dev):
+    if t is None:
+        return 0
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n}, got shape {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return t.data_ptr()
+
+
+def _attn_common(q, k, v, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts):
+    """Checks shared by both directions: (batch, heads, kv_heads, q_rows, kv_rows, dim, docs, strides, pointers)."""
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("q must be float16 or bfloat16")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be [batch, heads, rows, head_dim]")
+    dev = q.device
+    batch, heads, sq, dim = q.shape
+    _, kv_heads, sk, _ = k.shape
+    if kv_heads == 0 or heads % kv_heads:
+        raise ValueError(f"{heads} heads cannot share {kv_heads} K/V heads")
+    strides = (_need_heads(q, "q", (batch, heads, sq, dim), q.dtype, dev),
+               _need_heads(k, "k", (batch, kv_heads, sk, dim), q.dtype, dev),
+               _need_heads(v, "v", (batch, kv_heads, sk, dim), q.dtype, dev))
+    docs = 0
+    if doc_offsets is not None:
+        docs = doc_offsets.shape[0] - 1 if doc_offsets.dim() == 1 else 0
+        if docs < 1:
+            raise ValueError("doc_offsets must be a vector of at least two offsets")
+        if batch != 1 or sq != sk:
+            raise ValueError("documents are packed along the rows of one item, the same for queries and keys")
+        if q_lens is not None or kv_lens is not None or q_starts is not None:
+            raise ValueError("doc_offsets excludes q_lens, kv_lens and q_starts")
+    slope_ptr = 0
+    if slopes is not None:
+        _need(slopes, "slopes", device=dev, dtypes=(torch.float32,), numel=heads)
+        slope_ptr = slopes.data_ptr()
+    lists = (slope_ptr, _need_lens(prefix_lens, "prefix_lens", docs or batch, dev),
+             _need_lens(doc_offsets, "doc_offsets", docs + 1, dev), _need_lens(q_lens, "q_lens", batch, dev),
+             _need_lens(kv_lens, "kv_lens", batch, dev), _need_lens(q_starts, "q_starts", batch, dev))
+    return batch, heads, kv_heads, sq, sk, dim, docs, strides, lists
+
+
+def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slopes=None, causal: bool = False,
+              prefix_lens=None, doc_offsets=None, q_lens=None, kv_lens=None, q_starts=None, out=None, lse=None,
+              workspace=None, stream=None):
+    """Attention on head rows as ``prepare`` writes them.
+
+    q: float16/bfloat16 [batch, heads, Sq, D]; k, v: [batch, kv_heads, Sk, D]
+    of the same type, kv_heads dividing heads (head h reads K/V head
+    h // (heads // kv_heads)), D a multiple of 8 up to 128.  Any batch, head
+    and row strides that are multiples of 8 elements will do, so a token-major
+    tensor is passed as its ``transpose(1, 2)`` and a cache as a slice.
+
+    Scores are scale * q.k (default 1 / sqrt(D)), bent to softcap * tanh(z /
+    softcap) when ``softcap`` is positive, less ``slopes[h]`` (float32
+    [heads]) times the distance of query and key.  A row sees the keys below
+    its item's ``kv_lens`` (int32 [batch]); with ``causal`` of those only the
+    ones up to its own position, and the first ``prefix_lens`` of them (int32
+    [batch], or one per document).  ``q_lens`` limits the rows that attend;
+    ``q_starts`` is row 0's position among the keys (default: 0 when Sq == Sk,
+    else kv_len - q_len).  ``doc_offsets`` (int32 [n + 1], from 0) packs n
+    documents along the rows of one item: each attends within itself.
+
+    Returns (out, lse): out like q, lse float32 [batch, heads, Sq], the
+    natural logarithm of each row's sum of exponentials.  Rows that see
+    nothing have out = 0 and lse = -inf.  A call with few rows per K/V head
+    (tokens produced one by one) splits the keys over the GPU and joins the
+    parts (h3qk_attention)."""
+    batch, heads, kv_heads, sq, sk, dim, docs, strides, lists = _attn_common(
+        q, k, v, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
+    dev = q.device
+    if out is None:
+        out = torch.empty_like(q)
+    out_strides = _need_heads(out, "out", (batch, heads, sq, dim), q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((batch, heads, sq), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", device=dev, dtypes=(torch.float32,), numel=batch * heads * sq)
+
+    def args(ws, ws_bytes):
+        return _ATTN.pack(_DTYPES[q.dtype], batch, heads, kv_heads, dim, 1 if causal else 0, docs, 0, scale or 0.0,
+                          softcap, sq, sk, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                          0, 0, 0, 0, *lists, ws, ws_bytes, *strides[0], *strides[1], *strides[2], *out_strides,
+                          *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES)
+
+    packed = args(0, 0)
+    need = _size("h3qk_attention_workspace_bytes", dev, packed)
+    if need:
+        workspace, ws_bytes = _workspace(workspace, need, dev)
+        packed = args(workspace.data_ptr(), ws_bytes)
+    _call("h3qk_attention", dev, packed, _stream(stream, dev))
+    return out, lse

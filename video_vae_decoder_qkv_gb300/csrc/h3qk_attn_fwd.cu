@@ -1,0 +1,400 @@
+// Attention forward, many rows: one block takes 256 query rows of a head and
+// streams its keys and values once.
+//
+//   s = bend(q k^T),  m = running row maximum,  p = 2^(s - m),
+//   o = sum p v / sum p,  lse = ln(sum e^s)
+//
+// Two groups of four warps own 128 rows each, one thread a row, so the
+// softmax needs no exchange between threads.  One thread issues the matrix
+// products, one warp the tile loads.  The products of one group run while
+// the other group computes its softmax:
+//   tensor unit   S0 S1 | O0 S0' O1 S1' | ...      (S = q k^T, O += p v)
+// P replaces S in TMEM (as 16-bit pairs) and is the product's A operand from
+// there; the tensor unit works in order, so S' may be issued behind the O
+// that reads P from the same columns.  O stays in TMEM; it is rescaled only
+// when some row's maximum has grown by more than 2^8, otherwise the old
+// maximum serves on (p then reaches 2^8, far from any overflow; for fp16 all
+// p are kept 2^7 larger, so that flat rows do not fall into subnormals).
+//
+// P is rounded to the input type: that is what the tensor unit multiplies.
+// The row sum adds the unrounded p in binary32, O accumulates in binary32.
+//
+// Bound: at head_dim 128 by the tensor unit (2 x 512 cycles a tile and
+// group against about 900 of softmax, which overlaps); at 64 by the
+// exponentials and the arithmetic around them.
+#include "h3qk_attn.cuh"
+
+namespace {
+
+using namespace h3qk_tc;
+using h3qk_core::Bend;
+using h3qk_core::Params;
+using h3qk_core::Stretch;
+
+constexpr int kTile = 128;             // rows of a group, keys of a tile
+constexpr int kThreads = 384;          // 2 x 4 softmax warps; products, loads, two idle
+// Registers a thread, from the 168 of the launch: 8 x 216 + 4 x 72 = 12 x 168.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr float kSlack = 8.0f;         // log2: growth of the maximum that is tolerated
+constexpr int kBlockBytes = 128 * 128; // 64 columns of a tile
+
+template <int DP>
+struct FwdShape {
+    static constexpr int kBlocks = DP / 64;
+    static constexpr int kTileBytes = kBlocks * kBlockBytes;
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+};
+
+struct FwdShared {
+    uint64_t full[8], empty[8];
+    uint64_t q_full, fixed;
+    uint64_t s_full[2], p_ready[2], o_done[2], drain;
+    uint32_t tmem;
+    int stop;
+};
+
+template <bool BF16, int DP, bool BENT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p)
+{
+    using Shape = FwdShape<DP>;
+    constexpr int kStages = Shape::kStages;
+    constexpr float kShift = BF16 ? 0.0f : 7.0f;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ FwdShared sh;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t q_smem = base, ring = base + 2 * Shape::kTileBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = blockIdx.y;
+    const int kv_head = head / p.group;
+
+    Stretch s;
+    // Causal rows see more keys the later they are: the longest tiles go first.
+    const int block = p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    if (!h3qk_core::find_stretch(s, p, block, blockIdx.z, 2 * kTile, false)) return;
+    const int tile_row = s.tile * 2 * kTile;
+    int n[2], seen = 0;  // tiles of each group, keys that any row of the block sees
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int first = tile_row + g * kTile;
+        const int last = min(first + kTile, s.rows) - 1;
+        const int lim = last < first ? 0 : max(h3qk_core::limit_of(s, p.causal, last), 0);
+        n[g] = (lim + kTile - 1) / kTile;
+        seen = max(seen, lim);
+    }
+    const int n_all = max(n[0], n[1]);
+    // Rows of the last tile that no row of the block sees: unwritten cache
+    // rows, another document's, later tokens.  They are cleared (0 * NaN is
+    // NaN, even with p = 0); past the tensor's end the loads give zeros.
+    const bool fix = n_all * kTile > seen && s.k0 + seen < p.kv_rows;
+
+    const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
+    const uint32_t s_full = smem_addr(sh.s_full), p_ready = smem_addr(sh.p_ready), o_done = smem_addr(sh.o_done);
+    const uint32_t q_full = smem_addr(&sh.q_full), fixed = smem_addr(&sh.fixed);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(full + 8 * i, 1);
+            bar_init(empty + 8 * i, 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            bar_init(s_full + 8 * g, 1);
+            bar_init(p_ready + 8 * g, 4);
+            bar_init(o_done + 8 * g, 1);
+        }
+        bar_init(q_full, 1);
+        bar_init(fixed, 1);
+        bar_init(smem_addr(&sh.drain), 1);
+        sh.stop = 0;
+        bar_init_done();
+    }
+    if (warp == 8) tmem_alloc(smem_addr(&sh.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile int* stop = &sh.stop;
+
+    if (warp > 9) {
+        regs_down<kOtherRegs>();
+    } else if (warp == 9) {
+        regs_down<kOtherRegs>();
+        // ---- tile loads: Q, then K and V tiles in turn ----------------------
+        int issued = 0;
+        bool ok = true;
+        if (lane == 0 && n_all > 0) {
+            tma_prefetch(&map_k);
+            tma_prefetch(&map_v);
+            bar_expect(q_full, 2 * Shape::kTileBytes);
+            for (int g = 0; g < 2; ++g)
+                for (int b = 0; b < Shape::kBlocks; ++b)
+                    tma_load(q_smem + g * Shape::kTileBytes + b * kBlockBytes, &map_q, 64 * b,
+                             s.row0 + tile_row + g * kTile, head, s.item, q_full);
+            for (int i = 0; i < 2 * n_all && ok; ++i) {
+                const int st = i % kStages;
+                ok = bar_wait(empty + 8 * st, ((i / kStages) & 1) ^ 1, stop);
+                if (!ok) break;
+                bar_expect(full + 8 * st, Shape::kTileBytes);
+                const int row = s.k0 + (i >> 1) * kTile;
+                for (int b = 0; b < Shape::kBlocks; ++b)
+                    tma_load(ring + st * Shape::kTileBytes + b * kBlockBytes, (i & 1) ? &map_v : &map_k, 64 * b, row,
+                             kv_head, s.item, full + 8 * st);
+                issued = i + 1;
+            }
+        }
+        __syncwarp();
+        if (fix) {
+            const int i = 2 * n_all - 1, st = i % kStages;
+            if (bar_wait(full + 8 * st, (i / kStages) & 1, stop)) {
+                const int first = seen - (n_all - 1) * kTile;  // rows to keep
+                for (int b = 0; b < Shape::kBlocks; ++b)
+                    for (int o = first * 128 + lane * 16; o < kBlockBytes; o += 512)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         ring + st * Shape::kTileBytes + b * kBlockBytes + o),
+                                     "r"(0)
+                                     : "memory");
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(fixed);
+            }
+        }
+        __syncwarp();
+        if (*stop && lane == 0) {
+            // Given up: this block's loads must land before it leaves.
+            if (n_all > 0)
+                for (int t = 0; t < kMaxTries && !bar_test(q_full, 0); ++t) {}
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                for (int t = 0; t < kMaxTries && !bar_test(full + 8 * (i % kStages), (i / kStages) & 1); ++t) {}
+        }
+    } else if (warp == 8) {
+        regs_down<kOtherRegs>();
+        // ---- matrix products ------------------------------------------------
+        if (lane == 0 && n_all > 0) {
+            constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
+            constexpr uint32_t shape_o = mma_shape(BF16, 128, DP, true);
+            const int steps = (p.dim + 15) / 16;
+            auto scores = [&](int g, uint32_t k_tile) {
+                const uint64_t a = tile_desc(q_smem + g * Shape::kTileBytes, 16), b = tile_desc(k_tile, 16);
+                for (int i = 0; i < steps; ++i) {
+                    const uint32_t off = ((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4;
+                    mma_ss(tmem + g * 128, a + off, b + off, shape_s, i > 0);
+                }
+                mma_commit(s_full + 8 * g);
+            };
+            auto values = [&](int g, uint32_t v_tile, bool add) {
+                const uint64_t b = tile_desc(v_tile, kBlockBytes);
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i)
+                    mma_ts(tmem + 256 + g * DP, tmem + g * 128 + 8 * i, b + (i * 2048 >> 4), shape_o, add || i > 0);
+                mma_commit(o_done + 8 * g);
+            };
+            auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
+            auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
+            bool ok = bar_wait(q_full, 0, stop) && loaded(0);
+            if (ok) {
+                for (int g = 0; g < 2; ++g)
+                    if (n[g] > 0) scores(g, tile_at(0));
+                mma_commit(empty);
+            }
+            for (int j = 0; j < n_all && ok; ++j) {
+                const bool more = j + 1 < n_all;
+                ok = loaded(2 * j + 1) && (!more || loaded(2 * j + 2));
+                if (ok && fix && !more) ok = bar_wait(fixed, 0, stop);
+                for (int g = 0; g < 2 && ok; ++g) {
+                    if (j < n[g]) {
+                        ok = bar_wait(p_ready + 8 * g, j & 1, stop);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(g, tile_at(2 * j + 1), j > 0);
+                    }
+                    if (j + 1 < n[g]) scores(g, tile_at(2 * j + 2));
+                }
+                if (!ok) break;
+                mma_commit(empty + 8 * ((2 * j + 1) % kStages));
+                if (more) mma_commit(empty + 8 * ((2 * j + 2) % kStages));
+            }
+            if (*stop) {
+                const uint32_t drain = smem_addr(&sh.drain);
+                mma_commit(drain);
+                for (int t = 0; t < kMaxTries && !bar_test(drain, 0); ++t) {}
+            }
+        }
+        __syncwarp();
+    } else {
+        regs_up<kSoftmaxRegs>();
+        // ---- softmax: one thread a row --------------------------------------
+        const int g = warp >> 2;
+        const int r = threadIdx.x & 127;
+        const int i_row = tile_row + g * kTile + r;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_cols = tmem + g * 128 + lanes, o_cols = tmem + 256 + g * DP + lanes;
+        const int lim = h3qk_core::limit_of(s, p.causal, i_row);
+        const int lim_first = h3qk_core::limit_of(s, p.causal, tile_row + g * kTile);
+        const Bend bend = h3qk_core::bend_of(p, head);
+        // Scores to powers of two: the bend gives exponents itself.
+        const float c = BENT ? 1.0f : p.scale * h3qk_core::kLog2e;
+        const uint64_t cc = pair(c, c);
+        float m = -INFINITY;
+        uint64_t sum2 = pair(0.0f, 0.0f);
+        bool ok = true;
+        for (int j = 0; j < n[g] && ok; ++j) {
+            ok = bar_wait(s_full + 8 * g, j & 1, stop);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t sr[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32(sr[b], s_cols + 32 * b);
+            tmem_wait_ld();
+            if constexpr (BENT) {
+                float far = static_cast<float>(s.start + i_row - j * kTile);
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float v = __uint_as_float(sr[b][e]) * bend.in;
+                        if (bend.capped) v = bend.cap * h3qk_core::tanh_half(v);
+                        v = fmaf(-bend.slope, fabsf(far - static_cast<float>(32 * b + e)), v);
+                        sr[b][e] = __float_as_uint(v);
+                    }
+            }
+            if ((j + 1) * kTile > lim_first) {
+                const int left = lim - j * kTile;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * b + e >= left) sr[b][e] = 0xff800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                mx[b] = __uint_as_float(sr[b][0]);
+#pragma unroll
+                for (int e = 1; e < 32; ++e) mx[b] = fmaxf(mx[b], __uint_as_float(sr[b][e]));
+            }
+            const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            if (__any_sync(0xffffffffu, (top - m) * c > kSlack)) {
+                if (j > 0) {
+                    const float f = top == -INFINITY ? 1.0f : exp2_fast((m - top) * c);
+                    const uint64_t ff = pair(f, f);
+                    sum2 = mul_pair(sum2, ff);
+                    ok = bar_wait(o_done + 8 * g, (j - 1) & 1, stop);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int d = 0; d < DP; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o, o_cols + d);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(o_cols + d, o);
+                    }
+                }
+                m = top;
+            }
+            const float mc = (m == -INFINITY ? 0.0f : m * c) - kShift;
+            const uint64_t nm = pair(-mc, -mc);
+            uint64_t part[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t pr[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float lo, hi;
+                    unpair(lo, hi, fma_pair(pair(__uint_as_float(sr[b][2 * e]), __uint_as_float(sr[b][2 * e + 1])), cc, nm));
+                    lo = exp2_fast(lo);
+                    hi = exp2_fast(hi);
+                    part[e & 1] = add_pair(part[e & 1], pair(lo, hi));
+                    pr[e] = round_pair<BF16>(lo, hi);
+                }
+                tmem_st16(s_cols + 16 * b, pr);
+            }
+            sum2 = add_pair(sum2, add_pair(part[0], part[1]));
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(p_ready + 8 * g);
+        }
+        if (ok && n[g] > 0) ok = bar_wait(o_done + 8 * g, (n[g] - 1) & 1, stop);
+        tc_fence_after();
+        float lo, hi;
+        unpair(lo, hi, sum2);
+        const float sum = lo + hi;
+        const bool live = ok && i_row < s.rows && n[g] > 0 && sum > 0.0f;
+        const bool write = i_row < s.span;
+        const int64_t row = s.row0 + i_row;
+        if (write)
+            p.lse[(static_cast<int64_t>(s.item) * p.heads + head) * p.q_rows + row] =
+                !ok ? __int_as_float(0x7fc00000)
+                    : (i_row < s.rows && n[g] > 0 && !(sum == 0.0f))
+                          ? ((m == -INFINITY ? 0.0f : m * c) - kShift + log2f(sum)) * h3qk_core::kLn2
+                          : -INFINITY;
+        const bool nan_row = ok && i_row < s.rows && n[g] > 0 && sum != sum;
+        const float inv = nan_row ? sum : live ? 1.0f / sum : 0.0f;
+        uint16_t* out = p.out + s.item * p.os.item + head * p.os.head + row * p.os.row;
+#pragma unroll
+        for (int d = 0; d < DP; d += 32) {
+            uint32_t o[32];
+            if (n[g] > 0) {
+                tmem_ld32(o, o_cols + d);
+                tmem_wait_ld();
+            }
+            if (write) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (d + 8 * q < p.dim) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = live || nan_row ? round_pair<BF16>(__uint_as_float(o[8 * q + 2 * e]) * inv,
+                                                                      __uint_as_float(o[8 * q + 2 * e + 1]) * inv)
+                                                   : 0u;
+                        *reinterpret_cast<uint4*>(out + d + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *stop) atomicAdd(p.stuck, 1u);
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+template <bool BF16, int DP, bool BENT>
+cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
+{
+    constexpr int smem = FwdShape<DP>::kSmem;
+    auto* kernel = attention_kernel<BF16, DP, BENT>;
+    static bool raised[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    if (!raised[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        raised[dev] = true;
+    }
+    const dim3 grid(static_cast<unsigned>(h3qk_core::tiles_of(p, p.q_rows, 2 * kTile)), p.heads, p.batch);
+    kernel<<<grid, kThreads, smem, st>>>(m.q, m.k, m.v, p);
+    h3qk_internal_count_launch();
+    return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t by_shape(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
+{
+    const bool bent = p.cap > 0.0f || p.slopes;
+    if (p.dim <= 64) return bent ? launch<BF16, 64, true>(p, m, st) : launch<BF16, 64, false>(p, m, st);
+    return bent ? launch<BF16, 128, true>(p, m, st) : launch<BF16, 128, false>(p, m, st);
+}
+
+}  // namespace
+
+cudaError_t h3qk_core::forward_tiles(bool bf16, const Params& p, const Maps& m, cudaStream_t st)
+{
+    return bf16 ? by_shape<true>(p, m, st) : by_shape<false>(p, m, st);
+}
