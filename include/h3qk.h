@@ -534,6 +534,22 @@ typedef struct h3qk_attn {
 size_t h3qk_attention_workspace_bytes(const h3qk_attn* call);
 h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t stream);
 
+/*
+ * h3qk_attention_backward: from grad_out and the forward call's q, k, v, out
+ * and lse (and its masks, scale, softcap and slopes) to grad_q, grad_k and
+ * grad_v:
+ *   delta = sum_d grad_out out,  ds = p (grad_out.v - delta) (1 - (z/softcap)^2),
+ *   grad_v = sum_i p grad_out,  grad_q = scale sum_j ds k,  grad_k = scale sum_i ds q,
+ * grad_k and grad_v summed over the heads that share them.  p and ds are
+ * rounded to the input type for their products, sums are binary32, results
+ * are rounded once.  Rows that attend to nothing get grad_q = 0, keys that no
+ * row sees grad_k = grad_v = 0.  In fp16, ds below 2^-14 loses digits as any
+ * fp16 value does: scale the loss where gradients are that small.  The
+ * slopes get no gradient.  The workspace holds one float per query row.
+ */
+size_t h3qk_attention_backward_workspace_bytes(const h3qk_attn* call);
+h3qk_status h3qk_attention_backward(const h3qk_attn* call, h3qk_stream_t stream);
+
 /* Blocks of attention kernels on the current device that gave up waiting
  * since the library was loaded (synchronous: waits for the device); -1 when
  * the count cannot be read. */

@@ -19,9 +19,9 @@ from .h3qk import (H3QKError, amax, cast, norm_rope_tensor, prepare,  # noqa: F4
 
 __all__ = ["prepare", "prepare_host", "prepare_sage", "norm_rope_tensor", "amax", "cast", "prepare_dynamic_sharded",
            "silu_and_mul", "scaled_residual", "layer_norm", "layer_norm_backward", "prepare_backward", "attention",
-           "H3QKError"]
+           "attention_backward", "H3QKError"]
 
-_BLOCK = ("layer_norm", "layer_norm_backward", "prepare_backward", "attention")
+_BLOCK = ("layer_norm", "layer_norm_backward", "prepare_backward", "attention", "attention_backward")
 
 
 def __getattr__(name):

@@ -26,6 +26,8 @@ _SIGNATURES = {
     "h3qk_layer_norm_backward": (_INT, [_P, _I64, _P, _INT, _I64, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
     "h3qk_attention_workspace_bytes": (_SZ, [ctypes.c_char_p]),
     "h3qk_attention": (_INT, [ctypes.c_char_p, _P]),
+    "h3qk_attention_backward_workspace_bytes": (_SZ, [ctypes.c_char_p]),
+    "h3qk_attention_backward": (_INT, [ctypes.c_char_p, _P]),
     "h3qk_attention_stuck": (_I64, []),
     "h3qk_prepare_backward_workspace_bytes": (_SZ, [_I32]),
     "h3qk_prepare_backward": (_INT, [_P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _SZ,
@@ -335,3 +337,36 @@ def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slop
         packed = args(workspace.data_ptr(), ws_bytes)
     _call("h3qk_attention", dev, packed, _stream(stream, dev))
     return out, lse
+
+
+def attention_backward(grad_out, q, k, v, out, lse, *, scale: float | None = None, softcap: float = 0.0, slopes=None,
+                       causal: bool = False, prefix_lens=None, doc_offsets=None, q_lens=None, kv_lens=None,
+                       q_starts=None, grad_q=None, grad_k=None, grad_v=None, workspace=None, stream=None):
+    """The gradient of ``attention``: grad_out like out, the forward's q, k, v
+    and keyword arguments, out and lse as it returned them.  Returns (grad_q,
+    grad_k, grad_v) like q, k and v; heads that share a K/V head add to one
+    gradient, and rows and keys that take no part get zeros.  The same call
+    gives the same bits every time.  The slopes get no gradient
+    (h3qk_attention_backward)."""
+    batch, heads, kv_heads, sq, sk, dim, docs, strides, lists = _attn_common(
+        q, k, v, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
+    dev = q.device
+    row, key = (batch, heads, sq, dim), (batch, kv_heads, sk, dim)
+    out_strides = _need_heads(out, "out", row, q.dtype, dev)
+    do_strides = _need_heads(grad_out, "grad_out", row, q.dtype, dev)
+    _need(lse, "lse", device=dev, dtypes=(torch.float32,), numel=batch * heads * sq)
+    grad_q = torch.empty_like(q) if grad_q is None else grad_q
+    grad_k = torch.empty_like(k) if grad_k is None else grad_k
+    grad_v = torch.empty_like(v) if grad_v is None else grad_v
+    dq_strides = _need_heads(grad_q, "grad_q", row, q.dtype, dev)
+    dk_strides = _need_heads(grad_k, "grad_k", key, q.dtype, dev)
+    dv_strides = _need_heads(grad_v, "grad_v", key, q.dtype, dev)
+    # one binary32 word a row, as h3qk_attention_backward_workspace_bytes says
+    workspace, ws_bytes = _workspace(workspace, (batch * heads * sq * 4 + 15) // 16 * 16, dev)
+    packed = _ATTN.pack(_DTYPES[q.dtype], batch, heads, kv_heads, dim, 1 if causal else 0, docs, 0, scale or 0.0, softcap,
+                        sq, sk, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                        grad_out.data_ptr(), grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), *lists,
+                        workspace.data_ptr(), ws_bytes, *strides[0], *strides[1], *strides[2], *out_strides, *do_strides,
+                        *dq_strides, *dk_strides, *dv_strides)
+    _call("h3qk_attention_backward", dev, packed, _stream(stream, dev))
+    return grad_q, grad_k, grad_v

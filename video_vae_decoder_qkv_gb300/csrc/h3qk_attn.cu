@@ -26,7 +26,6 @@ struct Tensor {
     const void* data;
     h3qk_strides s;
     int64_t heads, rows;
-    bool input;
 };
 
 // A tensor's strides, with those of single-entry dimensions replaced by ones
@@ -176,6 +175,13 @@ unsigned int* stuck_addr()
     return addr[dev];
 }
 
+// The runtime could not give the stuck counter or a tensor map.
+h3qk_status no_maps()
+{
+    const cudaError_t e = cudaGetLastError();
+    return h3qk_internal_fail_cuda(e != cudaSuccess ? e : cudaErrorInvalidValue);
+}
+
 void fill(Params& p, const h3qk_attn& a)
 {
     p.batch = a.batch;
@@ -217,10 +223,10 @@ extern "C" h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t strea
     const h3qk_attn& a = *call;
     h3qk_status s = check_sizes(a);
     if (s != H3QK_OK) return s;
-    Tensor t[4] = {{a.q, a.q_strides, a.heads, a.q_rows, true},
-                   {a.k, a.k_strides, a.kv_heads, a.kv_rows, true},
-                   {a.v, a.v_strides, a.kv_heads, a.kv_rows, true},
-                   {a.out, a.out_strides, a.heads, a.q_rows, false}};
+    Tensor t[4] = {{a.q, a.q_strides, a.heads, a.q_rows},
+                   {a.k, a.k_strides, a.kv_heads, a.kv_rows},
+                   {a.v, a.v_strides, a.kv_heads, a.kv_rows},
+                   {a.out, a.out_strides, a.heads, a.q_rows}};
     Range r[4], lists[6];
     for (int i = 0; i < 4; ++i)
         if ((s = check_tensor(t[i], a.batch, a.head_dim, &r[i])) != H3QK_OK) return s;
@@ -265,11 +271,75 @@ extern "C" h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t strea
         if (a.kv_rows == 0) t[i] = t[0];
     p.stuck = stuck_addr();
     if (!p.stuck || !encode(&m.q, t[0], bf16, a.batch, a.head_dim) || !encode(&m.k, t[1], bf16, a.batch, a.head_dim) ||
-        !encode(&m.v, t[2], bf16, a.batch, a.head_dim)) {
-        const cudaError_t e = cudaGetLastError();
-        return h3qk_internal_fail_cuda(e != cudaSuccess ? e : cudaErrorInvalidValue);
-    }
+        !encode(&m.v, t[2], bf16, a.batch, a.head_dim))
+        return no_maps();
     return h3qk_ops::status_of(h3qk_core::forward_tiles(bf16, p, m, st));
+}
+
+extern "C" size_t h3qk_attention_backward_workspace_bytes(const h3qk_attn* call)
+{
+    if (!call || check_sizes(*call) != H3QK_OK) return 0;
+    return (static_cast<size_t>(call->batch) * call->heads * call->q_rows * 4 + 15) / 16 * 16;
+}
+
+extern "C" h3qk_status h3qk_attention_backward(const h3qk_attn* call, h3qk_stream_t stream)
+{
+    if (!call) return H3QK_ERR_INVALID_ARG;
+    const h3qk_attn& a = *call;
+    h3qk_status s = check_sizes(a);
+    if (s != H3QK_OK) return s;
+    constexpr int kIn = 5, kAll = 8;
+    Tensor t[kAll] = {{a.q, a.q_strides, a.heads, a.q_rows},
+                      {a.k, a.k_strides, a.kv_heads, a.kv_rows},
+                      {a.v, a.v_strides, a.kv_heads, a.kv_rows},
+                      {a.out, a.out_strides, a.heads, a.q_rows},
+                      {a.grad_out, a.grad_out_strides, a.heads, a.q_rows},
+                      {a.grad_q, a.grad_q_strides, a.heads, a.q_rows},
+                      {a.grad_k, a.grad_k_strides, a.kv_heads, a.kv_rows},
+                      {a.grad_v, a.grad_v_strides, a.kv_heads, a.kv_rows}};
+    Range r[kAll], lists[6];
+    for (int i = 0; i < kAll; ++i)
+        if ((s = check_tensor(t[i], a.batch, a.head_dim, &r[i])) != H3QK_OK) return s;
+    if ((s = check_lists(a, lists)) != H3QK_OK) return s;
+    if (a.q_rows == 0 && a.kv_rows == 0) return H3QK_OK;
+    const size_t need = h3qk_attention_backward_workspace_bytes(call);
+    if (a.q_rows > 0 && (!a.lse || !a.workspace || a.workspace_bytes < need)) return H3QK_ERR_INVALID_ARG;
+    if (!aligned(a.lse, 4) || (need && !aligned(a.workspace, 16))) return H3QK_ERR_MISALIGNED;
+    const Range lse = range_of(a.lse, static_cast<int64_t>(a.batch) * a.heads * a.q_rows * 4);
+    const Range outs[4] = {r[5], r[6], r[7], range_of(a.workspace, need)};
+    for (int i = 0; i < 4; ++i) {
+        if (i < 3 && !disjoint_rows(t[kIn + i], a.batch, a.head_dim)) return H3QK_ERR_ALIAS;
+        for (int k = i + 1; k < 4; ++k)
+            if (overlap(outs[i], outs[k])) return H3QK_ERR_ALIAS;
+        for (int k = 0; k < kIn; ++k)
+            if (overlap(outs[i], r[k])) return H3QK_ERR_ALIAS;
+        for (const Range& l : lists)
+            if (overlap(outs[i], l)) return H3QK_ERR_ALIAS;
+        if (overlap(outs[i], lse)) return H3QK_ERR_ALIAS;
+    }
+    Params p = {};
+    fill(p, a);
+    p.out = static_cast<uint16_t*>(a.out);
+    p.os = plain(t[3].s);
+    p.dout = static_cast<const uint16_t*>(a.grad_out);
+    p.dos = plain(t[4].s);
+    p.dq = static_cast<uint16_t*>(a.grad_q);
+    p.dqs = plain(t[5].s);
+    p.dk = static_cast<uint16_t*>(a.grad_k);
+    p.dks = plain(t[6].s);
+    p.dv = static_cast<uint16_t*>(a.grad_v);
+    p.dvs = plain(t[7].s);
+    p.delta = static_cast<float*>(a.workspace);
+    p.stuck = stuck_addr();
+    // Without rows or without keys nothing is loaded; the maps then describe the other tensors.
+    const int of[4] = {a.q_rows ? 0 : 1, a.kv_rows ? 1 : 0, a.kv_rows ? 2 : 0, a.q_rows ? 4 : 1};
+    const bool bf16 = a.dtype == H3QK_BF16;
+    Maps m;
+    CUtensorMap* maps[4] = {&m.q, &m.k, &m.v, &m.dout};
+    bool ok = p.stuck != nullptr;
+    for (int i = 0; i < 4; ++i) ok = ok && encode(maps[i], t[of[i]], bf16, a.batch, a.head_dim);
+    if (!ok) return no_maps();
+    return h3qk_ops::status_of(h3qk_core::backward_tiles(bf16, p, m, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int64_t h3qk_attention_stuck(void)

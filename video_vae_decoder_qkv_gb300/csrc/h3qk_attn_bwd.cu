@@ -1,0 +1,707 @@
+// Attention backward.  With p = 2^(s - lse) recomputed from the scores,
+//   delta = sum_d dout out,  dp = dout v^T,  ds = p (dp - delta) bend'(z),
+//   dv = p^T dout,  dq = scale ds k,  dk = scale ds^T q.
+//
+// Two kernels, each of which owns its sums: one block per 128 query rows for
+// dq (and delta), one per 128 keys of a K/V head for dk and dv, which walks
+// the query tiles of every head that shares them.  s and dp are computed
+// twice (7 products instead of 5), which buys results without atomics, the
+// same bits every time, and no binary32 copy of dq in memory.
+//
+// Both keep scores and dp in TMEM with the block's own rows as lanes, eight
+// warps turn them into p and ds (one thread a row and half the columns), and
+// p and ds return to TMEM as 16-bit A operands over the columns they came
+// from, each half of the warps within its own columns.  The tensor unit works
+// in order, so a product may be issued behind the one that still reads its
+// destination's old contents.
+#include "h3qk_attn.cuh"
+
+namespace {
+
+using namespace h3qk_tc;
+using h3qk_core::Bend;
+using h3qk_core::Params;
+using h3qk_core::Stretch;
+
+constexpr int kTile = 128;
+constexpr int kThreads = 384;           // 8 warps of arithmetic; products, loads, row statistics
+constexpr int kBlockBytes = 128 * 128;  // 64 columns of a tile
+
+template <int DP>
+struct BwdShape {
+    static constexpr int kBlocks = DP / 64;
+    static constexpr int kTileBytes = kBlocks * kBlockBytes;
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kTiles = (2 + kStages) * kTileBytes;  // the barriers follow
+};
+
+struct BwdShared {
+    uint64_t full[8], empty[8];
+    uint64_t own, fixed[2], done, drain;
+    uint64_t s_full[2], dp_full, p_ready, ds_ready, st_full[2], st_empty[2];
+    uint32_t tmem;
+    int stop;
+    alignas(16) float lse[2][kTile];
+    alignas(16) float delta[2][kTile];
+};
+
+// P is kept 2^10 larger in fp16, so that flat rows over many keys do not fall
+// into subnormals (p <= 1, so 2^10 is far from overflow); dv takes it back.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 10.0f;
+template <bool BF16>
+constexpr float kDrop = BF16 ? 1.0f : 1.0f / 1024.0f;
+
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int blocks, int row, int head, int item,
+                                          uint32_t bar)
+{
+    for (int b = 0; b < blocks; ++b) tma_load(dst + b * kBlockBytes, map, 64 * b, row, head, item, bar);
+}
+
+// Clears rows [first, 128) of a tile (one warp).
+__device__ __forceinline__ void clear_rows(uint32_t tile, int blocks, int first)
+{
+    const int lane = threadIdx.x & 31;
+    for (int b = 0; b < blocks; ++b)
+        for (int o = first * 128 + lane * 16; o < kBlockBytes; o += 512)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + b * kBlockBytes + o), "r"(0) : "memory");
+}
+
+// a b^T over the channels: both tiles K-major.
+__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a_tile, uint32_t b_tile, int steps, uint32_t shape)
+{
+    const uint64_t a = tile_desc(a_tile, 16), b = tile_desc(b_tile, 16);
+    for (int i = 0; i < steps; ++i) {
+        const uint32_t off = ((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4;
+        mma_ss(d, a + off, b + off, shape, i > 0);
+    }
+}
+
+// d += a b over 128 rows of b: a 16-bit pairs in TMEM, its two halves 64
+// columns apart; b with its channels as N.
+__device__ __forceinline__ void product_sum(uint32_t d, uint32_t a, uint32_t b_tile, uint32_t shape, bool add)
+{
+    const uint64_t b = tile_desc(b_tile, kBlockBytes);
+#pragma unroll
+    for (int i = 0; i < kTile / 16; ++i)
+        mma_ts(d, a + (i >> 2) * 64 + (i & 3) * 8, b + (i * 2048 >> 4), shape, add || i > 0);
+}
+
+// Writes DP/2 (or DP) columns of TMEM, scaled and rounded, as part of a row.
+template <bool BF16, int COLS>
+__device__ __forceinline__ void write_row(uint16_t* dst, uint32_t cols, int first, int dim, float by, bool zero, bool write)
+{
+#pragma unroll
+    for (int d = 0; d < COLS; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(o, cols + d);
+        tmem_wait_ld(o);
+        if (write) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (first + d + 8 * q < dim) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = zero ? 0u
+                                    : round_pair<BF16>(__uint_as_float(o[8 * q + 2 * e]) * by,
+                                                       __uint_as_float(o[8 * q + 2 * e + 1]) * by);
+                    *reinterpret_cast<uint4*>(dst + first + d + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+        }
+    }
+}
+
+// Given up: loads in flight must land before the block leaves.
+__device__ __forceinline__ void drain_loads(uint32_t full, int stages, int issued)
+{
+    for (int i = max(0, issued - stages); i < issued; ++i)
+        for (int t = 0; t < kMaxTries && !bar_test(full + 8 * (i % stages), (i / stages) & 1); ++t) {}
+}
+
+__device__ __forceinline__ void drain_products(uint32_t bar)
+{
+    mma_commit(bar);
+    for (int t = 0; t < kMaxTries && !bar_test(bar, 0); ++t) {}
+}
+
+// ---------------------------------------------------------------------------
+// dq: a block's 128 query rows against the keys they see.
+//   tensor unit   S0 dP0 | S1 dQ0 dP1 | S2 dQ1 dP2 | ...
+// S is double-buffered, so p of the next tile is computed while dQ and dP run.
+// ---------------------------------------------------------------------------
+template <bool BF16, int DP, bool BENT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                        const __grid_constant__ Params p)
+{
+    using Shape = BwdShape<DP>;
+    constexpr int kStages = Shape::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    BwdShared& sh = *reinterpret_cast<BwdShared*>(smem_raw + Shape::kTiles);
+    const uint32_t base = smem_addr(smem_raw);
+    if (base & 1023u) {  // the swizzle needs it; the launch gives it
+        if (threadIdx.x == 0) atomicAdd(p.stuck, 1u);
+        return;
+    }
+    const uint32_t q_smem = base, do_smem = base + Shape::kTileBytes, ring = base + 2 * Shape::kTileBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = blockIdx.y, kv_head = head / p.group;
+
+    Stretch s;
+    const int block = p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    if (!h3qk_core::find_stretch(s, p, block, blockIdx.z, kTile, false)) return;
+    const int tile_row = s.tile * kTile;
+    const int last = min(tile_row + kTile, s.rows) - 1;
+    const int seen = last < tile_row ? 0 : max(h3qk_core::limit_of(s, p.causal, last), 0);
+    const int n = (seen + kTile - 1) / kTile;
+    const bool fix = n * kTile > seen && s.k0 + seen < p.kv_rows;
+
+    const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty), own = smem_addr(&sh.own);
+    const uint32_t s_full = smem_addr(sh.s_full), dp_full = smem_addr(&sh.dp_full), ds_ready = smem_addr(&sh.ds_ready);
+    const uint32_t fixed = smem_addr(sh.fixed), done = smem_addr(&sh.done);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(full + 8 * i, 1);
+            bar_init(empty + 8 * i, 1);
+        }
+        bar_init(own, 1);
+        for (int i = 0; i < 2; ++i) bar_init(fixed + 8 * i, 1);
+        bar_init(done, 1);
+        bar_init(smem_addr(&sh.drain), 1);
+        bar_init(s_full, 1);
+        bar_init(s_full + 8, 1);
+        bar_init(dp_full, 1);
+        bar_init(ds_ready, 8);
+        sh.stop = 0;
+        bar_init_done();
+    }
+    if (warp == 8) tmem_alloc(smem_addr(&sh.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const uint32_t t_dp = tmem + 128, t_dq = tmem + 256;
+    auto t_s = [&](int j) { return tmem + ((j & 1) ? 384 : 0); };
+    volatile int* stop = &sh.stop;
+
+    if (warp == 9) {
+        int issued = 0;
+        if (lane == 0 && n > 0) {
+            bar_expect(own, 2 * Shape::kTileBytes);
+            load_tile(q_smem, &map_q, Shape::kBlocks, s.row0 + tile_row, head, s.item, own);
+            load_tile(do_smem, &map_do, Shape::kBlocks, s.row0 + tile_row, head, s.item, own);
+            for (int i = 0; i < 2 * n; ++i) {
+                const int st = i % kStages;
+                if (!bar_wait(empty + 8 * st, ((i / kStages) & 1) ^ 1, stop)) break;
+                bar_expect(full + 8 * st, Shape::kTileBytes);
+                load_tile(ring + st * Shape::kTileBytes, (i & 1) ? &map_v : &map_k, Shape::kBlocks,
+                          s.k0 + (i >> 1) * kTile, kv_head, s.item, full + 8 * st);
+                issued = i + 1;
+            }
+        }
+        __syncwarp();
+        if (fix) {
+            // Keys of the last tile that no row of the block sees: cleared,
+            // for dq multiplies ds = 0 with them.  (dp of such keys is not used.)
+            const int i = 2 * n - 2, st = i % kStages;
+            if (bar_wait(full + 8 * st, (i / kStages) & 1, stop)) {
+                clear_rows(ring + st * Shape::kTileBytes, Shape::kBlocks, seen - (n - 1) * kTile);
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(fixed);
+            }
+        }
+        __syncwarp();
+        if (*stop && lane == 0) {
+            if (n > 0)
+                for (int t = 0; t < kMaxTries && !bar_test(own, 0); ++t) {}
+            drain_loads(full, kStages, issued);
+        }
+    } else if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
+            constexpr uint32_t shape_d = mma_shape(BF16, 128, DP, true);
+            const int steps = (p.dim + 15) / 16;
+            auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
+            auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
+            auto release = [&](int i) { mma_commit(empty + 8 * (i % kStages)); };
+            auto scores = [&](int j) {
+                if (!loaded(2 * j)) return false;
+                if (fix && j == n - 1 && !bar_wait(fixed, 0, stop)) return false;
+                product_rows(t_s(j), q_smem, tile_at(2 * j), steps, shape_s);
+                mma_commit(s_full + 8 * (j & 1));
+                return true;
+            };
+            auto dprobs = [&](int j) {
+                if (!loaded(2 * j + 1)) return false;
+                product_rows(t_dp, do_smem, tile_at(2 * j + 1), steps, shape_s);
+                mma_commit(dp_full);
+                release(2 * j + 1);
+                return true;
+            };
+            bool ok = bar_wait(own, 0, stop) && scores(0) && dprobs(0);
+            for (int j = 0; j < n && ok; ++j) {
+                if (j + 1 < n) ok = scores(j + 1);
+                ok = ok && bar_wait(ds_ready, j & 1, stop);
+                if (!ok) break;
+                tc_fence_after();
+                product_sum(t_dq, t_dp, tile_at(2 * j), shape_d, j > 0);
+                release(2 * j);
+                if (j + 1 < n) ok = dprobs(j + 1);
+            }
+            if (ok) mma_commit(done);
+            if (*stop) drain_products(smem_addr(&sh.drain));
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        const int g = warp >> 2, r = threadIdx.x & 127;
+        const int i_row = tile_row + r;
+        const bool has = i_row < s.rows;
+        const int64_t row = s.row0 + i_row;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        // delta = dout . out of the row; each half of the warps takes every other 8 channels.
+        float part = 0.0f;
+        if (has) {
+            const uint16_t* o = p.out + s.item * p.os.item + head * p.os.head + row * p.os.row;
+            const uint16_t* d = p.dout + s.item * p.dos.item + head * p.dos.head + row * p.dos.row;
+            for (int c = 8 * g; c < p.dim; c += 16) {
+                const uint4 ov = __ldg(reinterpret_cast<const uint4*>(o + c));
+                const uint4 dv = __ldg(reinterpret_cast<const uint4*>(d + c));
+                const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 a = widen_pair<BF16>(ow[e]), b = widen_pair<BF16>(dw[e]);
+                    part = fmaf(a.x, b.x, part);
+                    part = fmaf(a.y, b.y, part);
+                }
+            }
+        }
+        sh.delta[g][r] = part;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float delta = sh.delta[0][r] + sh.delta[1][r];
+        const int64_t stat = (static_cast<int64_t>(s.item) * p.heads + head) * p.q_rows + row;
+        float lse = INFINITY;  // p = 0
+        if (has) {
+            if (g == 0) p.delta[stat] = delta;
+            const float v = __ldg(p.lse + stat);
+            if (v != -INFINITY) lse = v * h3qk_core::kLog2e;
+        }
+        const int lim = h3qk_core::limit_of(s, p.causal, i_row);
+        const int lim_first = h3qk_core::limit_of(s, p.causal, tile_row);
+        const Bend bend = h3qk_core::bend_of(p, head);
+        const float c = p.scale * h3qk_core::kLog2e;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            ok = bar_wait(s_full + 8 * (j & 1), (j >> 1) & 1, stop);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t sr[2][32];
+            tmem_ld32(sr[0], t_s(j) + lanes + 64 * g);
+            tmem_ld32(sr[1], t_s(j) + lanes + 64 * g + 32);
+            tmem_wait_ld(sr[0]);
+            tmem_wait_ld(sr[1]);
+            const float far = static_cast<float>(s.start + i_row - j * kTile - 64 * g);
+            const bool edge = (j + 1) * kTile > lim_first;
+            const int left = lim - j * kTile - 64 * g;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float v = __uint_as_float(sr[b][e]);
+                    float pv;
+                    if constexpr (BENT) {
+                        v *= bend.in;
+                        float t = 0.0f;
+                        if (bend.capped) {
+                            t = h3qk_core::tanh_half(v);
+                            v = bend.cap * t;
+                        }
+                        v = fmaf(-bend.slope, fabsf(far - static_cast<float>(32 * b + e)), v);
+                        pv = exp2_fast(v - lse) * fmaf(-t, t, 1.0f);
+                    } else {
+                        pv = exp2_fast(fmaf(v, c, -lse));
+                    }
+                    sr[b][e] = __float_as_uint(pv);
+                }
+            ok = bar_wait(dp_full, j & 1, stop);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t dp[32], w[16];
+                tmem_ld32(dp, t_dp + lanes + 64 * g + 32 * b);
+                tmem_wait_ld(dp);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float d[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        d[q] = __uint_as_float(sr[b][2 * e + q]) * (__uint_as_float(dp[2 * e + q]) - delta);
+                        if (edge && 32 * b + 2 * e + q >= left) d[q] = 0.0f;
+                    }
+                    w[e] = round_pair<BF16>(d[0], d[1]);
+                }
+                tmem_st16(t_dp + lanes + 64 * g + 16 * b, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(ds_ready);
+        }
+        if (ok && n > 0) ok = bar_wait(done, 0, stop);
+        tc_fence_after();
+        uint16_t* dst = p.dq + s.item * p.dqs.item + head * p.dqs.head + row * p.dqs.row;
+        write_row<BF16, DP / 2>(dst, t_dq + lanes + g * (DP / 2), g * (DP / 2), p.dim, p.scale, !(ok && has && n > 0),
+                                i_row < s.span);
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *stop) atomicAdd(p.stuck, 1u);
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dk, dv: a block's 128 keys of a K/V head against the query tiles that see
+// them, of every head that shares it.
+//   tensor unit   S0 dP0 | dV0 S1 dK0 dP1 | dV1 S2 dK1 dP2 | ...
+// (S = k q^T and dP = v dout^T: the keys are the lanes.)  p of the next tile
+// is computed while dK and dP run, ds while dV and S run.
+// ---------------------------------------------------------------------------
+template <bool BF16, int DP, bool BENT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                         const __grid_constant__ Params p)
+{
+    using Shape = BwdShape<DP>;
+    constexpr int kStages = Shape::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    BwdShared& sh = *reinterpret_cast<BwdShared*>(smem_raw + Shape::kTiles);
+    const uint32_t base = smem_addr(smem_raw);
+    if (base & 1023u) {  // the swizzle needs it; the launch gives it
+        if (threadIdx.x == 0) atomicAdd(p.stuck, 1u);
+        return;
+    }
+    const uint32_t k_smem = base, v_smem = base + Shape::kTileBytes, ring = base + 2 * Shape::kTileBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kv_head = blockIdx.y;
+
+    Stretch s;
+    if (!h3qk_core::find_stretch(s, p, blockIdx.x, blockIdx.z, kTile, true)) return;
+    const int tile_key = s.tile * kTile;
+    const int q_tiles = (s.rows + kTile - 1) / kTile;
+    // First query tile that sees any of the keys; none if the keys do not exist.
+    const int first_row = !p.causal || tile_key < s.prefix ? 0 : max(tile_key - s.start, 0);
+    const int q_first = tile_key < s.keys ? min(first_row / kTile, q_tiles) : q_tiles;
+    const int per_head = q_tiles - q_first;
+    const int n = per_head * p.group;
+    // Rows of each head's last query tile past the rows that attend.
+    const bool fix = s.rows % kTile != 0 && s.row0 + s.rows < p.q_rows;
+
+    const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty), own = smem_addr(&sh.own);
+    const uint32_t s_full = smem_addr(sh.s_full), dp_full = smem_addr(&sh.dp_full);
+    const uint32_t p_ready = smem_addr(&sh.p_ready), ds_ready = smem_addr(&sh.ds_ready);
+    const uint32_t st_full = smem_addr(sh.st_full), st_empty = smem_addr(sh.st_empty);
+    const uint32_t fixed = smem_addr(sh.fixed), done = smem_addr(&sh.done);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(full + 8 * i, 1);
+            bar_init(empty + 8 * i, 1);
+        }
+        bar_init(own, 1);
+        for (int i = 0; i < 2; ++i) bar_init(fixed + 8 * i, 1);
+        bar_init(done, 1);
+        bar_init(smem_addr(&sh.drain), 1);
+        bar_init(s_full, 1);
+        bar_init(dp_full, 1);
+        bar_init(p_ready, 8);
+        bar_init(ds_ready, 8);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(st_full + 8 * i, 1);
+            bar_init(st_empty + 8 * i, 8);
+        }
+        sh.stop = 0;
+        bar_init_done();
+    }
+    if (warp == 8) tmem_alloc(smem_addr(&sh.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+    volatile int* stop = &sh.stop;
+    auto head_of = [&](int i) { return kv_head * p.group + i / per_head; };
+    auto row_of = [&](int i) { return (q_first + i % per_head) * kTile; };
+
+    if (warp == 9) {
+        int issued = 0;
+        if (lane == 0 && n > 0) {
+            bar_expect(own, 2 * Shape::kTileBytes);
+            load_tile(k_smem, &map_k, Shape::kBlocks, s.k0 + tile_key, kv_head, s.item, own);
+            load_tile(v_smem, &map_v, Shape::kBlocks, s.k0 + tile_key, kv_head, s.item, own);
+            for (int i = 0; i < 2 * n; ++i) {
+                const int st = i % kStages;
+                if (!bar_wait(empty + 8 * st, ((i / kStages) & 1) ^ 1, stop)) break;
+                bar_expect(full + 8 * st, Shape::kTileBytes);
+                load_tile(ring + st * Shape::kTileBytes, (i & 1) ? &map_do : &map_q, Shape::kBlocks,
+                          s.row0 + row_of(i >> 1), head_of(i >> 1), s.item, full + 8 * st);
+                issued = i + 1;
+            }
+        }
+        __syncwarp();
+        if (*stop && lane == 0) {
+            if (n > 0)
+                for (int t = 0; t < kMaxTries && !bar_test(own, 0); ++t) {}
+            drain_loads(full, kStages, issued);
+        }
+    } else if (warp == 10) {
+        // Statistics of each query tile: lse in powers of two (infinite where
+        // the row sees nothing or does not attend, so that p = 0), and delta.
+        for (int i = 0; i < n; ++i) {
+            float l[4], d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = row_of(i) + 32 * e + lane;
+                l[e] = INFINITY;
+                d[e] = 0.0f;
+                if (r < s.rows) {
+                    const int64_t at = (static_cast<int64_t>(s.item) * p.heads + head_of(i)) * p.q_rows + s.row0 + r;
+                    const float v = __ldg(p.lse + at);
+                    if (v != -INFINITY) l[e] = fmaf(v, h3qk_core::kLog2e, -kLift<BF16>);
+                    d[e] = __ldcg(p.delta + at) * kDrop<BF16>;
+                }
+            }
+            if (!bar_wait(st_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, stop)) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sh.lse[i & 1][32 * e + lane] = l[e];
+                sh.delta[i & 1][32 * e + lane] = d[e];
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(st_full + 8 * (i & 1));
+            if (fix && i % per_head == per_head - 1) {
+                // The head's last tile: rows that do not attend are cleared, for
+                // dv and dk multiply p = ds = 0 with them.  The wait above says
+                // that tile i - 2 is done, so this tile's stages are in their
+                // present use; the products wait for `fixed` before the next.
+                bool ok = true;
+                for (int k = 2 * i; k < 2 * i + 2 && ok; ++k) {
+                    ok = bar_wait(full + 8 * (k % kStages), (k / kStages) & 1, stop);
+                    if (ok) clear_rows(ring + (k % kStages) * Shape::kTileBytes, Shape::kBlocks, s.rows % kTile);
+                }
+                if (!ok) break;
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(fixed + 8 * (i / per_head & 1));
+            }
+        }
+    } else if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
+            constexpr uint32_t shape_d = mma_shape(BF16, 128, DP, true);
+            const int steps = (p.dim + 15) / 16;
+            auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
+            auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
+            auto release = [&](int i) { mma_commit(empty + 8 * (i % kStages)); };
+            // The clearing warp is at most one head ahead: two barriers tell its turns apart.
+            auto cleared = [&](int h) { return bar_wait(fixed + 8 * (h & 1), (h >> 1) & 1, stop); };
+            auto scores = [&](int i) {
+                if (!loaded(2 * i)) return false;
+                if (fix && i % per_head == per_head - 1 && !cleared(i / per_head)) return false;
+                product_rows(t_s, k_smem, tile_at(2 * i), steps, shape_s);
+                mma_commit(s_full);
+                return true;
+            };
+            auto dprobs = [&](int i) {
+                if (!loaded(2 * i + 1)) return false;
+                product_rows(t_dp, v_smem, tile_at(2 * i + 1), steps, shape_s);
+                mma_commit(dp_full);
+                return true;
+            };
+            bool ok = bar_wait(own, 0, stop) && scores(0) && dprobs(0);
+            for (int i = 0; i < n && ok; ++i) {
+                ok = bar_wait(p_ready, i & 1, stop);
+                if (!ok) break;
+                tc_fence_after();
+                product_sum(t_dv, t_s, tile_at(2 * i + 1), shape_d, i > 0);
+                release(2 * i + 1);
+                if (i + 1 < n) ok = scores(i + 1);
+                ok = ok && bar_wait(ds_ready, i & 1, stop);
+                if (!ok) break;
+                tc_fence_after();
+                product_sum(t_dk, t_dp, tile_at(2 * i), shape_d, i > 0);
+                release(2 * i);
+                if (i + 1 < n) ok = dprobs(i + 1);
+            }
+            if (ok) mma_commit(done);
+            if (*stop) drain_products(smem_addr(&sh.drain));
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        const int g = warp >> 2, r = threadIdx.x & 127;
+        const int key = tile_key + r;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        // Row i sees the key when i >= from.
+        const int from = p.causal && key >= s.prefix ? key - s.start : -h3qk_core::kFar;
+        const int last_key = min(tile_key + kTile, s.keys) - 1;
+        const int from_last = p.causal && last_key >= s.prefix ? last_key - s.start : -h3qk_core::kFar;
+        const float c = p.scale * h3qk_core::kLog2e;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int row0 = row_of(i) + 64 * g;
+            const Bend bend = h3qk_core::bend_of(p, head_of(i));
+            ok = bar_wait(st_full + 8 * (i & 1), (i >> 1) & 1, stop) && bar_wait(s_full, i & 1, stop);
+            if (!ok) break;
+            tc_fence_after();
+            const float4* lse = reinterpret_cast<const float4*>(sh.lse[i & 1] + 64 * g);
+            const float4* del = reinterpret_cast<const float4*>(sh.delta[i & 1] + 64 * g);
+            uint32_t sr[2][32];
+            tmem_ld32(sr[0], t_s + lanes + 64 * g);
+            tmem_ld32(sr[1], t_s + lanes + 64 * g + 32);
+            tmem_wait_ld(sr[0]);
+            tmem_wait_ld(sr[1]);
+            const bool edge = row_of(i) < from_last;
+            const float far = static_cast<float>(s.start + row0 - key);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e4 = 0; e4 < 8; ++e4) {
+                    const float4 l4 = lse[8 * b + e4];
+                    const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+                    float pv[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int e = 4 * e4 + q;
+                        float v = __uint_as_float(sr[b][e]);
+                        float keep = 1.0f;
+                        if constexpr (BENT) {
+                            v *= bend.in;
+                            if (bend.capped) {
+                                const float t = h3qk_core::tanh_half(v);
+                                v = bend.cap * t;
+                                keep = fmaf(-t, t, 1.0f);
+                            }
+                            v = fmaf(-bend.slope, fabsf(far + static_cast<float>(32 * b + e)), v);
+                            pv[q] = exp2_fast(v - lv[q]);
+                        } else {
+                            pv[q] = exp2_fast(fmaf(v, c, -lv[q]));
+                        }
+                        if (edge && row0 + 32 * b + e < from) pv[q] = 0.0f;
+                        sr[b][e] = __float_as_uint(BENT ? pv[q] * keep : pv[q]);
+                    }
+                    w[2 * e4] = round_pair<BF16>(pv[0], pv[1]);
+                    w[2 * e4 + 1] = round_pair<BF16>(pv[2], pv[3]);
+                }
+                tmem_st16(t_s + lanes + 64 * g + 16 * b, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(p_ready);
+            ok = bar_wait(dp_full, i & 1, stop);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t dp[32], w[16];
+                tmem_ld32(dp, t_dp + lanes + 64 * g + 32 * b);
+                tmem_wait_ld(dp);
+#pragma unroll
+                for (int e4 = 0; e4 < 8; ++e4) {
+                    const float4 d4 = del[8 * b + e4];
+                    const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
+                    float d[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        d[q] = __uint_as_float(sr[b][4 * e4 + q]) *
+                               fmaf(__uint_as_float(dp[4 * e4 + q]), kDrop<BF16>, -dv[q]);
+                    w[2 * e4] = round_pair<BF16>(d[0], d[1]);
+                    w[2 * e4 + 1] = round_pair<BF16>(d[2], d[3]);
+                }
+                tmem_st16(t_dp + lanes + 64 * g + 16 * b, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(ds_ready);
+                bar_arrive(st_empty + 8 * (i & 1));
+            }
+        }
+        if (ok && n > 0) ok = bar_wait(done, 0, stop);
+        tc_fence_after();
+        const int64_t row = s.k0 + key;
+        const bool zero = !(ok && n > 0 && key < s.keys);
+        if (g == 0)
+            write_row<BF16, DP>(p.dv + s.item * p.dvs.item + kv_head * p.dvs.head + row * p.dvs.row, t_dv + lanes, 0,
+                                p.dim, kDrop<BF16>, zero, key < s.span);
+        else
+            write_row<BF16, DP>(p.dk + s.item * p.dks.item + kv_head * p.dks.head + row * p.dks.row, t_dk + lanes, 0,
+                                p.dim, p.scale, zero, key < s.span);
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *stop) atomicAdd(p.stuck, 1u);
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+template <typename K>
+cudaError_t raise(K* kernel, int smem, bool (&raised)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    if (raised[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    raised[dev] = e == cudaSuccess;
+    return e;
+}
+
+template <bool BF16, int DP, bool BENT>
+cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
+{
+    constexpr int smem = BwdShape<DP>::kTiles + static_cast<int>(sizeof(BwdShared));
+    static_assert(smem <= 227 * 1024, "tiles and barriers exceed a block's shared memory");
+    static bool raised[2][64] = {};
+    auto* dq = attention_dq_kernel<BF16, DP, BENT>;
+    auto* dkv = attention_dkv_kernel<BF16, DP, BENT>;
+    cudaError_t e = raise(dq, smem, raised[0]);
+    if (e == cudaSuccess) e = raise(dkv, smem, raised[1]);
+    if (e != cudaSuccess) return e;
+    if (p.q_rows > 0) {
+        const dim3 grid(static_cast<unsigned>(h3qk_core::tiles_of(p, p.q_rows, kTile)), p.heads, p.batch);
+        dq<<<grid, kThreads, smem, st>>>(m.q, m.k, m.v, m.dout, p);
+        h3qk_internal_count_launch();
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (p.kv_rows > 0) {
+        const dim3 grid(static_cast<unsigned>(h3qk_core::tiles_of(p, p.kv_rows, kTile)), p.kv_heads, p.batch);
+        dkv<<<grid, kThreads, smem, st>>>(m.q, m.k, m.v, m.dout, p);
+        h3qk_internal_count_launch();
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+template <bool BF16>
+cudaError_t by_shape(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
+{
+    const bool bent = p.cap > 0.0f || p.slopes;
+    if (p.dim <= 64) return bent ? launch<BF16, 64, true>(p, m, st) : launch<BF16, 64, false>(p, m, st);
+    return bent ? launch<BF16, 128, true>(p, m, st) : launch<BF16, 128, false>(p, m, st);
+}
+
+}  // namespace
+
+cudaError_t h3qk_core::backward_tiles(bool bf16, const Params& p, const Maps& m, cudaStream_t st)
+{
+    return bf16 ? by_shape<true>(p, m, st) : by_shape<false>(p, m, st);
+}

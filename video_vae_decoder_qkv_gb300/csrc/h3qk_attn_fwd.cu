@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t sr[4][32];
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_ld32(sr[b], s_cols + 32 * b);
-            tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_wait_ld(sr[b]);
             if constexpr (BENT) {
                 float far = static_cast<float>(s.start + i_row - j * kTile);
 #pragma unroll
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int d = 0; d < DP; d += 32) {
                         uint32_t o[32];
                         tmem_ld32(o, o_cols + d);
-                        tmem_wait_ld();
+                        tmem_wait_ld(o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                         tmem_st32(o_cols + d, o);
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t o[32];
             if (n[g] > 0) {
                 tmem_ld32(o, o_cols + d);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
             }
             if (write) {
 #pragma unroll
