@@ -67,24 +67,43 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int blocks, int first)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + b * kBlockBytes + o), "r"(0) : "memory");
 }
 
-// a b^T over the channels: both tiles K-major.
-__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a_tile, uint32_t b_tile, int steps, uint32_t shape)
+// a b^T over the channels: both tiles K-major.  `then` gets an arrival when
+// the product is done.
+template <int DP>
+__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a_tile, uint32_t b_tile, int steps, uint32_t shape,
+                                             uint32_t then)
 {
     const uint64_t a = tile_desc(a_tile, 16), b = tile_desc(b_tile, 16);
-    for (int i = 0; i < steps; ++i) {
-        const uint32_t off = ((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4;
-        mma_ss(d, a + off, b + off, shape, i > 0);
+    if (elect_lane()) {
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+            if (i < steps) {
+                const uint32_t off = ((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4;
+                mma_ss(d, a + off, b + off, shape, i > 0);
+            }
+        mma_commit(then);
     }
+    __syncwarp();
 }
 
 // d += a b over 128 rows of b: a 16-bit pairs in TMEM, its two halves 64
 // columns apart; b with its channels as N.
-__device__ __forceinline__ void product_sum(uint32_t d, uint32_t a, uint32_t b_tile, uint32_t shape, bool add)
+__device__ __forceinline__ void product_sum(uint32_t d, uint32_t a, uint32_t b_tile, uint32_t shape, bool add, uint32_t then)
 {
     const uint64_t b = tile_desc(b_tile, kBlockBytes);
+    if (elect_lane()) {
 #pragma unroll
-    for (int i = 0; i < kTile / 16; ++i)
-        mma_ts(d, a + (i >> 2) * 64 + (i & 3) * 8, b + (i * 2048 >> 4), shape, add || i > 0);
+        for (int i = 0; i < kTile / 16; ++i)
+            mma_ts(d, a + (i >> 2) * 64 + (i & 3) * 8, b + (i * 2048 >> 4), shape, add || i > 0);
+        mma_commit(then);
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void signal(uint32_t bar)
+{
+    if (elect_lane()) mma_commit(bar);
+    __syncwarp();
 }
 
 // Writes DP/2 (or DP) columns of TMEM, scaled and rounded, as part of a row.
@@ -146,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     const uint32_t q_smem = base, do_smem = base + Shape::kTileBytes, ring = base + 2 * Shape::kTileBytes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int head = blockIdx.y, kv_head = head / p.group;
 
     Stretch s;
@@ -220,25 +239,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_loads(full, kStages, issued);
         }
     } else if (warp == 8) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
             constexpr uint32_t shape_d = mma_shape(BF16, 128, DP, true);
             const int steps = (p.dim + 15) / 16;
             auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
             auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
-            auto release = [&](int i) { mma_commit(empty + 8 * (i % kStages)); };
+            auto free = [&](int i) { return empty + 8 * (i % kStages); };
             auto scores = [&](int j) {
                 if (!loaded(2 * j)) return false;
                 if (fix && j == n - 1 && !bar_wait(fixed, 0, stop)) return false;
-                product_rows(t_s(j), q_smem, tile_at(2 * j), steps, shape_s);
-                mma_commit(s_full + 8 * (j & 1));
+                product_rows<DP>(t_s(j), q_smem, tile_at(2 * j), steps, shape_s, s_full + 8 * (j & 1));
                 return true;
             };
             auto dprobs = [&](int j) {
                 if (!loaded(2 * j + 1)) return false;
-                product_rows(t_dp, do_smem, tile_at(2 * j + 1), steps, shape_s);
-                mma_commit(dp_full);
-                release(2 * j + 1);
+                product_rows<DP>(t_dp, do_smem, tile_at(2 * j + 1), steps, shape_s, dp_full);
+                signal(free(2 * j + 1));
                 return true;
             };
             bool ok = bar_wait(own, 0, stop) && scores(0) && dprobs(0);
@@ -247,12 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = ok && bar_wait(ds_ready, j & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
-                product_sum(t_dq, t_dp, tile_at(2 * j), shape_d, j > 0);
-                release(2 * j);
+                product_sum(t_dq, t_dp, tile_at(2 * j), shape_d, j > 0, free(2 * j));
                 if (j + 1 < n) ok = dprobs(j + 1);
             }
-            if (ok) mma_commit(done);
-            if (*stop) drain_products(smem_addr(&sh.drain));
+            if (ok) signal(done);
+            __syncwarp();
+            if (*stop && elect_lane()) drain_products(smem_addr(&sh.drain));
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -388,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     const uint32_t k_smem = base, v_smem = base + Shape::kTileBytes, ring = base + 2 * Shape::kTileBytes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int kv_head = blockIdx.y;
 
     Stretch s;
@@ -501,26 +518,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 8) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
             constexpr uint32_t shape_d = mma_shape(BF16, 128, DP, true);
             const int steps = (p.dim + 15) / 16;
             auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
             auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
-            auto release = [&](int i) { mma_commit(empty + 8 * (i % kStages)); };
+            auto free = [&](int i) { return empty + 8 * (i % kStages); };
             // The clearing warp is at most one head ahead: two barriers tell its turns apart.
             auto cleared = [&](int h) { return bar_wait(fixed + 8 * (h & 1), (h >> 1) & 1, stop); };
             auto scores = [&](int i) {
                 if (!loaded(2 * i)) return false;
                 if (fix && i % per_head == per_head - 1 && !cleared(i / per_head)) return false;
-                product_rows(t_s, k_smem, tile_at(2 * i), steps, shape_s);
-                mma_commit(s_full);
+                product_rows<DP>(t_s, k_smem, tile_at(2 * i), steps, shape_s, s_full);
                 return true;
             };
             auto dprobs = [&](int i) {
                 if (!loaded(2 * i + 1)) return false;
-                product_rows(t_dp, v_smem, tile_at(2 * i + 1), steps, shape_s);
-                mma_commit(dp_full);
+                product_rows<DP>(t_dp, v_smem, tile_at(2 * i + 1), steps, shape_s, dp_full);
                 return true;
             };
             bool ok = bar_wait(own, 0, stop) && scores(0) && dprobs(0);
@@ -528,18 +543,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = bar_wait(p_ready, i & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
-                product_sum(t_dv, t_s, tile_at(2 * i + 1), shape_d, i > 0);
-                release(2 * i + 1);
+                product_sum(t_dv, t_s, tile_at(2 * i + 1), shape_d, i > 0, free(2 * i + 1));
                 if (i + 1 < n) ok = scores(i + 1);
                 ok = ok && bar_wait(ds_ready, i & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
-                product_sum(t_dk, t_dp, tile_at(2 * i), shape_d, i > 0);
-                release(2 * i);
+                product_sum(t_dk, t_dp, tile_at(2 * i), shape_d, i > 0, free(2 * i));
                 if (i + 1 < n) ok = dprobs(i + 1);
             }
-            if (ok) mma_commit(done);
-            if (*stop) drain_products(smem_addr(&sh.drain));
+            if (ok) signal(done);
+            __syncwarp();
+            if (*stop && elect_lane()) drain_products(smem_addr(&sh.drain));
         }
         __syncwarp();
     } else if (warp < 8) {

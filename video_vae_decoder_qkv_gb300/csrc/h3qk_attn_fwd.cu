@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ FwdShared sh;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t q_smem = base, ring = base + 2 * Shape::kTileBytes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int head = blockIdx.y;
     const int kv_head = head / p.group;
 
@@ -170,51 +170,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
         regs_down<kOtherRegs>();
         // ---- matrix products ------------------------------------------------
-        if (lane == 0 && n_all > 0) {
+        if (n_all > 0) {
             constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
             constexpr uint32_t shape_o = mma_shape(BF16, 128, DP, true);
             const int steps = (p.dim + 15) / 16;
-            auto scores = [&](int g, uint32_t k_tile) {
-                const uint64_t a = tile_desc(q_smem + g * Shape::kTileBytes, 16), b = tile_desc(k_tile, 16);
-                for (int i = 0; i < steps; ++i) {
-                    const uint32_t off = ((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4;
-                    mma_ss(tmem + g * 128, a + off, b + off, shape_s, i > 0);
-                }
-                mma_commit(s_full + 8 * g);
-            };
-            auto values = [&](int g, uint32_t v_tile, bool add) {
-                const uint64_t b = tile_desc(v_tile, kBlockBytes);
+            auto scores = [&](int g, int i) {  // from K tile i of the ring
+                const uint64_t a = tile_desc(q_smem + g * Shape::kTileBytes, 16);
+                const uint64_t b = tile_desc(ring + (i % kStages) * Shape::kTileBytes, 16);
+                if (elect_lane()) {
 #pragma unroll
-                for (int i = 0; i < kTile / 16; ++i)
-                    mma_ts(tmem + 256 + g * DP, tmem + g * 128 + 8 * i, b + (i * 2048 >> 4), shape_o, add || i > 0);
-                mma_commit(o_done + 8 * g);
+                    for (int k = 0; k < DP / 16; ++k)
+                        if (k < steps) {
+                            constexpr int kStep = 32 >> 4, kNext = kBlockBytes >> 4;
+                            const uint32_t off = (k >> 2) * kNext + (k & 3) * kStep;
+                            mma_ss(tmem + g * 128, a + off, b + off, shape_s, k > 0);
+                        }
+                    mma_commit(s_full + 8 * g);
+                }
+                __syncwarp();
             };
-            auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
+            auto values = [&](int g, int i, bool add) {
+                const uint64_t b = tile_desc(ring + (i % kStages) * Shape::kTileBytes, kBlockBytes);
+                if (elect_lane()) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem + 256 + g * DP, tmem + g * 128 + 8 * k, b + (k * 2048 >> 4), shape_o, add || k > 0);
+                    mma_commit(o_done + 8 * g);
+                }
+                __syncwarp();
+            };
+            auto release = [&](int i) {
+                if (elect_lane()) mma_commit(empty + 8 * (i % kStages));
+                __syncwarp();
+            };
             auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
             bool ok = bar_wait(q_full, 0, stop) && loaded(0);
             if (ok) {
                 for (int g = 0; g < 2; ++g)
-                    if (n[g] > 0) scores(g, tile_at(0));
-                mma_commit(empty);
+                    if (n[g] > 0) scores(g, 0);
+                release(0);
             }
             for (int j = 0; j < n_all && ok; ++j) {
                 const bool more = j + 1 < n_all;
                 ok = loaded(2 * j + 1) && (!more || loaded(2 * j + 2));
                 if (ok && fix && !more) ok = bar_wait(fixed, 0, stop);
-                for (int g = 0; g < 2 && ok; ++g) {
-                    if (j < n[g]) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (ok && j < n[g]) {
                         ok = bar_wait(p_ready + 8 * g, j & 1, stop);
-                        if (!ok) break;
                         tc_fence_after();
-                        values(g, tile_at(2 * j + 1), j > 0);
+                        if (ok) values(g, 2 * j + 1, j > 0);
                     }
-                    if (j + 1 < n[g]) scores(g, tile_at(2 * j + 2));
+                    if (ok && j + 1 < n[g]) scores(g, 2 * j + 2);
                 }
                 if (!ok) break;
-                mma_commit(empty + 8 * ((2 * j + 1) % kStages));
-                if (more) mma_commit(empty + 8 * ((2 * j + 2) % kStages));
+                release(2 * j + 1);
+                if (more) release(2 * j + 2);
             }
-            if (*stop) {
+            __syncwarp();
+            if (*stop && elect_lane()) {
                 const uint32_t drain = smem_addr(&sh.drain);
                 mma_commit(drain);
                 for (int t = 0; t < kMaxTries && !bar_test(drain, 0); ++t) {}

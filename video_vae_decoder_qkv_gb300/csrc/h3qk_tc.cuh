@@ -181,6 +181,19 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
+// One lane of a converged warp: the products' issuer.  The whole warp runs
+// the loop around it, so that descriptors and addresses stay in uniform
+// registers, where the instruction takes them from.
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes));
+    return yes != 0;
+}
 // The barrier gets one arrival when all products issued so far by this thread are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
