@@ -35,15 +35,29 @@ _SIGNATURES = {
 }
 
 
+_functions = {}   # name -> (library, function): a reloaded library gets its own
+_sizes = {}       # workspace sizes by entry point, device and shape
+
+
 def _fn(name):
-    f = getattr(h3qk.lib(), name)
-    if f.argtypes is None:
+    L = h3qk.lib()
+    known = _functions.get(name)
+    if known is None or known[0] is not L:
+        f = getattr(L, name)
         f.restype, f.argtypes = _SIGNATURES[name]
-    return f
+        known = _functions[name] = (L, f)
+    return known[1]
+
+
+# The current stream's address without the Stream object around it (2 us less
+# a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, dev):
     if stream is None:
+        if _raw_stream is not None and dev.index is not None:
+            return _raw_stream(dev.index)
         return torch.cuda.current_stream(dev).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
@@ -61,12 +75,21 @@ def _call(name, dev, *args):
         raise H3QKError(st, h3qk.status_string(st), int(h3qk.lib().h3qk_last_cuda_error()), name)
 
 
-def _size(name, dev, *args):
-    """A workspace size, asked with the tensors' device current."""
-    if dev.index == torch.cuda.current_device():
-        return _fn(name)(*args)
-    with torch.cuda.device(dev):
-        return _fn(name)(*args)
+def _size(name, dev, *args, key=None):
+    """A workspace size, asked once per device and shape (the arguments, or
+    ``key``) with the tensors' device current."""
+    at = (name, dev.index, key or args)
+    n = _sizes.get(at)
+    if n is None:
+        if dev.index == torch.cuda.current_device():
+            n = _fn(name)(*args)
+        else:
+            with torch.cuda.device(dev):
+                n = _fn(name)(*args)
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        _sizes[at] = n
+    return n
 
 
 def _workspace(workspace, nbytes, dev):
@@ -79,6 +102,8 @@ def _workspace(workspace, nbytes, dev):
 def _need_rows(x, name, dtypes):
     if x.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
+    if x.dim() == 2 and x.is_contiguous():
+        return
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError(f"{name} must be 2-D [rows, width] with unit inner stride")
     if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
@@ -93,7 +118,7 @@ def _need_affine(w, name, width, batch, dev):
     """The groups a weight stands for: [width] is shared, [batch, width] has a row per item."""
     if w.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {w.dtype}")
-    if tuple(w.shape) not in ((width,), (batch, width)):
+    if w.shape != (width,) and w.shape != (batch, width):
         raise ValueError(f"{name} must have shape ({width},) or ({batch}, {width}), got {tuple(w.shape)}")
     if not w.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -109,7 +134,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6, batch: int = 1, 
     adaptive norm).  Returns (y, stats): y [rows, width] of x's type, stats
     float32 [rows, 2] with each row's mean and reciprocal deviation, which
     ``layer_norm_backward`` reads (h3qk_layer_norm)."""
-    _need_rows(x, "x", tuple(_DTYPES))
+    _need_rows(x, "x", _DTYPES)
     rows, width = x.shape
     dev = x.device
     if batch < 1 or rows % batch:
@@ -141,7 +166,7 @@ def layer_norm_backward(grad_out, x, weight, stats, *, batch: int = 1, need_weig
     (grad_x, grad_weight, grad_bias); the last two are float32 of the
     weight's shape, summed over the rows that share them, or None without a
     weight or with ``need_weight_grad=False`` (h3qk_layer_norm_backward)."""
-    _need_rows(x, "x", tuple(_DTYPES))
+    _need_rows(x, "x", _DTYPES)
     _need_rows(grad_out, "grad_out", (x.dtype,))
     rows, width = x.shape
     dev = x.device
@@ -232,7 +257,7 @@ _NO_STRIDES = (0, 0, 0)
 def _need_heads(t, name, shape, dtype, dev):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
@@ -330,12 +355,16 @@ def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slop
                           0, 0, 0, 0, *lists, ws, ws_bytes, *strides[0], *strides[1], *strides[2], *out_strides,
                           *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES)
 
-    packed = args(0, 0)
-    need = _size("h3qk_attention_workspace_bytes", dev, packed)
+    # the size depends on the shape alone
+    shape = (batch, heads, kv_heads, sq, sk, dim, docs)
+    need = _sizes.get(("h3qk_attention_workspace_bytes", dev.index, shape))
+    if need is None:
+        need = _size("h3qk_attention_workspace_bytes", dev, args(0, 0), key=shape)
+    ws = ws_bytes = 0
     if need:
         workspace, ws_bytes = _workspace(workspace, need, dev)
-        packed = args(workspace.data_ptr(), ws_bytes)
-    _call("h3qk_attention", dev, packed, _stream(stream, dev))
+        ws = workspace.data_ptr()
+    _call("h3qk_attention", dev, args(ws, ws_bytes), _stream(stream, dev))
     return out, lse
 
 

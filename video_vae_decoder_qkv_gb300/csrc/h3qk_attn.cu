@@ -78,17 +78,19 @@ bool use_split(const h3qk_attn& a)
     return a.docs == 0 && a.q_rows * (a.heads / a.kv_heads) <= kSplitRows;
 }
 
-// How the split kernel cuts the keys: enough chunks for six blocks an SM
-// over the whole call, but none under 128 keys (two turns of a block's four
-// warps) and none over 1,024 (uneven caches then still fill the SMs).
+// How the split kernel cuts the keys: into one block for each that the SMs
+// hold at once (4 an SM up to 64 channels, 2 beyond: their shared memory), over
+// the whole call, but into chunks of at least 128 keys (two turns of a block's
+// four warps) and at most 2,048 (uneven caches still fill the SMs).
 void split_of(const h3qk_attn& a, int32_t* splits, int32_t* chunk)
 {
     const int64_t rows = a.q_rows * (a.heads / a.kv_heads);
     const int64_t base = static_cast<int64_t>(a.batch) * a.kv_heads * ((rows + 15) / 16);
-    const int64_t want = (6 * static_cast<int64_t>(h3qk_internal_sm_count()) + base - 1) / base;
+    const int64_t slots = (a.head_dim <= 64 ? 4 : 2) * static_cast<int64_t>(h3qk_internal_sm_count());
+    const int64_t want = base < slots ? slots / base : 1;
     int64_t c = (a.kv_rows + want - 1) / want;
     c = (c + 63) / 64 * 64;
-    c = c < 128 ? 128 : c > 1024 ? 1024 : c;
+    c = c < 128 ? 128 : c > 2048 ? 2048 : c;
     // the grid's first dimension and the join's loop stay small
     while ((a.kv_rows + c - 1) / c > 4096) c *= 2;
     *chunk = static_cast<int32_t>(c);

@@ -7,12 +7,15 @@
 // the warps meet in shared memory once at the end.  A second, chained kernel
 // joins the chunks.
 //
-// K and V go from global memory straight into the fragments of the 16 x 8 x 16
-// product, 16 bytes a load, without shared memory: the contraction over
+// K and V go from global memory into the fragments of the 16 x 8 x 16
+// product, 16 bytes a load: the contraction over
 // channels may be taken in any order, so a lane's 8 neighbouring channels of
 // a key serve two steps if Q is held in the same order; and the columns of O
 // may come in any order, so a lane's 8 neighbouring channels of two keys
-// become (key, key + 1) pairs with one byte permute each.  The tensor work is
+// become (key, key + 1) pairs with one byte permute each.  The loads run ahead
+// as asynchronous copies; each lane copies just the 16-byte pieces it will use
+// itself, into slots of its own, so there is nothing to synchronise and no
+// bank conflict.  The tensor work is
 // a few percent of the load time, so the older warp-wide product does here;
 // tcgen05's 128 rows would be nearly empty.
 #include "h3qk_attn.cuh"
@@ -43,13 +46,13 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 load_once(const uint16_t* p)
+constexpr int kAhead = 3;  // turns of 16 keys a warp has in flight or in use
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint4* dst, const uint16_t* src, bool there)
 {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i)
@@ -74,7 +77,12 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
 {
     constexpr int NB = 2 * DH;
     constexpr float kShift = BF16 ? 0.0f : 7.0f;
-    __shared__ float sh_o[kWarps][kRows][64 * DH + 4];
+    // [warp][turn][piece][lane]: K 2 x NB pieces, V 4 x DH; at the end the warps' O
+    constexpr int kPieces = 2 * NB + 4 * DH;
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    auto& slots = *reinterpret_cast<uint4(*)[kWarps][kAhead][kPieces][32]>(dynamic);
+    float(*sh_o)[kRows][64 * DH + 4] = reinterpret_cast<float(*)[kRows][64 * DH + 4]>(slots);
+    static_assert(sizeof(slots) >= kWarps * kRows * (64 * DH + 4) * 4, "the warps' O fits the slots");
     __shared__ float sh_m[kWarps][kRows], sh_l[kWarps][kRows];
     h3qk_ops::allow_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -126,15 +134,15 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
             }
         const uint16_t* kp = p.k + s.item * p.ks.item + kv * p.ks.head + 8 * c;
         const uint16_t* vp = p.v + s.item * p.vs.item + kv * p.vs.head + 8 * g;
-        for (int j = k_first + 16 * warp; j < k_end; j += 16 * kWarps) {
-            uint4 kr[2][NB], vr[4][DH];
+        auto fetch = [&](int j, int turn) {
+            uint4(*to)[32] = slots[warp][turn];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int key = j + 8 * t + g;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    kr[t][b] = make_uint4(0, 0, 0, 0);
-                    if (key < k_end && 32 * b + 8 * c < p.dim) kr[t][b] = load_once(kp + key * p.ks.row + 32 * b);
+                    const bool there = key < k_end && 32 * b + 8 * c < p.dim;
+                    copy16(&to[t * NB + b][lane], there ? kp + key * p.ks.row + 32 * b : kp, there);
                 }
             }
 #pragma unroll
@@ -142,10 +150,33 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
                 const int key = j + 2 * c + (t & 1) + 8 * (t >> 1);
 #pragma unroll
                 for (int b = 0; b < DH; ++b) {
-                    vr[t][b] = make_uint4(0, 0, 0, 0);
-                    if (key < k_end && 64 * b + 8 * g < p.dim) vr[t][b] = load_once(vp + key * p.vs.row + 64 * b);
+                    const bool there = key < k_end && 64 * b + 8 * g < p.dim;
+                    copy16(&to[2 * NB + t * DH + b][lane], there ? vp + key * p.vs.row + 64 * b : vp, there);
                 }
             }
+        };
+        int j = k_first + 16 * warp;
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i) {
+            if (j + i * 16 * kWarps < k_end) fetch(j + i * 16 * kWarps, i);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int turn = 0;
+        for (; j < k_end; j += 16 * kWarps) {
+            const int next = j + (kAhead - 1) * 16 * kWarps;
+            if (next < k_end) fetch(next, turn == 0 ? kAhead - 1 : turn - 1);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            uint4 kr[2][NB], vr[4][DH];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) kr[t][b] = slots[warp][turn][t * NB + b][lane];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int b = 0; b < DH; ++b) vr[t][b] = slots[warp][turn][2 * NB + t * DH + b][lane];
+            turn = turn + 1 == kAhead ? 0 : turn + 1;
             float sc[2][4] = {};
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -214,6 +245,8 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
         }
     }
 
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
     // Join the block's warps.  Column n = 2c + e of product t of block b is
     // channel 64 b + 8 n + t.
 #pragma unroll
@@ -270,53 +303,68 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
     }
 }
 
-// One warp a row: the chunks' maxima and sums first, then their O, in order.
+// One block a row: each warp joins every fourth chunk, in order, then the
+// block joins its warps.
 template <bool BF16>
-__global__ void __launch_bounds__(128) join_split_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(32 * kWarps) join_split_kernel(const __grid_constant__ Params p)
 {
     constexpr float kShift = BF16 ? 0.0f : 7.0f;
-    h3qk_ops::wait_for_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    __shared__ float4 sh_v[kWarps][32];
+    __shared__ float sh_sum[kWarps], sh_top[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int all = p.group * p.q_rows;
     const int tiles = (all + kRows - 1) / kRows;
-    if (r >= static_cast<int64_t>(p.batch) * p.kv_heads * all) return;
-    const int t = static_cast<int>(r % all);
-    const int kv = static_cast<int>(r / all % p.kv_heads);
-    const int item = static_cast<int>(r / all / p.kv_heads);
-    const float* part = p.part + ((static_cast<int64_t>(item) * p.kv_heads + kv) * tiles + t / kRows) * p.splits *
-                                     part_floats(p.dim);
-    const int in = t % kRows;
-    auto stat = [&](int sp) {
-        return __ldcg(reinterpret_cast<const float2*>(part + sp * part_floats(p.dim) + kRows * p.dim + 2 * in));
-    };
+    const int t = static_cast<int>(blockIdx.x % all);
+    const int kv = static_cast<int>(blockIdx.x / all % p.kv_heads);
+    const int item = static_cast<int>(blockIdx.x / all / p.kv_heads);
+    const int64_t size = part_floats(p.dim);
+    const float* part = p.part + ((static_cast<int64_t>(item) * p.kv_heads + kv) * tiles + t / kRows) * p.splits * size;
+    const int in = t % kRows, d = 4 * lane;
+    h3qk_ops::wait_for_previous();
+    auto stat = [&](int sp) { return __ldcg(reinterpret_cast<const float2*>(part + sp * size + kRows * p.dim + 2 * in)); };
     float top = -INFINITY;
-    for (int sp = lane; sp < p.splits; sp += 32) top = fmaxf(top, stat(sp).x);
+    for (int sp = threadIdx.x; sp < p.splits; sp += 32 * kWarps) top = fmaxf(top, stat(sp).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh_top[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) top = fmaxf(top, sh_top[q]);
     float sum = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int d = 4 * lane;
-    for (int s0 = 0; s0 < p.splits; s0 += 32) {
+    for (int s0 = 0; s0 < p.splits; s0 += 32 * kWarps) {
+        const int mine_at = s0 + lane * kWarps + warp;
         float2 mine = make_float2(-INFINITY, 0.0f);
-        if (s0 + lane < p.splits) mine = stat(s0 + lane);
+        if (mine_at < p.splits) mine = stat(mine_at);
         // a chunk without visible keys left no O; a NaN sum is passed on
         const float f = mine.y == 0.0f ? 0.0f : exp2_fast(mine.x - top);
-        const int n = min(32, p.splits - s0);
-#pragma unroll 4
+        const int n = min(32, (p.splits - s0 - warp + kWarps - 1) / kWarps);
+#pragma unroll 8
         for (int i = 0; i < n; ++i) {
             const float fi = __shfl_sync(0xffffffffu, f, i);
             const float li = __shfl_sync(0xffffffffu, mine.y, i);
-            if (li == 0.0f) continue;
             sum = fmaf(li, fi, sum);
-            if (d < p.dim) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(part + (s0 + i) * part_floats(p.dim) + in * p.dim + d));
+            if (d < p.dim && li != 0.0f) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(part + (s0 + i * kWarps + warp) * size + in * p.dim + d));
                 v.x = fmaf(x.x, fi, v.x);
                 v.y = fmaf(x.y, fi, v.y);
                 v.z = fmaf(x.z, fi, v.z);
                 v.w = fmaf(x.w, fi, v.w);
             }
         }
+    }
+    sh_v[warp][lane] = v;
+    if (lane == 0) sh_sum[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int q = 1; q < kWarps; ++q) {
+        const float4 x = sh_v[q][lane];
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+        sum += sh_sum[q];
     }
     const int head = kv * p.group + t / p.q_rows, row = t % p.q_rows;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -329,19 +377,33 @@ __global__ void __launch_bounds__(128) join_split_kernel(const __grid_constant__
     if (lane == 0) finish_lse<BF16>(p, item, head, row, top, sum, kShift);
 }
 
+template <bool BF16, int DH>
+cudaError_t launch_split(const Params& p, dim3 grid, cudaStream_t st)
+{
+    constexpr int smem = kWarps * kAhead * 8 * DH * 512;
+    auto* kernel = attention_split_kernel<BF16, DH>;
+    static bool raised[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    if (!raised[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        raised[dev] = true;
+    }
+    kernel<<<grid, 32 * kWarps, smem, st>>>(p);
+    h3qk_internal_count_launch();
+    return cudaGetLastError();
+}
+
 template <bool BF16>
 cudaError_t launch(const Params& p, cudaStream_t st)
 {
     const int all = p.group * p.q_rows;
     const dim3 grid(p.splits, p.kv_heads * ((all + kRows - 1) / kRows), p.batch);
-    if (p.dim <= 64) attention_split_kernel<BF16, 1><<<grid, 32 * kWarps, 0, st>>>(p);
-    else attention_split_kernel<BF16, 2><<<grid, 32 * kWarps, 0, st>>>(p);
-    h3qk_internal_count_launch();
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = p.dim <= 64 ? launch_split<BF16, 1>(p, grid, st) : launch_split<BF16, 2>(p, grid, st);
     if (e != cudaSuccess || p.splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * all;
-    return h3qk_ops::launch_chained(join_split_kernel<BF16>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0,
-                                    st, p);
+    return h3qk_ops::launch_chained(join_split_kernel<BF16>, dim3(static_cast<unsigned>(rows)), dim3(32 * kWarps), 0, st, p);
 }
 
 }  // namespace

@@ -101,15 +101,21 @@ __global__ void __launch_bounds__(32 * kWarps, 2) prepare_backward_kernel(const 
         }
         const uint16_t* x = p.qkv + r * p.row_stride + 8 * c;
         const int64_t gbase = b * p.out_bstride + s * p.out_sstride + 8 * c;
-        for (int h = h0; h < h1; ++h) {
-            const int64_t go = gbase + h * p.out_hstride;
-            uint4 xv[2] = {}, gv[3] = {};
-            if (live) {
-                xv[0] = load_stream(x + h * D);
-                xv[1] = load_stream(x + HD + h * D);
+        // The next head's five loads are on their way while this one is computed.
+        uint4 nx[2] = {}, ng[3] = {};
+        auto fetch = [&](int h) {
+            if (live && h < h1) {
+                const int64_t go = gbase + h * p.out_hstride;
+                nx[0] = load_stream(x + h * D);
+                nx[1] = load_stream(x + HD + h * D);
 #pragma unroll
-                for (int t = 0; t < 3; ++t) gv[t] = load_stream(a.grad[t] + go);
+                for (int t = 0; t < 3; ++t) ng[t] = load_stream(a.grad[t] + go);
             }
+        };
+        fetch(h0);
+        for (int h = h0; h < h1; ++h) {
+            const uint4 xv[2] = {nx[0], nx[1]}, gv[3] = {ng[0], ng[1], ng[2]};
+            fetch(h + 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 float xf[8], dn[8];

@@ -3,10 +3,12 @@
 //   xh = (x - mean) rstd,  y = xh w + b
 //   g = dy w,  dx = rstd (g - mean(g) - xh mean(g xh)),  dw = sum_rows dy xh,  db = sum_rows dy
 //
-// Both directions are bound by HBM: each element is loaded once, held in
-// registers (16-bit elements packed) through both reductions, and written
-// once.  A row of up to 32 lanes' worth of elements belongs to one warp
-// (eight rows a block, shuffles only); a longer one to a block of its own.
+// Both directions are bound by HBM: each element crosses it once each way.
+// Rows come in asynchronously a few ahead of their use, since a row's two
+// reductions leave the memory idle otherwise.  A row of up to 512 columns
+// belongs to one warp (eight rows a block, shuffles only); a longer one to a
+// block of its own.  Blocks walk many rows with every thread on fixed
+// columns, so weights are read once and stay in registers.
 // The variance is the sum of squared deviations from the mean just found,
 // not E[x^2] - mean^2, which loses all digits where |mean| >> deviation.
 //
@@ -15,6 +17,9 @@
 // then writes one partial row and a second, chained kernel adds the partial
 // rows in a fixed order: no atomics, the same bits on every run.
 #include "h3qk_ops.cuh"
+#include "h3qk_tc.cuh"
+
+#include <type_traits>
 
 namespace {
 
@@ -27,69 +32,11 @@ using h3qk_detail::range_of;
 constexpr int kMaxWidth = 16384;  // 512 threads of 32 elements
 constexpr int kRowsPerBlock = 8;  // warp-per-row blocks
 
-// VEC neighbouring elements as stored, and as binary32.
-template <typename T, int VEC>
-struct Pack {
-    typename T::raw v[VEC];
-};
-
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load_pack(const typename T::raw* p)
-{
-    constexpr int bytes = sizeof(typename T::raw) * VEC;
-    Pack<T, VEC> r;
-    if constexpr (bytes == 16) {
-        *reinterpret_cast<uint4*>(r.v) = __ldg(reinterpret_cast<const uint4*>(p));
-    } else if constexpr (bytes == 8) {
-        *reinterpret_cast<uint2*>(r.v) = __ldg(reinterpret_cast<const uint2*>(p));
-    } else if constexpr (bytes == 4) {
-        *reinterpret_cast<uint32_t*>(r.v) = __ldg(reinterpret_cast<const uint32_t*>(p));
-    } else {
-        r.v[0] = __ldg(p);
-    }
-    return r;
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_pack(typename T::raw* p, const Pack<T, VEC>& r)
-{
-    constexpr int bytes = sizeof(typename T::raw) * VEC;
-    if constexpr (bytes == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
-    else if constexpr (bytes == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(r.v);
-    else if constexpr (bytes == 4) *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(r.v);
-    else p[0] = r.v[0];
-}
-
-template <typename T>
-__device__ __forceinline__ float widen(typename T::raw v)
-{
-    if constexpr (sizeof(v) == 4) return v;
-    else if constexpr (T::kBf16) return __uint_as_float(static_cast<uint32_t>(v) << 16);
-    else return __half2float(__ushort_as_half(v));
-}
-
-template <typename T>
-__device__ __forceinline__ typename T::raw narrow(float v)
-{
-    if constexpr (sizeof(typename T::raw) == 4) return v;
-    else if constexpr (T::kBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    else return __half_as_ushort(__float2half_rn(v));
-}
-
-template <int VEC>
-__device__ __forceinline__ void load_f32(float (&o)[VEC], const float* p)
-{
-    if constexpr (VEC % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) {
-            const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
-            o[4 * i] = f.x; o[4 * i + 1] = f.y; o[4 * i + 2] = f.z; o[4 * i + 3] = f.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = __ldg(p + i);
-    }
-}
+using h3qk_tc::add_pair;
+using h3qk_tc::fma_pair;
+using h3qk_tc::mul_pair;
+using h3qk_tc::pair;
+using h3qk_tc::unpair;
 
 struct LnArgs {
     const void* x;
@@ -106,196 +53,549 @@ struct LnArgs {
     float eps, inv_width;
 };
 
-// The sum of v over the threads of one row; `slot` alternates so that one
-// barrier per sum is enough.
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float v, float* red, int slot)
+// Two elements as stored.
+template <typename T>
+using Word = std::conditional_t<sizeof(typename T::raw) == 2, uint32_t, uint64_t>;
+
+// Two elements in binary32 (arithmetic is on such pairs: the packed
+// instructions round each half on its own).
+template <typename T>
+__device__ __forceinline__ uint64_t widen(Word<T> v)
 {
-    v = warp_sum(v);
-    if constexpr (!WARP) {
-        const int warps = blockDim.x >> 5;
-        float* r = red + 32 * slot;
-        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-        __syncthreads();
-        const int lane = threadIdx.x & 31;
-        v = warp_sum(lane < warps ? r[lane] : 0.0f);
+    if constexpr (sizeof(v) == 8) {
+        return v;
+    } else {
+        const float2 f = h3qk_tc::widen_pair<T::kBf16>(v);
+        return pair(f.x, f.y);
     }
-    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ Word<T> narrow(uint64_t v)
+{
+    if constexpr (sizeof(Word<T>) == 8) {
+        return v;
+    } else {
+        float lo, hi;
+        unpair(lo, hi, v);
+        return h3qk_tc::round_pair<T::kBf16>(lo, hi);
+    }
+}
+
+// What one thread holds of a row: CPT chunks of VEC neighbouring elements,
+// lanes * VEC columns apart, as pairs.  With single elements a pair is two chunks.
+template <typename T, int VEC, int CPT>
+struct Slice {
+    static constexpr int kElems = VEC * CPT, kPairs = kElems / 2;
+    static constexpr int kChunkBytes = VEC * static_cast<int>(sizeof(typename T::raw));
+    static_assert(kElems % 2 == 0, "elements go in pairs");
+    using Raw = typename T::raw;
+    int lanes, lane, width;
+
+    __device__ __forceinline__ int column(int e) const { return (e / VEC * lanes + lane) * VEC + e % VEC; }
+    __device__ __forceinline__ bool has(int k) const { return (k * lanes + lane) * VEC < width; }
+
+    static __device__ __forceinline__ void put(Word<T> (&w)[kPairs], int k, const uint4& v)
+    {
+        if constexpr (sizeof(Word<T>) == 4) {
+            w[4 * k] = v.x;
+            w[4 * k + 1] = v.y;
+            w[4 * k + 2] = v.z;
+            w[4 * k + 3] = v.w;
+        } else {
+            w[2 * k] = v.x | static_cast<uint64_t>(v.y) << 32;
+            w[2 * k + 1] = v.z | static_cast<uint64_t>(v.w) << 32;
+        }
+    }
+    static __device__ __forceinline__ void put_one(Word<T> (&w)[kPairs], int k, Raw v)
+    {
+        if constexpr (sizeof(Raw) == 2) w[k / 2] |= static_cast<Word<T>>(v) << (16 * (k & 1));
+        else w[k / 2] |= static_cast<Word<T>>(__float_as_uint(v)) << (32 * (k & 1));
+    }
+    __device__ __forceinline__ void store(Raw* row, const Word<T> (&w)[kPairs]) const
+    {
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+            if (!has(k)) continue;
+            Raw* p = row + (k * lanes + lane) * VEC;
+            if constexpr (kChunkBytes == 16) {
+                uint4 v;
+                if constexpr (sizeof(Word<T>) == 4)
+                    v = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                else
+                    v = make_uint4(static_cast<uint32_t>(w[2 * k]), static_cast<uint32_t>(w[2 * k] >> 32),
+                                   static_cast<uint32_t>(w[2 * k + 1]), static_cast<uint32_t>(w[2 * k + 1] >> 32));
+                *reinterpret_cast<uint4*>(p) = v;
+            } else if constexpr (VEC == 2) {
+                *reinterpret_cast<Word<T>*>(p) = w[k];
+            } else if constexpr (sizeof(Raw) == 2) {
+                *p = static_cast<Raw>(w[k / 2] >> (16 * (k & 1)));
+            } else {
+                *p = __uint_as_float(static_cast<uint32_t>(w[k / 2] >> (32 * (k & 1))));
+            }
+        }
+    }
+    // Values of a float vector at the thread's columns (`rest` past its end).
+    __device__ __forceinline__ void load_f32(uint64_t (&o)[kPairs], const float* v, float rest) const
+    {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            float f[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c = column(2 * e + q);
+                f[q] = c < width ? __ldg(v + c) : rest;
+            }
+            o[e] = pair(f[0], f[1]);
+        }
+    }
+    // v with zeros past the row.
+    __device__ __forceinline__ uint64_t inside(uint64_t v, int e) const
+    {
+        if constexpr (VEC >= 2) {
+            return has(2 * e / VEC) ? v : pair(0.0f, 0.0f);
+        } else {
+            float lo, hi;
+            unpair(lo, hi, v);
+            return pair(has(2 * e) ? lo : 0.0f, has(2 * e + 1) ? hi : 0.0f);
+        }
+    }
+};
+
+// Rows ahead of their use, in shared memory, filled by asynchronous copies: a
+// ring of kTurns turns of kRows rows (of TENSORS tensors).  Rows whose chunks
+// are 16 bytes: each thread copies exactly the bytes that it will read
+// itself, so its own wait for its copies is all it needs.  Others (COVER):
+// the row's threads copy the aligned 16-byte pieces that cover the row, and a
+// barrier comes before its elements are read at their own offset.
+template <typename T, int VEC, int CPT, int TENSORS>
+struct Ring {
+    using S = Slice<T, VEC, CPT>;
+    using Raw = typename T::raw;
+    static constexpr bool kCover = S::kChunkBytes != 16;
+    static constexpr int kThreadBytes = TENSORS * CPT * S::kChunkBytes;  // of one row
+    static constexpr int kRows = kThreadBytes <= 64 ? 2 : 1;
+    static constexpr int kTurns = kThreadBytes <= 64 ? 2 : kThreadBytes <= 128 ? 3 : 1;
+    static constexpr int kSlots = kRows * kTurns;
+    static int bytes(int threads, int rows_at_once, int width)
+    {
+        return kSlots * (kCover ? TENSORS * rows_at_once * cover_bytes(width) : kThreadBytes * threads);
+    }
+    static __host__ __device__ int cover_bytes(int width)
+    {
+        return (width * static_cast<int>(sizeof(Raw)) + 15) / 16 * 16 + 16;
+    }
+
+    uint8_t* slots;
+    int sub;  // COVER: which of the block's rows
+
+    __device__ __forceinline__ uint8_t* own(int slot, int tensor, int k) const
+    {
+        return slots + (((slot * TENSORS + tensor) * CPT + k) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) *
+                           S::kChunkBytes;
+    }
+    __device__ __forceinline__ uint8_t* cover(const S& s, int slot, int tensor) const
+    {
+        return slots + ((sub * kSlots + slot) * TENSORS + tensor) * cover_bytes(s.width);
+    }
+    // Starts copying the row at `from` (of the tensor that begins at `base`).
+    __device__ __forceinline__ void fetch(const S& s, int slot, int tensor, const Raw* base, const Raw* from) const
+    {
+        if constexpr (!kCover) {
+#pragma unroll
+            for (int k = 0; k < CPT; ++k)
+                if (s.has(k)) {
+                    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(own(slot, tensor, k)));
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from + (k * s.lanes + s.lane) * VEC)
+                                 : "memory");
+                }
+        } else {
+            uint8_t* to = cover(s, slot, tensor);
+            const uintptr_t first = reinterpret_cast<uintptr_t>(from) & ~uintptr_t{15};
+            const uintptr_t end = reinterpret_cast<uintptr_t>(from + s.width);
+            for (uintptr_t p = first + 16 * s.lane; p < end; p += 16 * s.lanes) {
+                uint8_t* dst = to + (p - first);
+                if (p >= reinterpret_cast<uintptr_t>(base)) {
+                    const int n = end - p < 16 ? static_cast<int>(end - p) : 16;  // no byte past the row
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                                 "l"(p), "r"(n)
+                                 : "memory");
+                } else {
+                    // the tensor begins inside this piece
+                    for (const Raw* q = base; q < from + s.width && reinterpret_cast<uintptr_t>(q) < p + 16; ++q)
+                        *reinterpret_cast<Raw*>(dst + (reinterpret_cast<uintptr_t>(q) - p)) = __ldg(q);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void read(const S& s, int slot, int tensor, const Raw* from, Word<T> (&w)[S::kPairs]) const
+    {
+#pragma unroll
+        for (int e = 0; e < S::kPairs; ++e) w[e] = 0;
+        const uint8_t* row = nullptr;
+        if constexpr (kCover) row = cover(s, slot, tensor) + (reinterpret_cast<uintptr_t>(from) & 15);
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+            if constexpr (!kCover) {
+                if (s.has(k)) S::put(w, k, *reinterpret_cast<const uint4*>(own(slot, tensor, k)));
+            } else {
+                // no branch around each element: one past the row reads the last and is dropped
+                const int at = k * s.lanes + s.lane, most = (s.width - 1) / VEC;
+                if constexpr (VEC == 2) {
+                    const Word<T> v = *(reinterpret_cast<const Word<T>*>(row) + min(at, most));
+                    w[k] = at <= most ? v : 0;
+                } else {
+                    const Raw v = *(reinterpret_cast<const Raw*>(row) + min(at, most));
+                    S::put_one(w, k, at <= most ? v : Raw(0));
+                }
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Moves a ring on by one turn: `fetch(place)` starts the copies of the next
+// turn to come into a place of the ring; afterwards the current turn can be read.
+template <typename R, bool WARP, typename F>
+__device__ __forceinline__ void next_turn(int place, F& fetch)
+{
+    auto sync = [] {
+        if constexpr (WARP) __syncwarp();
+        else __syncthreads();
+    };
+    const int last = place == 0 ? R::kTurns - 1 : place - 1;
+    if constexpr (!R::kCover) {
+        fetch(last);
+        copies_close();
+        copies_wait<R::kTurns - 1>();
+    } else if constexpr (R::kTurns == 1) {
+        sync();
+        fetch(0);
+        copies_close();
+        copies_wait<0>();
+        sync();
+    } else {
+        // others may still read the place that the new copies go to, until the barrier
+        copies_wait<R::kTurns - 2>();
+        sync();
+        fetch(last);
+        copies_close();
+    }
+}
+
+// Sums of N (1, 2 or 4) values over the threads of one row, for all of them.
+// Within a warp the values are dealt out over the lanes as they are added:
+// N = 4 takes 6 exchanges instead of 20.  Blocks: one barrier a call; `slot`
+// alternates between calls, so that no thread overwrites what another still
+// reads.
+template <bool WARP, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int slot)
+{
+    const int lane = threadIdx.x & 31;
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = v[i];
+    int own = 0;  // which value this lane ends up with
+#pragma unroll
+    for (int n = N, o = 16; o > 0; o >>= 1) {
+        if (n > 1) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < n / 2; ++i) {
+                const float keep = upper ? x[n / 2 + i] : x[i], give = upper ? x[i] : x[n / 2 + i];
+                x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+            n /= 2;
+            own = 2 * own + (upper ? 1 : 0);
+        } else {
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+        }
+    }
+    if constexpr (WARP) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x[0], i * (32 / N));
+    } else {
+        float* r = red + slot * 16 * N;
+        if ((lane & (32 / N - 1)) == 0) r[16 * own + (threadIdx.x >> 5)] = x[0];
+        __syncthreads();
+        // Every warp adds the 16 entries of each value (zero past the last
+        // warp), 32 / N lanes a value.
+        constexpr int kLanes = 32 / N, kEach = kLanes < 16 ? 16 / kLanes : 1;
+        float t = r[16 * (lane / kLanes) + (lane % kLanes % 16)];
+#pragma unroll
+        for (int e = 1; e < kEach; ++e) t += r[16 * (lane / kLanes) + lane % kLanes + e * kLanes];
+#pragma unroll
+        for (int o = kLanes < 16 ? kLanes / 2 : 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = N == 1 ? t : __shfl_sync(0xffffffffu, t, i * kLanes);
+    }
+}
+
+__device__ __forceinline__ float sum_of(uint64_t v)
+{
+    float lo, hi;
+    unpair(lo, hi, v);
+    return lo + hi;
+}
+
+// Threads that the registers must do for: a row takes 512 at most; at 16
+// elements a thread the bound of 640 keeps them under 97, for two blocks of
+// 320 threads an SM.
+template <int ELEMS>
+constexpr int kBound = ELEMS == 16 ? 640 : 512;
+
+template <typename S, bool WARP>
+__device__ __forceinline__ S make_slice(int width)
+{
+    return S{WARP ? 32 : static_cast<int>(blockDim.x),
+             WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x), width};
 }
 
 template <typename T, int VEC, int CPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kRowsPerBlock : 512) layer_norm_kernel(const LnArgs a)
+__global__ void __launch_bounds__(WARP ? 32 * kRowsPerBlock : kBound<VEC * CPT>) layer_norm_kernel(const LnArgs a)
 {
-    __shared__ float red[64];
-    const int lane = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int lanes = WARP ? 32 : blockDim.x;
+    using S = Slice<T, VEC, CPT>;
+    using R = Ring<T, VEC, CPT, 1>;
+    using Raw = typename T::raw;
+    constexpr int NP = S::kPairs, NR = R::kRows;
+    constexpr bool kHold = NP <= 8;  // weights stay in registers
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    __shared__ __align__(16) float red[64];
+    const S s = make_slice<S, WARP>(a.width);
     const int sub = WARP ? (threadIdx.x >> 5) : 0;
-    constexpr int kRows = WARP ? kRowsPerBlock : 1;
+    constexpr int kBlockRows = WARP ? kRowsPerBlock : 1;
+    if constexpr (!WARP) {
+        for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i] = 0.0f;
+        __syncthreads();
+    }
     const int64_t g = blockIdx.y;
     const float* w = a.weight ? a.weight + g * a.width : nullptr;
     const float* b = a.bias ? a.bias + g * a.width : nullptr;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + sub; r < a.rows_per_group;
-         r += static_cast<int64_t>(gridDim.x) * kRows) {
-        const int64_t row = g * a.rows_per_group + r;
-        const typename T::raw* x = static_cast<const typename T::raw*>(a.x) + row * a.x_stride;
-        Pack<T, VEC> xv[CPT];
-        float s = 0.0f;
+    const int step = static_cast<int>(gridDim.x) * kBlockRows;  // from one of the block's rows to its next
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kBlockRows + sub, first = g * a.rows_per_group + r0;
+    const int count = r0 < a.rows_per_group ? static_cast<int>((a.rows_per_group - r0 + step - 1) / step) : 0;
+    const R ring{dynamic, sub};
+    const Raw* x0 = static_cast<const Raw*>(a.x);
+    const Raw *to_fetch = x0 + first * a.x_stride, *to_read = to_fetch;
+    const int64_t x_step = step * a.x_stride, y_step = step * a.out_stride;
+    Raw* y = static_cast<Raw*>(a.out) + first * a.out_stride;
+    float2* stats = reinterpret_cast<float2*>(a.stats) + first;
+    int fetched = 0;
+    auto fetch = [&](int place) {
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            if (c < a.width) xv[k] = load_pack<T, VEC>(x + c);
-        }
+        for (int i = 0; i < NR; ++i, ++fetched, to_fetch += x_step)
+            if (fetched < count) ring.fetch(s, place * NR + i, 0, x0, to_fetch);
+    };
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            if (c < a.width)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) s += widen<T>(xv[k].v[i]);
-        }
-        const float mean = row_sum<WARP>(s, red, 0) * a.inv_width;
-        s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            if (c < a.width)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float d = widen<T>(xv[k].v[i]) - mean;
-                    s = fmaf(d, d, s);
-                }
-        }
-        const float var = row_sum<WARP>(s, red, 1) * a.inv_width;
-        const float rstd = 1.0f / sqrtf(var + a.eps);
-        if (lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
-        typename T::raw* y = static_cast<typename T::raw*>(a.out) + row * a.out_stride;
-#pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            if (c < a.width) {
-                float wv[VEC], bv[VEC];
-                if (w) load_f32<VEC>(wv, w + c);
-                if (b) load_f32<VEC>(bv, b + c);
-                Pack<T, VEC> o;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    float v = (widen<T>(xv[k].v[i]) - mean) * rstd;
-                    if (w) v *= wv[i];
-                    if (b) v += bv[i];
-                    o.v[i] = narrow<T>(v);
-                }
-                store_pack<T, VEC>(y + c, o);
-            }
-        }
+    for (int q = 0; q < R::kTurns - 1; ++q) {
+        fetch(q);
+        copies_close();
     }
+    uint64_t wv[NP], bv[NP];
+    const uint64_t zero = pair(0.0f, 0.0f), one = pair(1.0f, 1.0f);
+    auto affine = [&]() {
+        if (w) s.load_f32(wv, w, 0.0f);
+        if (b) s.load_f32(bv, b, 0.0f);
+    };
+    if constexpr (kHold) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) wv[e] = one, bv[e] = zero;
+        affine();
+    }
+    int place = 0;
+    for (int done = 0; done < count; done += NR) {
+        next_turn<R, WARP>(place, fetch);
+        Word<T> x[NR][NP];
+        float v[NR], mean[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i, to_read += x_step) {
+            ring.read(s, place * NR + i, 0, to_read, x[i]);
+            uint64_t t = zero;
+#pragma unroll
+            for (int e = 0; e < NP; ++e) t = add_pair(t, widen<T>(x[i][e]));
+            v[i] = sum_of(t);
+        }
+        row_sum<WARP>(v, red, 0);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            mean[i] = v[i] * a.inv_width;
+            const uint64_t nm = pair(-mean[i], -mean[i]);
+            uint64_t t = zero;
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const uint64_t d = s.inside(add_pair(widen<T>(x[i][e]), nm), e);
+                t = fma_pair(d, d, t);
+            }
+            v[i] = sum_of(t);
+        }
+        row_sum<WARP>(v, red, 1);
+        if constexpr (!kHold) affine();
+#pragma unroll
+        for (int i = 0; i < NR; ++i, y += y_step, stats += step) {
+            if (done + i >= count) break;
+            const float rstd = rsqrtf(fmaf(v[i], a.inv_width, a.eps));
+            const uint64_t nm = pair(-mean[i], -mean[i]), rs = pair(rstd, rstd);
+            if (s.lane == 0) *stats = make_float2(mean[i], rstd);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                uint64_t t = mul_pair(add_pair(widen<T>(x[i][e]), nm), rs);
+                if constexpr (kHold) {
+                    t = fma_pair(t, wv[e], bv[e]);
+                } else {
+                    if (w) t = mul_pair(t, wv[e]);
+                    if (b) t = add_pair(t, bv[e]);
+                }
+                x[i][e] = narrow<T>(t);
+            }
+            s.store(y, x[i]);
+        }
+        place = place + 1 == R::kTurns ? 0 : place + 1;
+    }
+    copies_wait<0>();
 }
 
+// x and dy are taken from the ring twice, for the sums and, once these are
+// known, for dx: that costs less than holding both in registers beside the
+// weight gradients.  dx = rstd (g - mean(g) - xh mean(g xh)) is evaluated as
+// dy (w rstd) + (x A + B).
 template <typename T, int VEC, int CPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kRowsPerBlock : 512) layer_norm_backward_kernel(const LnArgs a)
+__global__ void __launch_bounds__(WARP ? 32 * kRowsPerBlock : kBound<VEC * CPT>) layer_norm_backward_kernel(const LnArgs a)
 {
-    extern __shared__ float merge[];  // WARP: [kRowsPerBlock][width], one of dw / db at a time
-    __shared__ float red[128];
+    using S = Slice<T, VEC, CPT>;
+    using R = Ring<T, VEC, CPT, 2>;
+    using Raw = typename T::raw;
+    constexpr int NP = S::kPairs, NR = R::kRows;
+    constexpr bool kHold = NP <= 8;
+    extern __shared__ __align__(16) uint8_t dynamic[];  // the ring; then, WARP: [kRowsPerBlock][width] sums
+    __shared__ __align__(16) float red[128];
     allow_dependents();
-    const int lane = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int lanes = WARP ? 32 : blockDim.x;
+    const S s = make_slice<S, WARP>(a.width);
     const int sub = WARP ? (threadIdx.x >> 5) : 0;
-    constexpr int kRows = WARP ? kRowsPerBlock : 1;
+    constexpr int kBlockRows = WARP ? kRowsPerBlock : 1;
+    if constexpr (!WARP) {
+        for (int i = threadIdx.x; i < 128; i += blockDim.x) red[i] = 0.0f;
+        __syncthreads();
+    }
     const int64_t g = blockIdx.y;
     const float* w = a.weight ? a.weight + g * a.width : nullptr;
-    float dw[CPT][VEC], db[CPT][VEC];
+    const int step = static_cast<int>(gridDim.x) * kBlockRows;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kBlockRows + sub, first = g * a.rows_per_group + r0;
+    const int count = r0 < a.rows_per_group ? static_cast<int>((a.rows_per_group - r0 + step - 1) / step) : 0;
+    const R ring{dynamic, sub};
+    const Raw *x0 = static_cast<const Raw*>(a.x), *d0 = static_cast<const Raw*>(a.dy);
+    const Raw *x_fetch = x0 + first * a.x_stride, *d_fetch = d0 + first * a.dy_stride;
+    const Raw *x_read = x_fetch, *d_read = d_fetch;
+    const int64_t x_step = step * a.x_stride, d_step = step * a.dy_stride, o_step = step * a.out_stride;
+    Raw* dx = static_cast<Raw*>(a.out) + first * a.out_stride;
+    const float2* stats = reinterpret_cast<const float2*>(a.stats) + first;
+    int fetched = 0;
+    auto fetch = [&](int place) {
 #pragma unroll
-    for (int k = 0; k < CPT; ++k)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dw[k][i] = db[k][i] = 0.0f;
-
-    int slot = 0;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + sub; r < a.rows_per_group;
-         r += static_cast<int64_t>(gridDim.x) * kRows, slot ^= 2) {
-        const int64_t row = g * a.rows_per_group + r;
-        const typename T::raw* x = static_cast<const typename T::raw*>(a.x) + row * a.x_stride;
-        const typename T::raw* dy = static_cast<const typename T::raw*>(a.dy) + row * a.dy_stride;
-        Pack<T, VEC> xv[CPT], dv[CPT];
-#pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            if (c < a.width) {
-                xv[k] = load_pack<T, VEC>(x + c);
-                dv[k] = load_pack<T, VEC>(dy + c);
+        for (int i = 0; i < NR; ++i, ++fetched, x_fetch += x_step, d_fetch += d_step)
+            if (fetched < count) {
+                ring.fetch(s, place * NR + i, 0, x0, x_fetch);
+                ring.fetch(s, place * NR + i, 1, d0, d_fetch);
             }
-        }
-        const float2 st = __ldg(reinterpret_cast<const float2*>(a.stats + 2 * row));
-        float sg = 0.0f, sgx = 0.0f;
+    };
 #pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            if (c < a.width) {
-                float wv[VEC];
-                if (w) load_f32<VEC>(wv, w + c);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float d = widen<T>(dv[k].v[i]);
-                    const float xh = (widen<T>(xv[k].v[i]) - st.x) * st.y;
-                    const float gi = w ? d * wv[i] : d;
-                    sg += gi;
-                    sgx = fmaf(gi, xh, sgx);
-                    dw[k][i] = fmaf(d, xh, dw[k][i]);
-                    db[k][i] += d;
-                }
-            }
-        }
-        const float mg = row_sum<WARP>(sg, red, slot) * a.inv_width;
-        const float mgx = row_sum<WARP>(sgx, red, slot + 1) * a.inv_width;
-        typename T::raw* dx = static_cast<typename T::raw*>(a.out) + row * a.out_stride;
-#pragma unroll
-        for (int k = 0; k < CPT; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            if (c < a.width) {
-                float wv[VEC];
-                if (w) load_f32<VEC>(wv, w + c);
-                Pack<T, VEC> o;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float d = widen<T>(dv[k].v[i]);
-                    const float xh = (widen<T>(xv[k].v[i]) - st.x) * st.y;
-                    const float gi = w ? d * wv[i] : d;
-                    o.v[i] = narrow<T>(st.y * (gi - mg - xh * mgx));
-                }
-                store_pack<T, VEC>(dx + c, o);
-            }
-        }
+    for (int q = 0; q < R::kTurns - 1; ++q) {
+        fetch(q);
+        copies_close();
     }
+    const uint64_t zero = pair(0.0f, 0.0f), one = pair(1.0f, 1.0f);
+    uint64_t wv[NP], dw[NP], db[NP];
+#pragma unroll
+    for (int e = 0; e < NP; ++e) wv[e] = one, dw[e] = db[e] = zero;
+    if constexpr (kHold) {
+        if (w) s.load_f32(wv, w, 0.0f);
+    }
+    int place = 0, slot = 0;
+    for (int done = 0; done < count; done += NR, slot ^= 1) {
+        float2 st[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            if (done + i < count) st[i] = __ldg(stats + i * step);
+        next_turn<R, WARP>(place, fetch);
+        if constexpr (!kHold) {
+            if (w) s.load_f32(wv, w, 0.0f);
+        }
+        float v[2 * NR];
+        // Past the last row the ring holds an old one: not counted.
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            v[2 * i] = v[2 * i + 1] = 0.0f;
+            if (done + i >= count) break;
+            Word<T> x[NP], dy[NP];
+            ring.read(s, place * NR + i, 0, x_read + i * x_step, x);
+            ring.read(s, place * NR + i, 1, d_read + i * d_step, dy);
+            const uint64_t nm = pair(-st[i].x, -st[i].x), rs = pair(st[i].y, st[i].y);
+            uint64_t sg = zero, sgx = zero;
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const uint64_t d = widen<T>(dy[e]);
+                const uint64_t t = mul_pair(mul_pair(d, rs), add_pair(widen<T>(x[e]), nm));  // dy xh
+                dw[e] = add_pair(dw[e], t);
+                db[e] = add_pair(db[e], d);
+                sg = fma_pair(d, wv[e], sg);
+                sgx = fma_pair(t, wv[e], sgx);
+            }
+            v[2 * i] = sum_of(sg);
+            v[2 * i + 1] = sum_of(sgx);
+        }
+        row_sum<WARP>(v, red, slot);
+#pragma unroll
+        for (int i = 0; i < NR; ++i, dx += o_step, stats += step, x_read += x_step, d_read += d_step) {
+            if (done + i >= count) break;
+            Word<T> x[NP], dy[NP];
+            ring.read(s, place * NR + i, 0, x_read, x);
+            ring.read(s, place * NR + i, 1, d_read, dy);
+            const float mg = v[2 * i] * a.inv_width, mgx = v[2 * i + 1] * a.inv_width;
+            const float fa = -st[i].y * st[i].y * mgx, fb = -fmaf(fa, st[i].x, st[i].y * mg);
+            const uint64_t ca = pair(fa, fa), cb = pair(fb, fb), rs = pair(st[i].y, st[i].y);
+#pragma unroll
+            for (int e = 0; e < NP; ++e)
+                x[e] = narrow<T>(fma_pair(widen<T>(dy[e]), mul_pair(wv[e], rs), fma_pair(widen<T>(x[e]), ca, cb)));
+            s.store(dx, x);
+        }
+        place = place + 1 == R::kTurns ? 0 : place + 1;
+    }
+    copies_wait<0>();
     if (!a.partial) return;
     float* part = a.partial + (g * a.parts + blockIdx.x) * 2 * a.width;
-    if constexpr (WARP) {
-        // The block's eight warps hold sums of the same columns.
+    float* merge = reinterpret_cast<float*>(dynamic);
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            __syncthreads();
+    for (int which = 0; which < 2; ++which) {
+        if constexpr (WARP) __syncthreads();
 #pragma unroll
-            for (int k = 0; k < CPT; ++k)
+        for (int e = 0; e < NP; ++e) {
+            float f[2];
+            unpair(f[0], f[1], which ? db[e] : dw[e]);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int c = (k * lanes + lane) * VEC + i;
-                    if (c < a.width) merge[sub * a.width + c] = which ? db[k][i] : dw[k][i];
+            for (int q = 0; q < 2; ++q) {
+                const int c = s.column(2 * e + q);
+                if (c < a.width) {
+                    if constexpr (WARP) merge[sub * a.width + c] = f[q];
+                    else part[which * a.width + c] = f[q];
                 }
-            __syncthreads();
-            for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
-                float s = 0.0f;
-#pragma unroll
-                for (int q = 0; q < kRowsPerBlock; ++q) s += merge[q * a.width + c];
-                part[which * a.width + c] = s;
             }
         }
-    } else {
+        if constexpr (WARP) {
+            // The block's eight warps hold sums of the same columns.
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
+                float t = 0.0f;
 #pragma unroll
-        for (int k = 0; k < CPT; ++k)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int c = (k * lanes + lane) * VEC + i;
-                if (c < a.width) {
-                    part[c] = dw[k][i];
-                    part[a.width + c] = db[k][i];
-                }
+                for (int q = 0; q < kRowsPerBlock; ++q) t += merge[q * a.width + c];
+                part[which * a.width + c] = t;
             }
+        }
     }
 }
 
@@ -325,37 +625,31 @@ __global__ void sum_parts_kernel(const float* partial, float* grad_weight, float
 
 // How a row is spread: elements per load, loads per thread, threads per row.
 // 16-byte loads where the rows allow them, else pairs of 16-bit elements,
-// else single ones; up to 32 elements a thread (their two sums of the
-// backward pass take 64 registers), and never more than 512 threads a row.
+// else single ones; 16 elements a thread (their weights and both sums of the
+// backward pass stay in registers), 32 beyond 8,192 columns, so that a row
+// never takes more than 512 threads.
 struct Spread {
     int vec, cpt, lanes;
 };
 
 Spread spread_of(int esz, int64_t width, bool vec16, bool vec4)
 {
-    const int full = 16 / esz;
     Spread s;
-    if (vec16) {
-        s.vec = full;
-        s.cpt = width <= 32 * full ? 1 : width <= 64 * full ? 2 : (esz == 2 || width <= 8192) ? 4 : 8;
-    } else if (vec4 && esz == 2) {
-        s.vec = 2;
-        s.cpt = width <= 256 ? 4 : width <= 8192 ? 8 : 16;
-    } else {
-        s.vec = 1;
-        s.cpt = width <= 128 ? 4 : width <= 8192 ? 16 : 32;
-    }
-    const int64_t per = static_cast<int64_t>(s.vec) * s.cpt;
-    s.lanes = static_cast<int>(((width + per - 1) / per + 31) / 32 * 32);
+    s.vec = vec16 ? 16 / esz : vec4 && esz == 2 ? 2 : 1;
+    const int elems = width <= 256 ? 8 : width <= 8192 ? 16 : 32;
+    s.cpt = elems / s.vec;
+    s.lanes = static_cast<int>(((width + elems - 1) / elems + 31) / 32 * 32);
     return s;
 }
 
+// Blocks along a group's rows, backward: those that are resident at once
+// (about 640 threads an SM at 96 registers), fewer where a block would have
+// under four rows, for each block adds a partial row to the second kernel's work.
 int64_t parts_of(int64_t rows_per_group, int64_t groups, bool warp, int lanes)
 {
-    const int64_t per_block = warp ? kRowsPerBlock : 1;
+    const int64_t per_block = warp ? kRowsPerBlock : 4;
     const int64_t want = (rows_per_group + per_block - 1) / per_block;
-    // Resident blocks: about 512 threads an SM (128 registers a thread).
-    const int64_t per_sm = warp ? 2 : (lanes >= 512 ? 1 : 512 / lanes);
+    const int64_t per_sm = warp ? 2 : (lanes > 320 ? 1 : 640 / lanes);
     int64_t cap = h3qk_internal_sm_count() * per_sm / groups;
     if (cap < 1) cap = 1;
     return want < cap ? want : cap;
@@ -365,54 +659,68 @@ int64_t parts_of(int64_t rows_per_group, int64_t groups, bool warp, int lanes)
 // which is fixed before alignment is known).
 int64_t max_parts(int64_t rows_per_group, int64_t groups)
 {
-    int64_t cap = h3qk_internal_sm_count() * static_cast<int64_t>(8) / groups;
+    int64_t cap = h3qk_internal_sm_count() * static_cast<int64_t>(10) / groups;
     if (cap < 1) cap = 1;
     return rows_per_group < cap ? rows_per_group : cap;
+}
+
+template <typename K>
+cudaError_t launch_with(K* kernel, bool (&raised)[64], dim3 grid, int threads, int smem, const LnArgs& a, cudaStream_t st)
+{
+    if (smem > 48 * 1024) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+        if (!raised[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+            if (e != cudaSuccess) return e;
+            raised[dev] = true;
+        }
+    }
+    kernel<<<grid, threads, smem, st>>>(a);
+    h3qk_internal_count_launch();
+    return cudaGetLastError();
 }
 
 template <typename T, int VEC, int CPT, bool WARP>
 cudaError_t launch(bool backward, const LnArgs& a, int64_t groups, int lanes, cudaStream_t st)
 {
-    const int threads = WARP ? 32 * kRowsPerBlock : lanes;
+    static bool raised[2][64] = {};
+    const int threads = WARP ? 32 * kRowsPerBlock : lanes, rows_at_once = WARP ? kRowsPerBlock : 1;
     if (backward) {
         const dim3 grid(static_cast<unsigned>(a.parts), static_cast<unsigned>(groups));
-        const size_t smem = WARP && a.partial ? static_cast<size_t>(kRowsPerBlock) * a.width * 4 : 0;
-        layer_norm_backward_kernel<T, VEC, CPT, WARP><<<grid, threads, smem, st>>>(a);
-    } else {
-        const int64_t want = WARP ? (a.rows_per_group + kRowsPerBlock - 1) / kRowsPerBlock : a.rows_per_group;
-        const int64_t cap = h3qk_internal_sm_count() * static_cast<int64_t>(2048 / threads);
-        const dim3 grid(static_cast<unsigned>(want < cap ? want : cap), static_cast<unsigned>(groups));
-        layer_norm_kernel<T, VEC, CPT, WARP><<<grid, threads, 0, st>>>(a);
+        const int sums = WARP && a.partial ? kRowsPerBlock * a.width * 4 : 0;
+        const int ring = Ring<T, VEC, CPT, 2>::bytes(threads, rows_at_once, a.width);
+        return launch_with(layer_norm_backward_kernel<T, VEC, CPT, WARP>, raised[0], grid, threads,
+                           sums > ring ? sums : ring, a, st);
     }
-    h3qk_internal_count_launch();
-    return cudaGetLastError();
+    const int64_t want = WARP ? (a.rows_per_group + kRowsPerBlock - 1) / kRowsPerBlock : a.rows_per_group;
+    const int64_t per_sm = threads >= 1024 ? 1 : 1024 / threads;
+    int64_t cap = h3qk_internal_sm_count() * per_sm / groups;
+    if (cap < 1) cap = 1;
+    const dim3 grid(static_cast<unsigned>(want < cap ? want : cap), static_cast<unsigned>(groups));
+    return launch_with(layer_norm_kernel<T, VEC, CPT, WARP>, raised[1], grid, threads,
+                       Ring<T, VEC, CPT, 1>::bytes(threads, rows_at_once, a.width), a, st);
 }
 
-// Only the pairs that spread_of can choose are instantiated.
+// Only the spreads that spread_of can choose are instantiated: 8 elements a
+// thread for one warp, 16 for a warp or a block, 32 for a block.
+template <typename T, int VEC>
+cudaError_t dispatch_vec(bool back, const LnArgs& a, int64_t groups, const Spread& s, cudaStream_t st)
+{
+    const int elems = s.vec * s.cpt;
+    if (elems == 8) return launch<T, VEC, 8 / VEC, true>(back, a, groups, s.lanes, st);
+    if (elems == 32) return launch<T, VEC, 32 / VEC, false>(back, a, groups, s.lanes, st);
+    if (s.lanes == 32) return launch<T, VEC, 16 / VEC, true>(back, a, groups, s.lanes, st);
+    return launch<T, VEC, 16 / VEC, false>(back, a, groups, s.lanes, st);
+}
+
 template <typename T, int FULL>
 cudaError_t dispatch(bool back, const LnArgs& a, int64_t groups, const Spread& s, cudaStream_t st)
 {
-    const bool warp = s.lanes == 32;
-    if (s.vec == FULL) {
-        if (s.cpt == 1) return launch<T, FULL, 1, true>(back, a, groups, s.lanes, st);
-        if (s.cpt == 2) return launch<T, FULL, 2, true>(back, a, groups, s.lanes, st);
-        if constexpr (FULL == 4)
-            if (s.cpt == 8) return launch<T, FULL, 8, false>(back, a, groups, s.lanes, st);
-        if (warp) return launch<T, FULL, 4, true>(back, a, groups, s.lanes, st);
-        return launch<T, FULL, 4, false>(back, a, groups, s.lanes, st);
-    }
-    if constexpr (FULL == 8) {
-        if (s.vec == 2) {
-            if (s.cpt == 4) return launch<T, 2, 4, true>(back, a, groups, s.lanes, st);
-            if (s.cpt == 16) return launch<T, 2, 16, false>(back, a, groups, s.lanes, st);
-            if (warp) return launch<T, 2, 8, true>(back, a, groups, s.lanes, st);
-            return launch<T, 2, 8, false>(back, a, groups, s.lanes, st);
-        }
-    }
-    if (s.cpt == 4) return launch<T, 1, 4, true>(back, a, groups, s.lanes, st);
-    if (s.cpt == 32) return launch<T, 1, 32, false>(back, a, groups, s.lanes, st);
-    if (warp) return launch<T, 1, 16, true>(back, a, groups, s.lanes, st);
-    return launch<T, 1, 16, false>(back, a, groups, s.lanes, st);
+    if (s.vec == FULL) return dispatch_vec<T, FULL>(back, a, groups, s, st);
+    if constexpr (FULL == 8)
+        if (s.vec == 2) return dispatch_vec<T, 2>(back, a, groups, s, st);
+    return dispatch_vec<T, 1>(back, a, groups, s, st);
 }
 
 cudaError_t dispatch_type(bool backward, int dtype, const LnArgs& a, int64_t groups, const Spread& s, cudaStream_t st)
