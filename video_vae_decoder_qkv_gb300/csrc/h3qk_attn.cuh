@@ -125,30 +125,44 @@ inline int64_t tiles_of(const Params& p, int64_t rows, int size)
 }
 
 // A raw score q.k as a power of two's exponent: cap * tanh(scale q.k / cap) -
-// slope * distance, times log2(e).  tanh(x) = 1 - 2 / (2^(2 x log2 e) + 1)
-// from the hardware's 2^x and 1/x: absolute error below 2^-21, where the
-// hardware's own tanh has only 2^-11.
+// slope * distance, times log2(e).  With r = 1 / (2^(2 x log2 e) + 1),
+// tanh(x) = 1 - 2 r and 1 - tanh(x)^2 = 4 r (1 - r): the hardware's 2^x and
+// 1/x leave an absolute error below 2^-21, where its own tanh has 2^-11.
+// Which bends a call has is fixed at compile time.
+enum Bends { kPlain = 0, kCapped = 1, kSloped = 2 };
+
 struct Bend {
     float in;     // scale * 2 log2(e) / cap, or scale * log2(e) without a cap
     float cap;    // cap * log2(e)
     float slope;  // slope * log2(e)
-    bool capped;
 };
 
 __device__ __forceinline__ Bend bend_of(const Params& p, int head)
 {
     Bend b;
-    b.capped = p.cap > 0.0f;
-    b.in = b.capped ? p.scale * 2.0f * kLog2e / p.cap : p.scale * kLog2e;
+    b.in = p.cap > 0.0f ? p.scale * 2.0f * kLog2e / p.cap : p.scale * kLog2e;
     b.cap = p.cap * kLog2e;
     b.slope = p.slopes ? __ldg(p.slopes + head) * kLog2e : 0.0f;
     return b;
 }
 
-__device__ __forceinline__ float tanh_half(float x2)  // tanh(x) from 2 x log2(e)
+// The exponent of a pair of raw scores whose keys are `far` away; with
+// `keep`, also 1 - tanh^2 of a cap.
+template <int BENDS, bool KEEP>
+__device__ __forceinline__ uint64_t bend_pair(uint64_t z, const Bend& b, float far_lo, float far_hi, uint64_t* keep)
 {
-    const float e = h3qk_tc::exp2_fast(fminf(x2, 126.0f));
-    return fmaf(-2.0f, h3qk_tc::rcp_fast(e + 1.0f), 1.0f);
+    using namespace h3qk_tc;
+    z = mul_pair(z, pair(b.in, b.in));
+    if constexpr (BENDS & kCapped) {
+        float lo, hi;
+        unpair(lo, hi, z);
+        unpair(lo, hi, add_pair(pair(exp2_fast(lo), exp2_fast(hi)), pair(1.0f, 1.0f)));
+        const uint64_t r = pair(rcp_fast(lo), rcp_fast(hi));
+        z = fma_pair(r, pair(-2.0f * b.cap, -2.0f * b.cap), pair(b.cap, b.cap));
+        if constexpr (KEEP) *keep = mul_pair(r, fma_pair(r, pair(-4.0f, -4.0f), pair(4.0f, 4.0f)));
+    }
+    if constexpr (BENDS & kSloped) z = fma_pair(pair(fabsf(far_lo), fabsf(far_hi)), pair(-b.slope, -b.slope), z);
+    return z;
 }
 
 // Host side: the kernels' launchers.

@@ -149,7 +149,7 @@ __device__ __forceinline__ void drain_products(uint32_t bar)
 //   tensor unit   S0 dP0 | S1 dQ0 dP1 | S2 dQ1 dP2 | ...
 // S is double-buffered, so p of the next tile is computed while dQ and dP run.
 // ---------------------------------------------------------------------------
-template <bool BF16, int DP, bool BENT>
+template <bool BF16, int DP, int BENDS>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lim_first = h3qk_core::limit_of(s, p.causal, tile_row);
         const Bend bend = h3qk_core::bend_of(p, head);
         const float c = p.scale * h3qk_core::kLog2e;
+        const uint64_t cc = pair(c, c), nl = pair(-lse, -lse), nd = pair(-delta, -delta);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             ok = bar_wait(s_full + 8 * (j & 1), (j >> 1) & 1, stop);
@@ -322,25 +323,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float far = static_cast<float>(s.start + i_row - j * kTile - 64 * g);
             const bool edge = (j + 1) * kTile > lim_first;
             const int left = lim - j * kTile - 64 * g;
+            uint64_t pp[2][16];  // p, and with a cap p (1 - tanh^2)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float v = __uint_as_float(sr[b][e]);
-                    float pv;
-                    if constexpr (BENT) {
-                        v *= bend.in;
-                        float t = 0.0f;
-                        if (bend.capped) {
-                            t = h3qk_core::tanh_half(v);
-                            v = bend.cap * t;
-                        }
-                        v = fmaf(-bend.slope, fabsf(far - static_cast<float>(32 * b + e)), v);
-                        pv = exp2_fast(v - lse) * fmaf(-t, t, 1.0f);
+                for (int e = 0; e < 16; ++e) {
+                    const uint64_t z = pair(__uint_as_float(sr[b][2 * e]), __uint_as_float(sr[b][2 * e + 1]));
+                    float lo, hi;
+                    uint64_t keep;
+                    if constexpr (BENDS == h3qk_core::kPlain) {
+                        unpair(lo, hi, fma_pair(z, cc, nl));
                     } else {
-                        pv = exp2_fast(fmaf(v, c, -lse));
+                        const float at = far - static_cast<float>(32 * b + 2 * e);
+                        unpair(lo, hi, add_pair(h3qk_core::bend_pair<BENDS, true>(z, bend, at, at - 1.0f, &keep), nl));
                     }
-                    sr[b][e] = __float_as_uint(pv);
+                    pp[b][e] = pair(exp2_fast(lo), exp2_fast(hi));
+                    if constexpr (BENDS & h3qk_core::kCapped) pp[b][e] = mul_pair(pp[b][e], keep);
                 }
             ok = bar_wait(dp_full, j & 1, stop);
             if (!ok) break;
@@ -353,10 +351,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     float d[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        d[q] = __uint_as_float(sr[b][2 * e + q]) * (__uint_as_float(dp[2 * e + q]) - delta);
-                        if (edge && 32 * b + 2 * e + q >= left) d[q] = 0.0f;
+                    unpair(d[0], d[1],
+                           mul_pair(pp[b][e],
+                                    add_pair(pair(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd)));
+                    if (edge) {
+                        if (32 * b + 2 * e >= left) d[0] = 0.0f;
+                        if (32 * b + 2 * e + 1 >= left) d[1] = 0.0f;
                     }
                     w[e] = round_pair<BF16>(d[0], d[1]);
                 }
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (S = k q^T and dP = v dout^T: the keys are the lanes.)  p of the next tile
 // is computed while dK and dP run, ds while dV and S run.
 // ---------------------------------------------------------------------------
-template <bool BF16, int DP, bool BENT>
+template <bool BF16, int DP, int BENDS>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
@@ -477,22 +477,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_loads(full, kStages, issued);
         }
     } else if (warp == 10) {
-        // Statistics of each query tile: lse in powers of two (infinite where
-        // the row sees nothing or does not attend, so that p = 0), and delta.
-        for (int i = 0; i < n; ++i) {
-            float l[4], d[4];
+        // Statistics of each query tile: -lse in powers of two (-infinite where
+        // the row sees nothing or does not attend, so that p = 0), and -delta.
+        // A tile's loads are all in flight before the turn of the tile before it.
+        float l[4], d[4];
+        auto fetch = [&](int i) {
+            const float* lse = p.lse + (static_cast<int64_t>(s.item) * p.heads + head_of(i)) * p.q_rows + s.row0;
+            const float* delta = p.delta + (lse - p.lse);
+            const int r0 = row_of(i) + lane;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int r = row_of(i) + 32 * e + lane;
-                l[e] = INFINITY;
-                d[e] = 0.0f;
-                if (r < s.rows) {
-                    const int64_t at = (static_cast<int64_t>(s.item) * p.heads + head_of(i)) * p.q_rows + s.row0 + r;
-                    const float v = __ldg(p.lse + at);
-                    if (v != -INFINITY) l[e] = fmaf(v, h3qk_core::kLog2e, -kLift<BF16>);
-                    d[e] = __ldcg(p.delta + at) * kDrop<BF16>;
-                }
+                const int r = min(r0 + 32 * e, s.rows - 1);
+                l[e] = __ldg(lse + r);
+                d[e] = __ldcg(delta + r);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool there = r0 + 32 * e < s.rows;
+                l[e] = there && l[e] != -INFINITY ? fmaf(l[e], -h3qk_core::kLog2e, kLift<BF16>) : -INFINITY;
+                d[e] = there ? d[e] * -kDrop<BF16> : 0.0f;
+            }
+        };
+        if (n > 0) fetch(0);
+        for (int i = 0; i < n; ++i) {
             if (!bar_wait(st_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, stop)) break;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -501,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) bar_arrive(st_full + 8 * (i & 1));
+            if (i + 1 < n) fetch(i + 1);
             if (fix && i % per_head == per_head - 1) {
                 // The head's last tile: rows that do not attend are cleared, for
                 // dv and dk multiply p = ds = 0 with them.  The wait above says
@@ -565,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last_key = min(tile_key + kTile, s.keys) - 1;
         const int from_last = p.causal && last_key >= s.prefix ? last_key - s.start : -h3qk_core::kFar;
         const float c = p.scale * h3qk_core::kLog2e;
+        const uint64_t cc = pair(c, c), drop = pair(kDrop<BF16>, kDrop<BF16>);
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int row0 = row_of(i) + 64 * g;
@@ -572,45 +581,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = bar_wait(st_full + 8 * (i & 1), (i >> 1) & 1, stop) && bar_wait(s_full, i & 1, stop);
             if (!ok) break;
             tc_fence_after();
-            const float4* lse = reinterpret_cast<const float4*>(sh.lse[i & 1] + 64 * g);
-            const float4* del = reinterpret_cast<const float4*>(sh.delta[i & 1] + 64 * g);
+            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sh.lse[i & 1] + 64 * g);
+            const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sh.delta[i & 1] + 64 * g);
             uint32_t sr[2][32];
             tmem_ld32(sr[0], t_s + lanes + 64 * g);
             tmem_ld32(sr[1], t_s + lanes + 64 * g + 32);
             tmem_wait_ld(sr[0]);
             tmem_wait_ld(sr[1]);
             const bool edge = row_of(i) < from_last;
+            const int hidden = from - row0;  // queries of this half that do not see the key
             const float far = static_cast<float>(s.start + row0 - key);
+            uint64_t pp[2][16];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 uint32_t w[16];
 #pragma unroll
-                for (int e4 = 0; e4 < 8; ++e4) {
-                    const float4 l4 = lse[8 * b + e4];
-                    const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-                    float pv[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int e = 4 * e4 + q;
-                        float v = __uint_as_float(sr[b][e]);
-                        float keep = 1.0f;
-                        if constexpr (BENT) {
-                            v *= bend.in;
-                            if (bend.capped) {
-                                const float t = h3qk_core::tanh_half(v);
-                                v = bend.cap * t;
-                                keep = fmaf(-t, t, 1.0f);
-                            }
-                            v = fmaf(-bend.slope, fabsf(far + static_cast<float>(32 * b + e)), v);
-                            pv[q] = exp2_fast(v - lv[q]);
-                        } else {
-                            pv[q] = exp2_fast(fmaf(v, c, -lv[q]));
-                        }
-                        if (edge && row0 + 32 * b + e < from) pv[q] = 0.0f;
-                        sr[b][e] = __float_as_uint(BENT ? pv[q] * keep : pv[q]);
+                for (int e = 0; e < 16; ++e) {
+                    const ulonglong2 l2 = nl[(16 * b + e) >> 1];
+                    const uint64_t l = (e & 1) ? l2.y : l2.x;
+                    const uint64_t z = pair(__uint_as_float(sr[b][2 * e]), __uint_as_float(sr[b][2 * e + 1]));
+                    float lo, hi;
+                    uint64_t keep;
+                    if constexpr (BENDS == h3qk_core::kPlain) {
+                        unpair(lo, hi, fma_pair(z, cc, l));
+                    } else {
+                        const float at = far + static_cast<float>(32 * b + 2 * e);
+                        unpair(lo, hi, add_pair(h3qk_core::bend_pair<BENDS, true>(z, bend, at, at + 1.0f, &keep), l));
                     }
-                    w[2 * e4] = round_pair<BF16>(pv[0], pv[1]);
-                    w[2 * e4 + 1] = round_pair<BF16>(pv[2], pv[3]);
+                    lo = exp2_fast(lo);
+                    hi = exp2_fast(hi);
+                    if (edge) {
+                        if (32 * b + 2 * e < hidden) lo = 0.0f;
+                        if (32 * b + 2 * e + 1 < hidden) hi = 0.0f;
+                    }
+                    pp[b][e] = pair(lo, hi);
+                    w[e] = round_pair<BF16>(lo, hi);
+                    if constexpr (BENDS & h3qk_core::kCapped) pp[b][e] = mul_pair(pp[b][e], keep);
                 }
                 tmem_st16(t_s + lanes + 64 * g + 16 * b, w);
             }
@@ -627,16 +633,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(dp, t_dp + lanes + 64 * g + 32 * b);
                 tmem_wait_ld(dp);
 #pragma unroll
-                for (int e4 = 0; e4 < 8; ++e4) {
-                    const float4 d4 = del[8 * b + e4];
-                    const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
-                    float d[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        d[q] = __uint_as_float(sr[b][4 * e4 + q]) *
-                               fmaf(__uint_as_float(dp[4 * e4 + q]), kDrop<BF16>, -dv[q]);
-                    w[2 * e4] = round_pair<BF16>(d[0], d[1]);
-                    w[2 * e4 + 1] = round_pair<BF16>(d[2], d[3]);
+                for (int e = 0; e < 16; ++e) {
+                    const ulonglong2 d2 = nd[(16 * b + e) >> 1];
+                    const uint64_t d = (e & 1) ? d2.y : d2.x;
+                    uint64_t t = pair(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1]));
+                    if constexpr (BF16) t = add_pair(t, d);
+                    else t = fma_pair(t, drop, d);
+                    float lo, hi;
+                    unpair(lo, hi, mul_pair(pp[b][e], t));
+                    w[e] = round_pair<BF16>(lo, hi);
                 }
                 tmem_st16(t_dp + lanes + 64 * g + 16 * b, w);
             }
@@ -679,14 +684,14 @@ cudaError_t raise(K* kernel, int smem, bool (&raised)[64])
     return e;
 }
 
-template <bool BF16, int DP, bool BENT>
+template <bool BF16, int DP, int BENDS>
 cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
 {
     constexpr int smem = BwdShape<DP>::kTiles + static_cast<int>(sizeof(BwdShared));
     static_assert(smem <= 227 * 1024, "tiles and barriers exceed a block's shared memory");
     static bool raised[2][64] = {};
-    auto* dq = attention_dq_kernel<BF16, DP, BENT>;
-    auto* dkv = attention_dkv_kernel<BF16, DP, BENT>;
+    auto* dq = attention_dq_kernel<BF16, DP, BENDS>;
+    auto* dkv = attention_dkv_kernel<BF16, DP, BENDS>;
     cudaError_t e = raise(dq, smem, raised[0]);
     if (e == cudaSuccess) e = raise(dkv, smem, raised[1]);
     if (e != cudaSuccess) return e;
@@ -705,12 +710,18 @@ cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
     return e;
 }
 
+template <bool BF16, int DP>
+cudaError_t by_bends(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
+{
+    using namespace h3qk_core;
+    if (p.cap > 0.0f) return p.slopes ? launch<BF16, DP, kCapped | kSloped>(p, m, st) : launch<BF16, DP, kCapped>(p, m, st);
+    return p.slopes ? launch<BF16, DP, kSloped>(p, m, st) : launch<BF16, DP, kPlain>(p, m, st);
+}
+
 template <bool BF16>
 cudaError_t by_shape(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
 {
-    const bool bent = p.cap > 0.0f || p.slopes;
-    if (p.dim <= 64) return bent ? launch<BF16, 64, true>(p, m, st) : launch<BF16, 64, false>(p, m, st);
-    return bent ? launch<BF16, 128, true>(p, m, st) : launch<BF16, 128, false>(p, m, st);
+    return p.dim <= 64 ? by_bends<BF16, 64>(p, m, st) : by_bends<BF16, 128>(p, m, st);
 }
 
 }  // namespace

@@ -10,8 +10,10 @@
 // the other group computes its softmax:
 //   tensor unit   S0 S1 | O0 S0' O1 S1' | ...      (S = q k^T, O += p v)
 // P replaces S in TMEM (as 16-bit pairs) and is the product's A operand from
-// there; the tensor unit works in order, so S' may be issued behind the O
-// that reads P from the same columns.  O stays in TMEM; it is rescaled only
+// there; the tensor unit works in order, so a new S may be issued behind the O
+// that reads P from the same columns.  TMEM's 512 columns hold both O and two
+// S at head_dim 128; up to 64 they hold three S, which the groups' tiles take
+// in turn, so that a group finds its next S done when it has left its last P.  O stays in TMEM; it is rescaled only
 // when some row's maximum has grown by more than 2^8, otherwise the old
 // maximum serves on (p then reaches 2^8, far from any overflow; for fp16 all
 // p are kept 2^7 larger, so that flat rows do not fall into subnormals).
@@ -23,6 +25,8 @@
 // group against about 900 of softmax, which overlaps); at 64 by the
 // exponentials and the arithmetic around them.
 #include "h3qk_attn.cuh"
+
+#include <type_traits>
 
 namespace {
 
@@ -43,6 +47,8 @@ struct FwdShape {
     static constexpr int kBlocks = DP / 64;
     static constexpr int kTileBytes = kBlocks * kBlockBytes;
     static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kScores = DP == 128 ? 2 : 3;  // S buffers
+    static constexpr uint32_t kOut = 128 * kScores;    // first column of O
     static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
 };
 
@@ -54,7 +60,7 @@ struct FwdShared {
     int stop;
 };
 
-template <bool BF16, int DP, bool BENT>
+template <bool BF16, int DP, int BENDS>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p)
@@ -174,58 +180,70 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
             constexpr uint32_t shape_o = mma_shape(BF16, 128, DP, true);
             const int steps = (p.dim + 15) / 16;
-            auto scores = [&](int g, int i) {  // from K tile i of the ring
-                const uint64_t a = tile_desc(q_smem + g * Shape::kTileBytes, 16);
-                const uint64_t b = tile_desc(ring + (i % kStages) * Shape::kTileBytes, 16);
-                if (elect_lane()) {
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        if (k < steps) {
-                            constexpr int kStep = 32 >> 4, kNext = kBlockBytes >> 4;
-                            const uint32_t off = (k >> 2) * kNext + (k & 3) * kStep;
-                            mma_ss(tmem + g * 128, a + off, b + off, shape_s, k > 0);
-                        }
-                    mma_commit(s_full + 8 * g);
-                }
-                __syncwarp();
-            };
-            auto values = [&](int g, int i, bool add) {
-                const uint64_t b = tile_desc(ring + (i % kStages) * Shape::kTileBytes, kBlockBytes);
-                if (elect_lane()) {
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + 256 + g * DP, tmem + g * 128 + 8 * k, b + (k * 2048 >> 4), shape_o, add || k > 0);
-                    mma_commit(o_done + 8 * g);
-                }
-                __syncwarp();
-            };
             auto release = [&](int i) {
                 if (elect_lane()) mma_commit(empty + 8 * (i % kStages));
                 __syncwarp();
             };
             auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
-            bool ok = bar_wait(q_full, 0, stop) && loaded(0);
-            if (ok) {
-                for (int g = 0; g < 2; ++g)
-                    if (n[g] > 0) scores(g, 0);
-                release(0);
-            }
-            for (int j = 0; j < n_all && ok; ++j) {
-                const bool more = j + 1 < n_all;
-                ok = loaded(2 * j + 1) && (!more || loaded(2 * j + 2));
-                if (ok && fix && !more) ok = bar_wait(fixed, 0, stop);
+            auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
+            // The groups take turns, and the turns take the S buffers in turn.  Each
+            // tile is waited for in group 0's turn and released in group 1's, also
+            // where one of them does not use it.
+            uint32_t s_next = tmem, p_next = tmem;
+            auto move = [&](uint32_t& at) { at = at + 128 == tmem + Shape::kOut ? tmem : at + 128; };
+            auto scores = [&](auto group, int j) {
+                constexpr int g = decltype(group)::value;
+                if (j >= n_all) return true;
+                if (g == 0 && !loaded(2 * j)) return false;
+                if (j < n[g]) {
+                    const uint64_t a = tile_desc(q_smem + g * Shape::kTileBytes, 16), b = tile_desc(tile_at(2 * j), 16);
+                    if (elect_lane()) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (ok && j < n[g]) {
-                        ok = bar_wait(p_ready + 8 * g, j & 1, stop);
-                        tc_fence_after();
-                        if (ok) values(g, 2 * j + 1, j > 0);
+                        for (int k = 0; k < DP / 16; ++k)
+                            if (k < steps) {
+                                constexpr int kStep = 32 >> 4, kNext = kBlockBytes >> 4;
+                                const uint32_t off = (k >> 2) * kNext + (k & 3) * kStep;
+                                mma_ss(s_next, a + off, b + off, shape_s, k > 0);
+                            }
+                        mma_commit(s_full + 8 * g);
                     }
-                    if (ok && j + 1 < n[g]) scores(g, 2 * j + 2);
+                    __syncwarp();
                 }
-                if (!ok) break;
-                release(2 * j + 1);
-                if (more) release(2 * j + 2);
+                move(s_next);
+                if (g == 1) release(2 * j);
+                return true;
+            };
+            auto values = [&](auto group, int j) {
+                constexpr int g = decltype(group)::value;
+                if (g == 0 && !loaded(2 * j + 1)) return false;
+                if (g == 0 && fix && j + 1 == n_all && !bar_wait(fixed, 0, stop)) return false;
+                if (j < n[g]) {
+                    if (!bar_wait(p_ready + 8 * g, j & 1, stop)) return false;
+                    tc_fence_after();
+                    const uint64_t b = tile_desc(tile_at(2 * j + 1), kBlockBytes);
+                    const uint32_t d = tmem + Shape::kOut + g * DP;
+                    if (elect_lane()) {
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ts(d, p_next + 8 * k, b + (k * 2048 >> 4), shape_o, j > 0 || k > 0);
+                        mma_commit(o_done + 8 * g);
+                    }
+                    __syncwarp();
+                }
+                move(p_next);
+                if (g == 1) release(2 * j + 1);
+                return true;
+            };
+            const std::integral_constant<int, 0> g0;
+            const std::integral_constant<int, 1> g1;
+            bool ok = bar_wait(q_full, 0, stop) && scores(g0, 0) && scores(g1, 0);
+            if constexpr (Shape::kScores == 2) {
+                for (int j = 0; j < n_all && ok; ++j)
+                    ok = values(g0, j) && scores(g0, j + 1) && values(g1, j) && scores(g1, j + 1);
+            } else {
+                ok = ok && scores(g0, 1);
+                for (int j = 0; j < n_all && ok; ++j)
+                    ok = values(g0, j) && scores(g1, j + 1) && values(g1, j) && scores(g0, j + 2);
             }
             __syncwarp();
             if (*stop && elect_lane()) {
@@ -242,12 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = threadIdx.x & 127;
         const int i_row = tile_row + g * kTile + r;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_cols = tmem + g * 128 + lanes, o_cols = tmem + 256 + g * DP + lanes;
+        const uint32_t o_cols = tmem + Shape::kOut + g * DP + lanes;
         const int lim = h3qk_core::limit_of(s, p.causal, i_row);
         const int lim_first = h3qk_core::limit_of(s, p.causal, tile_row + g * kTile);
         const Bend bend = h3qk_core::bend_of(p, head);
         // Scores to powers of two: the bend gives exponents itself.
-        const float c = BENT ? 1.0f : p.scale * h3qk_core::kLog2e;
+        const float c = BENDS != h3qk_core::kPlain ? 1.0f : p.scale * h3qk_core::kLog2e;
         const uint64_t cc = pair(c, c);
         float m = -INFINITY;
         uint64_t sum2 = pair(0.0f, 0.0f);
@@ -256,21 +274,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = bar_wait(s_full + 8 * g, j & 1, stop);
             if (!ok) break;
             tc_fence_after();
+            const uint32_t s_cols = tmem + (2 * j + g) % Shape::kScores * 128 + lanes;
             uint32_t sr[4][32];
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_ld32(sr[b], s_cols + 32 * b);
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_wait_ld(sr[b]);
-            if constexpr (BENT) {
-                float far = static_cast<float>(s.start + i_row - j * kTile);
+            if constexpr (BENDS != h3qk_core::kPlain) {
+                const float far = static_cast<float>(s.start + i_row - j * kTile);
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float v = __uint_as_float(sr[b][e]) * bend.in;
-                        if (bend.capped) v = bend.cap * h3qk_core::tanh_half(v);
-                        v = fmaf(-bend.slope, fabsf(far - static_cast<float>(32 * b + e)), v);
-                        sr[b][e] = __float_as_uint(v);
+                    for (int e = 0; e < 32; e += 2) {
+                        float lo, hi;
+                        unpair(lo, hi,
+                               h3qk_core::bend_pair<BENDS, false>(
+                                   pair(__uint_as_float(sr[b][e]), __uint_as_float(sr[b][e + 1])), bend,
+                                   far - static_cast<float>(32 * b + e), far - static_cast<float>(32 * b + e + 1), nullptr));
+                        sr[b][e] = __float_as_uint(lo);
+                        sr[b][e + 1] = __float_as_uint(hi);
                     }
             }
             if ((j + 1) * kTile > lim_first) {
@@ -284,9 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mx[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                mx[b] = __uint_as_float(sr[b][0]);
+                mx[b] = fmaxf(__uint_as_float(sr[b][0]), __uint_as_float(sr[b][1]));
 #pragma unroll
-                for (int e = 1; e < 32; ++e) mx[b] = fmaxf(mx[b], __uint_as_float(sr[b][e]));
+                for (int e = 2; e < 32; e += 2) mx[b] = max3(mx[b], __uint_as_float(sr[b][e]), __uint_as_float(sr[b][e + 1]));
             }
             const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
             if (__any_sync(0xffffffffu, (top - m) * c > kSlack)) {
@@ -294,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float f = top == -INFINITY ? 1.0f : exp2_fast((m - top) * c);
                     const uint64_t ff = pair(f, f);
                     sum2 = mul_pair(sum2, ff);
+                    // (This S being done, all O but the last one are.)
                     ok = bar_wait(o_done + 8 * g, (j - 1) & 1, stop);
                     if (!ok) break;
                     tc_fence_after();
@@ -332,6 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(p_ready + 8 * g);
         }
+        // The last two O may both be under way: each is waited for in its turn.
+        if (ok && n[g] > 1) ok = bar_wait(o_done + 8 * g, (n[g] - 2) & 1, stop);
         if (ok && n[g] > 0) ok = bar_wait(o_done + 8 * g, (n[g] - 1) & 1, stop);
         tc_fence_after();
         float lo, hi;
@@ -380,11 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool BF16, int DP, bool BENT>
+template <bool BF16, int DP, int BENDS>
 cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
 {
     constexpr int smem = FwdShape<DP>::kSmem;
-    auto* kernel = attention_kernel<BF16, DP, BENT>;
+    auto* kernel = attention_kernel<BF16, DP, BENDS>;
     static bool raised[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
@@ -399,12 +424,18 @@ cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
     return cudaGetLastError();
 }
 
+template <bool BF16, int DP>
+cudaError_t by_bends(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
+{
+    using namespace h3qk_core;
+    if (p.cap > 0.0f) return p.slopes ? launch<BF16, DP, kCapped | kSloped>(p, m, st) : launch<BF16, DP, kCapped>(p, m, st);
+    return p.slopes ? launch<BF16, DP, kSloped>(p, m, st) : launch<BF16, DP, kPlain>(p, m, st);
+}
+
 template <bool BF16>
 cudaError_t by_shape(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
 {
-    const bool bent = p.cap > 0.0f || p.slopes;
-    if (p.dim <= 64) return bent ? launch<BF16, 64, true>(p, m, st) : launch<BF16, 64, false>(p, m, st);
-    return bent ? launch<BF16, 128, true>(p, m, st) : launch<BF16, 128, false>(p, m, st);
+    return p.dim <= 64 ? by_bends<BF16, 64>(p, m, st) : by_bends<BF16, 128>(p, m, st);
 }
 
 }  // namespace

@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
     h3qk_core::find_stretch(s, p, 0, blockIdx.z, 1, false);
     const int all = p.group * p.q_rows;
 
+    const bool capped = p.cap > 0.0f;
+
     // The two rows of this lane.
     int lim[2], head[2], row[2];
     bool has[2];
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
                     for (int e = 0; e < 2; ++e) {
                         const int key = j + 8 * t + 2 * c + e;
                         float v = sc[t][2 * h + e] * bend[h].in;
-                        if (bend[h].capped) v = bend[h].cap * h3qk_core::tanh_half(v);
+                        if (capped) v = fmaf(-2.0f * bend[h].cap, rcp_fast(exp2_fast(v) + 1.0f), bend[h].cap);
                         v = fmaf(-bend[h].slope, fabsf(far[h] - static_cast<float>(key)), v);
                         v = key < lim[h] ? v : -INFINITY;
                         sc[t][2 * h + e] = v;

@@ -257,6 +257,12 @@ __device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b)
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // Two values rounded to 16 bits, lo in the low half.
 template <bool BF16>
 __device__ __forceinline__ uint32_t round_pair(float lo, float hi)
