@@ -125,9 +125,14 @@ inline int64_t tiles_of(const Params& p, int64_t rows, int size)
 }
 
 // A raw score q.k as a power of two's exponent: cap * tanh(scale q.k / cap) -
-// slope * distance, times log2(e).  With r = 1 / (2^(2 x log2 e) + 1),
-// tanh(x) = 1 - 2 r and 1 - tanh(x)^2 = 4 r (1 - r): the hardware's 2^x and
-// 1/x leave an absolute error below 2^-21, where its own tanh has 2^-11.
+// slope * distance, times log2(e).  With e = 2^(-2 |x| log2 e),
+// tanh |x| = (1 - e) / (1 + e) and 1 - tanh^2 = 4 e / (1 + e)^2, to an
+// absolute 2^-20 (the hardware's own tanh has 2^-11).  The reciprocal of
+// y = 1 + e in [1, 2] is made of multiply-adds, two at a time: the hardware's
+// 1/x runs at half the rate of its 2^x and would bound the capped kernels.
+// p(y) = (1 - T3(2y - 3) / T3(-3)) / y, a polynomial of degree 2 with
+// |1 - y p| <= 1/99 on [1, 2] (T3: Chebyshev's), then p (1 + h + h^2) with
+// h = 1 - y p, which leaves h^3, about 2^-20.
 // Which bends a call has is fixed at compile time.
 enum Bends { kPlain = 0, kCapped = 1, kSloped = 2 };
 
@@ -154,12 +159,19 @@ __device__ __forceinline__ uint64_t bend_pair(uint64_t z, const Bend& b, float f
     using namespace h3qk_tc;
     z = mul_pair(z, pair(b.in, b.in));
     if constexpr (BENDS & kCapped) {
+        const uint64_t one = pair(1.0f, 1.0f);
         float lo, hi;
         unpair(lo, hi, z);
-        unpair(lo, hi, add_pair(pair(exp2_fast(lo), exp2_fast(hi)), pair(1.0f, 1.0f)));
-        const uint64_t r = pair(rcp_fast(lo), rcp_fast(hi));
-        z = fma_pair(r, pair(-2.0f * b.cap, -2.0f * b.cap), pair(b.cap, b.cap));
-        if constexpr (KEEP) *keep = mul_pair(r, fma_pair(r, pair(-4.0f, -4.0f), pair(4.0f, 4.0f)));
+        const uint64_t e = pair(exp2_fast(-fabsf(lo)), exp2_fast(-fabsf(hi)));
+        const uint64_t y = fma_pair(e, pair(-1.0f, -1.0f), pair(-1.0f, -1.0f));  // -(1 + e)
+        uint64_t r = fma_pair(fma_pair(y, pair(32.0f / 99.0f, 32.0f / 99.0f), pair(144.0f / 99.0f, 144.0f / 99.0f)), y,
+                              pair(210.0f / 99.0f, 210.0f / 99.0f));
+        const uint64_t h = fma_pair(y, r, one);
+        r = fma_pair(r, fma_pair(h, h, h), r);
+        if constexpr (KEEP) *keep = mul_pair(mul_pair(e, pair(4.0f, 4.0f)), mul_pair(r, r));
+        float t_lo, t_hi;
+        unpair(t_lo, t_hi, mul_pair(fma_pair(e, pair(-b.cap, -b.cap), pair(b.cap, b.cap)), r));
+        z = pair(copysignf(t_lo, lo), copysignf(t_hi, hi));
     }
     if constexpr (BENDS & kSloped) z = fma_pair(pair(fabsf(far_lo), fabsf(far_hi)), pair(-b.slope, -b.slope), z);
     return z;

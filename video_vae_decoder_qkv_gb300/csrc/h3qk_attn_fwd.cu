@@ -55,7 +55,7 @@ struct FwdShape {
 struct FwdShared {
     uint64_t full[8], empty[8];
     uint64_t q_full, fixed;
-    uint64_t s_full[2], p_ready[2], o_done[2], drain;
+    uint64_t s_full[2], p_ready[2], o_done[2], all_done[2], drain;
     uint32_t tmem;
     int stop;
 };
@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
     const uint32_t s_full = smem_addr(sh.s_full), p_ready = smem_addr(sh.p_ready), o_done = smem_addr(sh.o_done);
+    const uint32_t all_done = smem_addr(sh.all_done);  // the last O, which is waited for by its own barrier
     const uint32_t q_full = smem_addr(&sh.q_full), fixed = smem_addr(&sh.fixed);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(s_full + 8 * g, 1);
             bar_init(p_ready + 8 * g, 4);
             bar_init(o_done + 8 * g, 1);
+            bar_init(all_done + 8 * g, 1);
         }
         bar_init(q_full, 1);
         bar_init(fixed, 1);
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
                             mma_ts(d, p_next + 8 * k, b + (k * 2048 >> 4), shape_o, j > 0 || k > 0);
-                        mma_commit(o_done + 8 * g);
+                        mma_commit((j + 1 < n[g] ? o_done : all_done) + 8 * g);
                     }
                     __syncwarp();
                 }
@@ -355,9 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(p_ready + 8 * g);
         }
-        // The last two O may both be under way: each is waited for in its turn.
-        if (ok && n[g] > 1) ok = bar_wait(o_done + 8 * g, (n[g] - 2) & 1, stop);
-        if (ok && n[g] > 0) ok = bar_wait(o_done + 8 * g, (n[g] - 1) & 1, stop);
+        if (ok && n[g] > 0) ok = bar_wait(all_done + 8 * g, 0, stop);
         tc_fence_after();
         float lo, hi;
         unpair(lo, hi, sum2);
