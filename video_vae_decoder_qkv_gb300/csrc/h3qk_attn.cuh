@@ -125,14 +125,12 @@ inline int64_t tiles_of(const Params& p, int64_t rows, int size)
 }
 
 // A raw score q.k as a power of two's exponent: cap * tanh(scale q.k / cap) -
-// slope * distance, times log2(e).  With e = 2^(-2 |x| log2 e),
-// tanh |x| = (1 - e) / (1 + e) and 1 - tanh^2 = 4 e / (1 + e)^2, to an
-// absolute 2^-20 (the hardware's own tanh has 2^-11).  The reciprocal of
-// y = 1 + e in [1, 2] is made of multiply-adds, two at a time: the hardware's
-// 1/x runs at half the rate of its 2^x and would bound the capped kernels.
-// p(y) = (1 - T3(2y - 3) / T3(-3)) / y, a polynomial of degree 2 with
-// |1 - y p| <= 1/99 on [1, 2] (T3: Chebyshev's), then p (1 + h + h^2) with
-// h = 1 - y p, which leaves h^3, about 2^-20.
+// slope * distance, times log2(e).  With e = 2^(-2 |x| log2 e) and
+// y = 1 + e in [1, 2], tanh |x| = (1 - e) / y and 1 - tanh^2 = 4 e / y^2, to an
+// absolute 2^-21 (the hardware's own tanh has 2^-11).  Four scores share one
+// hardware reciprocal, of the product of their y (1/x has half the rate of
+// 2^x, 16 a cycle and SM, and would bound the capped kernels; a reciprocal
+// from multiply-adds measured slower).
 // Which bends a call has is fixed at compile time.
 enum Bends { kPlain = 0, kCapped = 1, kSloped = 2 };
 
@@ -151,30 +149,66 @@ __device__ __forceinline__ Bend bend_of(const Params& p, int head)
     return b;
 }
 
-// The exponent of a pair of raw scores whose keys are `far` away; with
-// `keep`, also 1 - tanh^2 of a cap.
+// The exponents of four raw scores (two pairs) at distances far, far + dir,
+// ...; with KEEP, also 1 - tanh^2 of a cap.
 template <int BENDS, bool KEEP>
-__device__ __forceinline__ uint64_t bend_pair(uint64_t z, const Bend& b, float far_lo, float far_hi, uint64_t* keep)
+__device__ __forceinline__ void bend_four(uint64_t (&z)[2], const Bend& b, float far, float dir, uint64_t (&keep)[2])
 {
     using namespace h3qk_tc;
-    z = mul_pair(z, pair(b.in, b.in));
+    const uint64_t in = pair(b.in, b.in);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) z[i] = mul_pair(z[i], in);
     if constexpr (BENDS & kCapped) {
-        const uint64_t one = pair(1.0f, 1.0f);
-        float lo, hi;
-        unpair(lo, hi, z);
-        const uint64_t e = pair(exp2_fast(-fabsf(lo)), exp2_fast(-fabsf(hi)));
-        const uint64_t y = fma_pair(e, pair(-1.0f, -1.0f), pair(-1.0f, -1.0f));  // -(1 + e)
-        uint64_t r = fma_pair(fma_pair(y, pair(32.0f / 99.0f, 32.0f / 99.0f), pair(144.0f / 99.0f, 144.0f / 99.0f)), y,
-                              pair(210.0f / 99.0f, 210.0f / 99.0f));
-        const uint64_t h = fma_pair(y, r, one);
-        r = fma_pair(r, fma_pair(h, h, h), r);
-        if constexpr (KEEP) *keep = mul_pair(mul_pair(e, pair(4.0f, 4.0f)), mul_pair(r, r));
-        float t_lo, t_hi;
-        unpair(t_lo, t_hi, mul_pair(fma_pair(e, pair(-b.cap, -b.cap), pair(b.cap, b.cap)), r));
-        z = pair(copysignf(t_lo, lo), copysignf(t_hi, hi));
+        const uint64_t one = pair(1.0f, 1.0f), cap = pair(b.cap, b.cap), less = pair(-b.cap, -b.cap);
+        float lo[2], hi[2];
+        uint64_t e[2], y[2], r[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            unpair(lo[i], hi[i], z[i]);
+            e[i] = pair(exp2_fast(-fabsf(lo[i])), exp2_fast(-fabsf(hi[i])));
+            y[i] = add_pair(e[i], one);
+        }
+        float p_lo, p_hi;
+        unpair(p_lo, p_hi, mul_pair(y[0], y[1]));
+        const float all = rcp_fast(p_lo * p_hi);
+        const uint64_t both = pair(all * p_hi, all * p_lo);  // 1 / (y[0] y[1])
+        r[0] = mul_pair(both, y[1]);
+        r[1] = mul_pair(both, y[0]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (KEEP) keep[i] = mul_pair(mul_pair(e[i], pair(4.0f, 4.0f)), mul_pair(r[i], r[i]));
+            float t_lo, t_hi;
+            unpair(t_lo, t_hi, mul_pair(fma_pair(e[i], less, cap), r[i]));
+            z[i] = pair(copysignf(t_lo, lo[i]), copysignf(t_hi, hi[i]));
+        }
     }
-    if constexpr (BENDS & kSloped) z = fma_pair(pair(fabsf(far_lo), fabsf(far_hi)), pair(-b.slope, -b.slope), z);
-    return z;
+    if constexpr (BENDS & kSloped) {
+        const uint64_t slope = pair(-b.slope, -b.slope);
+        z[0] = fma_pair(pair(fabsf(far), fabsf(far + dir)), slope, z[0]);
+        z[1] = fma_pair(pair(fabsf(far + 2.0f * dir), fabsf(far + 3.0f * dir)), slope, z[1]);
+    }
+}
+
+// Registers a thread of the tile kernels' 12 warps: 168 at launch, which the 8
+// warps of arithmetic and the 4 others then share out as 8 x 216 + 4 x 72 =
+// 12 x 168.
+constexpr int kLaunchRegs = 168, kMathRegs = 216, kOtherRegs = 72;
+
+// Once per kernel and device: its shared memory limit.  A kernel that was
+// launched with other than kLaunchRegs registers would wait for registers
+// that do not exist: refused.
+template <typename K>
+cudaError_t ready(K* kernel, int smem, bool (&done)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    if (done[dev]) return cudaSuccess;
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e == cudaSuccess && a.numRegs != kLaunchRegs) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    done[dev] = e == cudaSuccess;
+    return e;
 }
 
 // Host side: the kernels' launchers.

@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* stop = &sh.stop;
 
     if (warp == 9) {
+        regs_down<h3qk_core::kOtherRegs>();
         int issued = 0;
         if (lane == 0 && n > 0) {
             bar_expect(own, 2 * Shape::kTileBytes);
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_loads(full, kStages, issued);
         }
     } else if (warp == 8) {
+        regs_down<h3qk_core::kOtherRegs>();
         if (n > 0) {
             constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
             constexpr uint32_t shape_d = mma_shape(BF16, 128, DP, true);
@@ -273,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp < 8) {
+        regs_up<h3qk_core::kMathRegs>();
         const int g = warp >> 2, r = threadIdx.x & 127;
         const int i_row = tile_row + r;
         const bool has = i_row < s.rows;
@@ -327,18 +330,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint64_t z = pair(__uint_as_float(sr[b][2 * e]), __uint_as_float(sr[b][2 * e + 1]));
-                    float lo, hi;
-                    uint64_t keep;
-                    if constexpr (BENDS == h3qk_core::kPlain) {
-                        unpair(lo, hi, fma_pair(z, cc, nl));
-                    } else {
-                        const float at = far - static_cast<float>(32 * b + 2 * e);
-                        unpair(lo, hi, add_pair(h3qk_core::bend_pair<BENDS, true>(z, bend, at, at - 1.0f, &keep), nl));
+                for (int e = 0; e < 16; e += 2) {
+                    uint64_t z[2], keep[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        z[i] = pair(__uint_as_float(sr[b][2 * (e + i)]), __uint_as_float(sr[b][2 * (e + i) + 1]));
+                    if constexpr (BENDS != h3qk_core::kPlain)
+                        h3qk_core::bend_four<BENDS, true>(z, bend, far - static_cast<float>(32 * b + 2 * e), -1.0f, keep);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float lo, hi;
+                        unpair(lo, hi, BENDS == h3qk_core::kPlain ? fma_pair(z[i], cc, nl) : add_pair(z[i], nl));
+                        pp[b][e + i] = pair(exp2_fast(lo), exp2_fast(hi));
+                        if constexpr (BENDS & h3qk_core::kCapped) pp[b][e + i] = mul_pair(pp[b][e + i], keep[i]);
                     }
-                    pp[b][e] = pair(exp2_fast(lo), exp2_fast(hi));
-                    if constexpr (BENDS & h3qk_core::kCapped) pp[b][e] = mul_pair(pp[b][e], keep);
                 }
             ok = bar_wait(dp_full, j & 1, stop);
             if (!ok) break;
@@ -373,6 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         write_row<BF16, DP / 2>(dst, t_dq + lanes + g * (DP / 2), g * (DP / 2), p.dim, p.scale, !(ok && has && n > 0),
                                 i_row < s.span);
         tc_fence_before();
+    } else {
+        regs_down<h3qk_core::kOtherRegs>();
     }
     __syncthreads();
     if (threadIdx.x == 0 && *stop) atomicAdd(p.stuck, 1u);
@@ -456,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto row_of = [&](int i) { return (q_first + i % per_head) * kTile; };
 
     if (warp == 9) {
+        regs_down<h3qk_core::kOtherRegs>();
         int issued = 0;
         if (lane == 0 && n > 0) {
             bar_expect(own, 2 * Shape::kTileBytes);
@@ -477,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_loads(full, kStages, issued);
         }
     } else if (warp == 10) {
+        regs_down<h3qk_core::kOtherRegs>();
         // Statistics of each query tile: -lse in powers of two (-infinite where
         // the row sees nothing or does not attend, so that p = 0), and -delta.
         // A tile's loads are all in flight before the turn of the tile before it.
@@ -526,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 8) {
+        regs_down<h3qk_core::kOtherRegs>();
         if (n > 0) {
             constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
             constexpr uint32_t shape_d = mma_shape(BF16, 128, DP, true);
@@ -565,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp < 8) {
+        regs_up<h3qk_core::kMathRegs>();
         const int g = warp >> 2, r = threadIdx.x & 127;
         const int key = tile_key + r;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -596,27 +607,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < 2; ++b) {
                 uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 16; e += 2) {
                     const ulonglong2 l2 = nl[(16 * b + e) >> 1];
-                    const uint64_t l = (e & 1) ? l2.y : l2.x;
-                    const uint64_t z = pair(__uint_as_float(sr[b][2 * e]), __uint_as_float(sr[b][2 * e + 1]));
-                    float lo, hi;
-                    uint64_t keep;
-                    if constexpr (BENDS == h3qk_core::kPlain) {
-                        unpair(lo, hi, fma_pair(z, cc, l));
-                    } else {
-                        const float at = far + static_cast<float>(32 * b + 2 * e);
-                        unpair(lo, hi, add_pair(h3qk_core::bend_pair<BENDS, true>(z, bend, at, at + 1.0f, &keep), l));
+                    uint64_t z[2], keep[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        z[i] = pair(__uint_as_float(sr[b][2 * (e + i)]), __uint_as_float(sr[b][2 * (e + i) + 1]));
+                    if constexpr (BENDS != h3qk_core::kPlain)
+                        h3qk_core::bend_four<BENDS, true>(z, bend, far + static_cast<float>(32 * b + 2 * e), 1.0f, keep);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint64_t l = i ? l2.y : l2.x;
+                        float lo, hi;
+                        unpair(lo, hi, BENDS == h3qk_core::kPlain ? fma_pair(z[i], cc, l) : add_pair(z[i], l));
+                        lo = exp2_fast(lo);
+                        hi = exp2_fast(hi);
+                        if (edge) {
+                            if (32 * b + 2 * (e + i) < hidden) lo = 0.0f;
+                            if (32 * b + 2 * (e + i) + 1 < hidden) hi = 0.0f;
+                        }
+                        pp[b][e + i] = pair(lo, hi);
+                        w[e + i] = round_pair<BF16>(lo, hi);
+                        if constexpr (BENDS & h3qk_core::kCapped) pp[b][e + i] = mul_pair(pp[b][e + i], keep[i]);
                     }
-                    lo = exp2_fast(lo);
-                    hi = exp2_fast(hi);
-                    if (edge) {
-                        if (32 * b + 2 * e < hidden) lo = 0.0f;
-                        if (32 * b + 2 * e + 1 < hidden) hi = 0.0f;
-                    }
-                    pp[b][e] = pair(lo, hi);
-                    w[e] = round_pair<BF16>(lo, hi);
-                    if constexpr (BENDS & h3qk_core::kCapped) pp[b][e] = mul_pair(pp[b][e], keep);
                 }
                 tmem_st16(t_s + lanes + 64 * g + 16 * b, w);
             }
@@ -664,6 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             write_row<BF16, DP>(p.dk + s.item * p.dks.item + kv_head * p.dks.head + row * p.dks.row, t_dk + lanes, 0,
                                 p.dim, p.scale, zero, key < s.span);
         tc_fence_before();
+    } else {
+        regs_down<h3qk_core::kOtherRegs>();
     }
     __syncthreads();
     if (threadIdx.x == 0 && *stop) atomicAdd(p.stuck, 1u);
@@ -673,27 +688,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <typename K>
-cudaError_t raise(K* kernel, int smem, bool (&raised)[64])
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-    if (raised[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    raised[dev] = e == cudaSuccess;
-    return e;
-}
-
 template <bool BF16, int DP, int BENDS>
 cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
 {
     constexpr int smem = BwdShape<DP>::kTiles + static_cast<int>(sizeof(BwdShared));
     static_assert(smem <= 227 * 1024, "tiles and barriers exceed a block's shared memory");
-    static bool raised[2][64] = {};
+    static bool done[2][64] = {};
     auto* dq = attention_dq_kernel<BF16, DP, BENDS>;
     auto* dkv = attention_dkv_kernel<BF16, DP, BENDS>;
-    cudaError_t e = raise(dq, smem, raised[0]);
-    if (e == cudaSuccess) e = raise(dkv, smem, raised[1]);
+    cudaError_t e = h3qk_core::ready(dq, smem, done[0]);
+    if (e == cudaSuccess) e = h3qk_core::ready(dkv, smem, done[1]);
     if (e != cudaSuccess) return e;
     if (p.q_rows > 0) {
         const dim3 grid(static_cast<unsigned>(h3qk_core::tiles_of(p, p.q_rows, kTile)), p.heads, p.batch);

@@ -37,8 +37,6 @@ using h3qk_core::Stretch;
 
 constexpr int kTile = 128;             // rows of a group, keys of a tile
 constexpr int kThreads = 384;          // 2 x 4 softmax warps; products, loads, two idle
-// Registers a thread, from the 168 of the launch: 8 x 216 + 4 x 72 = 12 x 168.
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr float kSlack = 8.0f;         // log2: growth of the maximum that is tolerated
 constexpr int kBlockBytes = 128 * 128; // 64 columns of a tile
 
@@ -125,9 +123,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* stop = &sh.stop;
 
     if (warp > 9) {
-        regs_down<kOtherRegs>();
+        regs_down<h3qk_core::kOtherRegs>();
     } else if (warp == 9) {
-        regs_down<kOtherRegs>();
+        regs_down<h3qk_core::kOtherRegs>();
         // ---- tile loads: Q, then K and V tiles in turn ----------------------
         int issued = 0;
         bool ok = true;
@@ -176,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < kMaxTries && !bar_test(full + 8 * (i % kStages), (i / kStages) & 1); ++t) {}
         }
     } else if (warp == 8) {
-        regs_down<kOtherRegs>();
+        regs_down<h3qk_core::kOtherRegs>();
         // ---- matrix products ------------------------------------------------
         if (n_all > 0) {
             constexpr uint32_t shape_s = mma_shape(BF16, 128, kTile, false);
@@ -256,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        regs_up<kSoftmaxRegs>();
+        regs_up<h3qk_core::kMathRegs>();
         // ---- softmax: one thread a row --------------------------------------
         const int g = warp >> 2;
         const int r = threadIdx.x & 127;
@@ -287,14 +285,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float lo, hi;
-                        unpair(lo, hi,
-                               h3qk_core::bend_pair<BENDS, false>(
-                                   pair(__uint_as_float(sr[b][e]), __uint_as_float(sr[b][e + 1])), bend,
-                                   far - static_cast<float>(32 * b + e), far - static_cast<float>(32 * b + e + 1), nullptr));
-                        sr[b][e] = __float_as_uint(lo);
-                        sr[b][e + 1] = __float_as_uint(hi);
+                    for (int e = 0; e < 32; e += 4) {
+                        uint64_t z[2], keep[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            z[i] = pair(__uint_as_float(sr[b][e + 2 * i]), __uint_as_float(sr[b][e + 2 * i + 1]));
+                        h3qk_core::bend_four<BENDS, false>(z, bend, far - static_cast<float>(32 * b + e), -1.0f, keep);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float lo, hi;
+                            unpair(lo, hi, z[i]);
+                            sr[b][e + 2 * i] = __float_as_uint(lo);
+                            sr[b][e + 2 * i + 1] = __float_as_uint(hi);
+                        }
                     }
             }
             if ((j + 1) * kTile > lim_first) {
@@ -410,14 +413,9 @@ cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
 {
     constexpr int smem = FwdShape<DP>::kSmem;
     auto* kernel = attention_kernel<BF16, DP, BENDS>;
-    static bool raised[64] = {false};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-    if (!raised[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        raised[dev] = true;
-    }
+    static bool done[64] = {false};
+    const cudaError_t e = h3qk_core::ready(kernel, smem, done);
+    if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(h3qk_core::tiles_of(p, p.q_rows, 2 * kTile)), p.heads, p.batch);
     kernel<<<grid, kThreads, smem, st>>>(m.q, m.k, m.v, p);
     h3qk_internal_count_launch();
