@@ -281,7 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool has = i_row < s.rows;
         const int64_t row = s.row0 + i_row;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        // delta = dout . out of the row; each half of the warps takes every other 8 channels.
+        // delta = dout . out of the row; each half of the warps takes every other
+        // 8 channels.  (out is rounded to its type, which is most of dq's error
+        // on rows with a few heavy keys; the exact delta is known only after the
+        // loop, in time for dk and dv.)
         float part = 0.0f;
         if (has) {
             const uint16_t* o = p.out + s.item * p.os.item + head * p.os.head + row * p.os.row;
@@ -304,7 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t stat = (static_cast<int64_t>(s.item) * p.heads + head) * p.q_rows + row;
         float lse = INFINITY;  // p = 0
         if (has) {
-            if (g == 0) p.delta[stat] = delta;
             const float v = __ldg(p.lse + stat);
             if (v != -INFINITY) lse = v * h3qk_core::kLog2e;
         }
@@ -313,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Bend bend = h3qk_core::bend_of(p, head);
         const float c = p.scale * h3qk_core::kLog2e;
         const uint64_t cc = pair(c, c), nl = pair(-lse, -lse), nd = pair(-delta, -delta);
+        uint64_t exact = pair(0.0f, 0.0f);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             ok = bar_wait(s_full + 8 * (j & 1), (j >> 1) & 1, stop);
@@ -326,7 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float far = static_cast<float>(s.start + i_row - j * kTile - 64 * g);
             const bool edge = (j + 1) * kTile > lim_first;
             const int left = lim - j * kTile - 64 * g;
-            uint64_t pp[2][16];  // p, and with a cap p (1 - tanh^2)
+            uint64_t pp[2][16];                            // p
+            uint64_t kp[BENDS & h3qk_core::kCapped ? 2 : 1][16];  // and with a cap 1 - tanh^2
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -341,8 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 2; ++i) {
                         float lo, hi;
                         unpair(lo, hi, BENDS == h3qk_core::kPlain ? fma_pair(z[i], cc, nl) : add_pair(z[i], nl));
-                        pp[b][e + i] = pair(exp2_fast(lo), exp2_fast(hi));
-                        if constexpr (BENDS & h3qk_core::kCapped) pp[b][e + i] = mul_pair(pp[b][e + i], keep[i]);
+                        lo = exp2_fast(lo);
+                        hi = exp2_fast(hi);
+                        if (edge) {
+                            if (32 * b + 2 * (e + i) >= left) lo = 0.0f;
+                            if (32 * b + 2 * (e + i) + 1 >= left) hi = 0.0f;
+                        }
+                        pp[b][e + i] = pair(lo, hi);
+                        if constexpr (BENDS & h3qk_core::kCapped) kp[b][e + i] = keep[i];
                     }
                 }
             ok = bar_wait(dp_full, j & 1, stop);
@@ -355,15 +365,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_ld(dp);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    float d[2];
-                    unpair(d[0], d[1],
-                           mul_pair(pp[b][e],
-                                    add_pair(pair(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd)));
-                    if (edge) {
-                        if (32 * b + 2 * e >= left) d[0] = 0.0f;
-                        if (32 * b + 2 * e + 1 >= left) d[1] = 0.0f;
+                    float lo = __uint_as_float(dp[2 * e]), hi = __uint_as_float(dp[2 * e + 1]);
+                    if (edge) {  // values that the row does not see may be anything
+                        if (32 * b + 2 * e >= left) lo = 0.0f;
+                        if (32 * b + 2 * e + 1 >= left) hi = 0.0f;
                     }
-                    w[e] = round_pair<BF16>(d[0], d[1]);
+                    const uint64_t t = pair(lo, hi);
+                    exact = fma_pair(pp[b][e], t, exact);
+                    uint64_t d = mul_pair(pp[b][e], add_pair(t, nd));
+                    if constexpr (BENDS & h3qk_core::kCapped) d = mul_pair(d, kp[b][e]);
+                    unpair(lo, hi, d);
+                    w[e] = round_pair<BF16>(lo, hi);
                 }
                 tmem_st16(t_dp + lanes + 64 * g + 16 * b, w);
             }
@@ -374,6 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && n > 0) ok = bar_wait(done, 0, stop);
         tc_fence_after();
+        // delta = sum_j p dp without the rounding of out, for dk and dv.
+        float lo, hi;
+        unpair(lo, hi, exact);
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // all have read the first delta
+        sh.delta[g][r] = lo + hi;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (g == 0 && has) p.delta[stat] = sh.delta[0][r] + sh.delta[1][r];
         uint16_t* dst = p.dq + s.item * p.dqs.item + head * p.dqs.head + row * p.dqs.row;
         write_row<BF16, DP / 2>(dst, t_dq + lanes + g * (DP / 2), g * (DP / 2), p.dim, p.scale, !(ok && has && n > 0),
                                 i_row < s.span);
