@@ -16,6 +16,8 @@
 // destination's old contents.
 #include "h3qk_attn.cuh"
 
+#include <type_traits>
+
 namespace {
 
 using namespace h3qk_tc;
@@ -315,7 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Bend bend = h3qk_core::bend_of(p, head);
         const float c = p.scale * h3qk_core::kLog2e;
         const uint64_t cc = pair(c, c), nl = pair(-lse, -lse), nd = pair(-delta, -delta);
-        uint64_t exact = pair(0.0f, 0.0f);
+        uint64_t exact[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) exact[e] = pair(0.0f, 0.0f);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             ok = bar_wait(s_full + 8 * (j & 1), (j >> 1) & 1, stop);
@@ -331,54 +335,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int left = lim - j * kTile - 64 * g;
             uint64_t pp[2][16];                            // p
             uint64_t kp[BENDS & h3qk_core::kCapped ? 2 : 1][16];  // and with a cap 1 - tanh^2
+            // Tiles that some row sees only in part have their own code: the
+            // comparisons would cost every tile a third of its time.
+            auto probabilities = [&](auto at_edge) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    uint64_t z[2], keep[2];
+                    for (int e = 0; e < 16; e += 2) {
+                        uint64_t z[2], keep[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        z[i] = pair(__uint_as_float(sr[b][2 * (e + i)]), __uint_as_float(sr[b][2 * (e + i) + 1]));
-                    if constexpr (BENDS != h3qk_core::kPlain)
-                        h3qk_core::bend_four<BENDS, true>(z, bend, far - static_cast<float>(32 * b + 2 * e), -1.0f, keep);
+                        for (int i = 0; i < 2; ++i)
+                            z[i] = pair(__uint_as_float(sr[b][2 * (e + i)]), __uint_as_float(sr[b][2 * (e + i) + 1]));
+                        if constexpr (BENDS != h3qk_core::kPlain)
+                            h3qk_core::bend_four<BENDS, true>(z, bend, far - static_cast<float>(32 * b + 2 * e), -1.0f, keep);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float lo, hi;
-                        unpair(lo, hi, BENDS == h3qk_core::kPlain ? fma_pair(z[i], cc, nl) : add_pair(z[i], nl));
-                        lo = exp2_fast(lo);
-                        hi = exp2_fast(hi);
-                        if (edge) {
-                            if (32 * b + 2 * (e + i) >= left) lo = 0.0f;
-                            if (32 * b + 2 * (e + i) + 1 >= left) hi = 0.0f;
+                        for (int i = 0; i < 2; ++i) {
+                            float lo, hi;
+                            unpair(lo, hi, BENDS == h3qk_core::kPlain ? fma_pair(z[i], cc, nl) : add_pair(z[i], nl));
+                            lo = exp2_fast(lo);
+                            hi = exp2_fast(hi);
+                            if constexpr (decltype(at_edge)::value) {
+                                if (32 * b + 2 * (e + i) >= left) lo = 0.0f;
+                                if (32 * b + 2 * (e + i) + 1 >= left) hi = 0.0f;
+                            }
+                            pp[b][e + i] = pair(lo, hi);
+                            if constexpr (BENDS & h3qk_core::kCapped) kp[b][e + i] = keep[i];
                         }
-                        pp[b][e + i] = pair(lo, hi);
-                        if constexpr (BENDS & h3qk_core::kCapped) kp[b][e + i] = keep[i];
                     }
-                }
+            };
+            if (edge) probabilities(std::true_type{});
+            else probabilities(std::false_type{});
             ok = bar_wait(dp_full, j & 1, stop);
             if (!ok) break;
             tc_fence_after();
+            auto gradients = [&](auto at_edge) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t dp[32], w[16];
-                tmem_ld32(dp, t_dp + lanes + 64 * g + 32 * b);
-                tmem_wait_ld(dp);
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t dp[32], w[16];
+                    tmem_ld32(dp, t_dp + lanes + 64 * g + 32 * b);
+                    tmem_wait_ld(dp);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float lo = __uint_as_float(dp[2 * e]), hi = __uint_as_float(dp[2 * e + 1]);
-                    if (edge) {  // values that the row does not see may be anything
-                        if (32 * b + 2 * e >= left) lo = 0.0f;
-                        if (32 * b + 2 * e + 1 >= left) hi = 0.0f;
+                    for (int e = 0; e < 16; ++e) {
+                        float lo = __uint_as_float(dp[2 * e]), hi = __uint_as_float(dp[2 * e + 1]);
+                        if constexpr (decltype(at_edge)::value) {  // values that the row does not see may be anything
+                            if (32 * b + 2 * e >= left) lo = 0.0f;
+                            if (32 * b + 2 * e + 1 >= left) hi = 0.0f;
+                        }
+                        const uint64_t t = pair(lo, hi);
+                        exact[e & 3] = fma_pair(pp[b][e], t, exact[e & 3]);
+                        uint64_t d = mul_pair(pp[b][e], add_pair(t, nd));
+                        if constexpr (BENDS & h3qk_core::kCapped) d = mul_pair(d, kp[b][e]);
+                        unpair(lo, hi, d);
+                        w[e] = round_pair<BF16>(lo, hi);
                     }
-                    const uint64_t t = pair(lo, hi);
-                    exact = fma_pair(pp[b][e], t, exact);
-                    uint64_t d = mul_pair(pp[b][e], add_pair(t, nd));
-                    if constexpr (BENDS & h3qk_core::kCapped) d = mul_pair(d, kp[b][e]);
-                    unpair(lo, hi, d);
-                    w[e] = round_pair<BF16>(lo, hi);
+                    tmem_st16(t_dp + lanes + 64 * g + 16 * b, w);
                 }
-                tmem_st16(t_dp + lanes + 64 * g + 16 * b, w);
-            }
+            };
+            if (edge) gradients(std::true_type{});
+            else gradients(std::false_type{});
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // delta = sum_j p dp without the rounding of out, for dk and dv.
         float lo, hi;
-        unpair(lo, hi, exact);
+        unpair(lo, hi, add_pair(add_pair(exact[0], exact[1]), add_pair(exact[2], exact[3])));
         asm volatile("bar.sync 1, 256;" ::: "memory");  // all have read the first delta
         sh.delta[g][r] = lo + hi;
         asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -622,36 +636,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int hidden = from - row0;  // queries of this half that do not see the key
             const float far = static_cast<float>(s.start + row0 - key);
             uint64_t pp[2][16];
+            auto probabilities = [&](auto at_edge) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t w[16];
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const ulonglong2 l2 = nl[(16 * b + e) >> 1];
-                    uint64_t z[2], keep[2];
+                    for (int e = 0; e < 16; e += 2) {
+                        const ulonglong2 l2 = nl[(16 * b + e) >> 1];
+                        uint64_t z[2], keep[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        z[i] = pair(__uint_as_float(sr[b][2 * (e + i)]), __uint_as_float(sr[b][2 * (e + i) + 1]));
-                    if constexpr (BENDS != h3qk_core::kPlain)
-                        h3qk_core::bend_four<BENDS, true>(z, bend, far + static_cast<float>(32 * b + 2 * e), 1.0f, keep);
+                        for (int i = 0; i < 2; ++i)
+                            z[i] = pair(__uint_as_float(sr[b][2 * (e + i)]), __uint_as_float(sr[b][2 * (e + i) + 1]));
+                        if constexpr (BENDS != h3qk_core::kPlain)
+                            h3qk_core::bend_four<BENDS, true>(z, bend, far + static_cast<float>(32 * b + 2 * e), 1.0f, keep);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint64_t l = i ? l2.y : l2.x;
-                        float lo, hi;
-                        unpair(lo, hi, BENDS == h3qk_core::kPlain ? fma_pair(z[i], cc, l) : add_pair(z[i], l));
-                        lo = exp2_fast(lo);
-                        hi = exp2_fast(hi);
-                        if (edge) {
-                            if (32 * b + 2 * (e + i) < hidden) lo = 0.0f;
-                            if (32 * b + 2 * (e + i) + 1 < hidden) hi = 0.0f;
+                        for (int i = 0; i < 2; ++i) {
+                            const uint64_t l = i ? l2.y : l2.x;
+                            float lo, hi;
+                            unpair(lo, hi, BENDS == h3qk_core::kPlain ? fma_pair(z[i], cc, l) : add_pair(z[i], l));
+                            lo = exp2_fast(lo);
+                            hi = exp2_fast(hi);
+                            if constexpr (decltype(at_edge)::value) {
+                                if (32 * b + 2 * (e + i) < hidden) lo = 0.0f;
+                                if (32 * b + 2 * (e + i) + 1 < hidden) hi = 0.0f;
+                            }
+                            pp[b][e + i] = pair(lo, hi);
+                            w[e + i] = round_pair<BF16>(lo, hi);
+                            if constexpr (BENDS & h3qk_core::kCapped) pp[b][e + i] = mul_pair(pp[b][e + i], keep[i]);
                         }
-                        pp[b][e + i] = pair(lo, hi);
-                        w[e + i] = round_pair<BF16>(lo, hi);
-                        if constexpr (BENDS & h3qk_core::kCapped) pp[b][e + i] = mul_pair(pp[b][e + i], keep[i]);
                     }
+                    tmem_st16(t_s + lanes + 64 * g + 16 * b, w);
                 }
-                tmem_st16(t_s + lanes + 64 * g + 16 * b, w);
-            }
+            };
+            if (edge) probabilities(std::true_type{});
+            else probabilities(std::false_type{});
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
