@@ -40,7 +40,7 @@ struct BwdShape {
 struct BwdShared {
     uint64_t full[8], empty[8];
     uint64_t own, fixed[2], done, drain;
-    uint64_t s_full[2], dp_full, p_ready, ds_ready, st_full[2], st_empty[2];
+    uint64_t s_full[2], s_free[2], dp_full[2], p_ready[2], ds_ready[2], st_full[2], st_empty[2];
     uint32_t tmem;
     int stop;
     alignas(16) float lse[2][kTile];
@@ -147,9 +147,15 @@ __device__ __forceinline__ void drain_products(uint32_t bar)
 }
 
 // ---------------------------------------------------------------------------
-// dq: a block's 128 query rows against the keys they see.
+// dq: a block's 128 query rows against the keys they see.  S and dP take
+// three buffers of 128 columns.  Up to 64 channels the arithmetic bounds the
+// kernel, and it should always find its next operand done:
+//   tensor unit   S0 dP0 S1 | dP1 dQ0 S2 | dP2 dQ1 S3 | ...
+// dP of the next tile goes where S of this one was as soon as all warps have
+// it in registers, and the S after that where ds was once dQ has read it.
+// Beyond, the tensor unit bounds it, and fetching V a turn earlier only takes
+// room in the ring from the loads (12 % slower); there S alone is ahead:
 //   tensor unit   S0 dP0 | S1 dQ0 dP1 | S2 dQ1 dP2 | ...
-// S is double-buffered, so p of the next tile is computed while dQ and dP run.
 // ---------------------------------------------------------------------------
 template <bool BF16, int DP, int BENDS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -180,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool fix = n * kTile > seen && s.k0 + seen < p.kv_rows;
 
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty), own = smem_addr(&sh.own);
-    const uint32_t s_full = smem_addr(sh.s_full), dp_full = smem_addr(&sh.dp_full), ds_ready = smem_addr(&sh.ds_ready);
+    const uint32_t s_full = smem_addr(sh.s_full), s_free = smem_addr(sh.s_free), dp_full = smem_addr(sh.dp_full);
+    const uint32_t ds_ready = smem_addr(sh.ds_ready);
     const uint32_t fixed = smem_addr(sh.fixed), done = smem_addr(&sh.done);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -191,10 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) bar_init(fixed + 8 * i, 1);
         bar_init(done, 1);
         bar_init(smem_addr(&sh.drain), 1);
-        bar_init(s_full, 1);
-        bar_init(s_full + 8, 1);
-        bar_init(dp_full, 1);
-        bar_init(ds_ready, 8);
+        // Two of each, taken in turn: neither side can be two turns ahead.
+        for (int i = 0; i < 2; ++i) {
+            bar_init(s_full + 8 * i, 1);
+            bar_init(dp_full + 8 * i, 1);
+            bar_init(s_free + 8 * i, 8);
+            bar_init(ds_ready + 8 * i, 8);
+        }
         sh.stop = 0;
         bar_init_done();
     }
@@ -202,9 +212,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-    const uint32_t t_dp = tmem + 128, t_dq = tmem + 256;
-    auto t_s = [&](int j) { return tmem + ((j & 1) ? 384 : 0); };
+    // The block holds all of TMEM, so its first column is 0: a constant, which
+    // keeps the products' addresses in uniform registers.
+    constexpr uint32_t tmem = 0;
+    constexpr uint32_t t_dq = tmem + 384;
+    constexpr bool kAhead = DP == 64;
+    // Columns of a tile's S and dP and of the next tile's S; moved on from tile to tile.
+    struct Place {
+        uint32_t s = tmem, dp = tmem + 128, next = tmem + 256;
+        __device__ __forceinline__ void move()
+        {
+            const uint32_t t = next;
+            next = kAhead ? dp : s;
+            if (kAhead) dp = s;
+            s = t;
+        }
+    };
+    auto turn = [](uint32_t bar, int j) { return bar + 8 * (j & 1); };
+    auto phase = [](int j) { return static_cast<uint32_t>(j >> 1) & 1u; };
     volatile int* stop = &sh.stop;
 
     if (warp == 9) {
@@ -250,26 +275,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
             auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
             auto free = [&](int i) { return empty + 8 * (i % kStages); };
-            auto scores = [&](int j) {
+            auto scores = [&](int j, uint32_t to) {
                 if (!loaded(2 * j)) return false;
                 if (fix && j == n - 1 && !bar_wait(fixed, 0, stop)) return false;
-                product_rows<DP>(t_s(j), q_smem, tile_at(2 * j), steps, shape_s, s_full + 8 * (j & 1));
+                product_rows<DP>(to, q_smem, tile_at(2 * j), steps, shape_s, turn(s_full, j));
                 return true;
             };
-            auto dprobs = [&](int j) {
+            auto dprobs = [&](int j, uint32_t to) {
                 if (!loaded(2 * j + 1)) return false;
-                product_rows<DP>(t_dp, do_smem, tile_at(2 * j + 1), steps, shape_s, dp_full);
+                product_rows<DP>(to, do_smem, tile_at(2 * j + 1), steps, shape_s, turn(dp_full, j));
                 signal(free(2 * j + 1));
                 return true;
             };
-            bool ok = bar_wait(own, 0, stop) && scores(0) && dprobs(0);
-            for (int j = 0; j < n && ok; ++j) {
-                if (j + 1 < n) ok = scores(j + 1);
-                ok = ok && bar_wait(ds_ready, j & 1, stop);
+            Place at;
+            bool ok = bar_wait(own, 0, stop) && scores(0, at.s) && dprobs(0, at.dp) && (n < 2 || scores(1, at.next));
+            for (int j = 0; j < n && ok; ++j, at.move()) {
+                if (kAhead && j + 1 < n) {
+                    ok = bar_wait(turn(s_free, j), phase(j), stop);
+                    tc_fence_after();
+                    ok = ok && dprobs(j + 1, at.s);
+                }
+                ok = ok && bar_wait(turn(ds_ready, j), phase(j), stop);
                 if (!ok) break;
                 tc_fence_after();
-                product_sum(t_dq, t_dp, tile_at(2 * j), shape_d, j > 0, free(2 * j));
-                if (j + 1 < n) ok = dprobs(j + 1);
+                product_sum(t_dq, at.dp, tile_at(2 * j), shape_d, j > 0, free(2 * j));
+                if (!kAhead && j + 1 < n) ok = dprobs(j + 1, at.dp);
+                if (ok && j + 2 < n) ok = scores(j + 2, kAhead ? at.dp : at.s);
             }
             if (ok) signal(done);
             __syncwarp();
@@ -321,15 +352,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) exact[e] = pair(0.0f, 0.0f);
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            ok = bar_wait(s_full + 8 * (j & 1), (j >> 1) & 1, stop);
+        Place at;
+        for (int j = 0; j < n; ++j, at.move()) {
+            ok = bar_wait(turn(s_full, j), phase(j), stop);
             if (!ok) break;
             tc_fence_after();
             uint32_t sr[2][32];
-            tmem_ld32(sr[0], t_s(j) + lanes + 64 * g);
-            tmem_ld32(sr[1], t_s(j) + lanes + 64 * g + 32);
+            tmem_ld32(sr[0], at.s + lanes + 64 * g);
+            tmem_ld32(sr[1], at.s + lanes + 64 * g + 32);
             tmem_wait_ld(sr[0]);
             tmem_wait_ld(sr[1]);
+            if constexpr (kAhead) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(turn(s_free, j));
+            }
             const float far = static_cast<float>(s.start + i_row - j * kTile - 64 * g);
             const bool edge = (j + 1) * kTile > lim_first;
             const int left = lim - j * kTile - 64 * g;
@@ -342,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        uint64_t z[2], keep[2];
+                        uint64_t z[2];
+                    [[maybe_unused]] uint64_t keep[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             z[i] = pair(__uint_as_float(sr[b][2 * (e + i)]), __uint_as_float(sr[b][2 * (e + i) + 1]));
@@ -365,14 +403,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (edge) probabilities(std::true_type{});
             else probabilities(std::false_type{});
-            ok = bar_wait(dp_full, j & 1, stop);
+            ok = bar_wait(turn(dp_full, j), phase(j), stop);
             if (!ok) break;
             tc_fence_after();
             auto gradients = [&](auto at_edge) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     uint32_t dp[32], w[16];
-                    tmem_ld32(dp, t_dp + lanes + 64 * g + 32 * b);
+                    tmem_ld32(dp, at.dp + lanes + 64 * g + 32 * b);
                     tmem_wait_ld(dp);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -388,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         unpair(lo, hi, d);
                         w[e] = round_pair<BF16>(lo, hi);
                     }
-                    tmem_st16(t_dp + lanes + 64 * g + 16 * b, w);
+                    tmem_st16(at.dp + lanes + 64 * g + 16 * b, w);
                 }
             };
             if (edge) gradients(std::true_type{});
@@ -396,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(ds_ready);
+            if (lane == 0) bar_arrive(turn(ds_ready, j));
         }
         if (ok && n > 0) ok = bar_wait(done, 0, stop);
         tc_fence_after();
@@ -418,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *stop) atomicAdd(p.stuck, 1u);
     if (warp == 8) {
         tc_fence_after();
-        tmem_free(tmem, 512);
+        tmem_free(sh.tmem, 512);
     }
 }
 
@@ -461,8 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool fix = s.rows % kTile != 0 && s.row0 + s.rows < p.q_rows;
 
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty), own = smem_addr(&sh.own);
-    const uint32_t s_full = smem_addr(sh.s_full), dp_full = smem_addr(&sh.dp_full);
-    const uint32_t p_ready = smem_addr(&sh.p_ready), ds_ready = smem_addr(&sh.ds_ready);
+    const uint32_t s_full = smem_addr(sh.s_full), dp_full = smem_addr(sh.dp_full);
+    const uint32_t p_ready = smem_addr(sh.p_ready), ds_ready = smem_addr(sh.ds_ready);
     const uint32_t st_full = smem_addr(sh.st_full), st_empty = smem_addr(sh.st_empty);
     const uint32_t fixed = smem_addr(sh.fixed), done = smem_addr(&sh.done);
     if (threadIdx.x == 0) {
@@ -475,8 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(done, 1);
         bar_init(smem_addr(&sh.drain), 1);
         bar_init(s_full, 1);
+        bar_init(s_full + 8, 1);
         bar_init(dp_full, 1);
         bar_init(p_ready, 8);
+        bar_init(p_ready + 8, 8);
         bar_init(ds_ready, 8);
         for (int i = 0; i < 2; ++i) {
             bar_init(st_full + 8 * i, 1);
@@ -489,8 +529,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+    // The block holds all of TMEM, so its first column is 0: a constant, which
+    // keeps the products' addresses in uniform registers.
+    constexpr uint32_t tmem = 0;
+    // S is double-buffered where TMEM has the room (up to 64 channels): the next
+    // tile's S is then done before its turn.
+    constexpr int kScores = DP == 64 ? 2 : 1;
+    const uint32_t t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+    auto t_s = [&](int i) { return kScores == 2 && (i & 1) ? tmem + 384 : tmem; };
+    auto s_bar = [&](int i) { return s_full + 8 * (kScores == 2 ? i & 1 : 0); };
+    auto s_phase = [&](int i) { return static_cast<uint32_t>(kScores == 2 ? i >> 1 : i) & 1u; };
     volatile int* stop = &sh.stop;
     auto head_of = [&](int i) { return kv_head * p.group + i / per_head; };
     auto row_of = [&](int i) { return (q_first + i % per_head) * kTile; };
@@ -576,12 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto tile_at = [&](int i) { return ring + (i % kStages) * Shape::kTileBytes; };
             auto loaded = [&](int i) { return bar_wait(full + 8 * (i % kStages), (i / kStages) & 1, stop); };
             auto free = [&](int i) { return empty + 8 * (i % kStages); };
-            // The clearing warp is at most one head ahead: two barriers tell its turns apart.
+            // The clearing warp is never a head ahead of the next but one to be waited
+            // for: two barriers tell its turns apart.
             auto cleared = [&](int h) { return bar_wait(fixed + 8 * (h & 1), (h >> 1) & 1, stop); };
             auto scores = [&](int i) {
                 if (!loaded(2 * i)) return false;
                 if (fix && i % per_head == per_head - 1 && !cleared(i / per_head)) return false;
-                product_rows<DP>(t_s, k_smem, tile_at(2 * i), steps, shape_s, s_full);
+                product_rows<DP>(t_s(i), k_smem, tile_at(2 * i), steps, shape_s, s_bar(i));
                 return true;
             };
             auto dprobs = [&](int i) {
@@ -589,13 +638,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 product_rows<DP>(t_dp, v_smem, tile_at(2 * i + 1), steps, shape_s, dp_full);
                 return true;
             };
-            bool ok = bar_wait(own, 0, stop) && scores(0) && dprobs(0);
+            bool ok = bar_wait(own, 0, stop) && scores(0) && dprobs(0) && (kScores == 1 || n < 2 || scores(1));
             for (int i = 0; i < n && ok; ++i) {
-                ok = bar_wait(p_ready, i & 1, stop);
+                ok = bar_wait(p_ready + 8 * (i & 1), (i >> 1) & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
-                product_sum(t_dv, t_s, tile_at(2 * i + 1), shape_d, i > 0, free(2 * i + 1));
-                if (i + 1 < n) ok = scores(i + 1);
+                product_sum(t_dv, t_s(i), tile_at(2 * i + 1), shape_d, i > 0, free(2 * i + 1));
+                if (i + kScores < n) ok = scores(i + kScores);
                 ok = ok && bar_wait(ds_ready, i & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
@@ -622,14 +671,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i) {
             const int row0 = row_of(i) + 64 * g;
             const Bend bend = h3qk_core::bend_of(p, head_of(i));
-            ok = bar_wait(st_full + 8 * (i & 1), (i >> 1) & 1, stop) && bar_wait(s_full, i & 1, stop);
+            ok = bar_wait(st_full + 8 * (i & 1), (i >> 1) & 1, stop) && bar_wait(s_bar(i), s_phase(i), stop);
             if (!ok) break;
             tc_fence_after();
             const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sh.lse[i & 1] + 64 * g);
             const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sh.delta[i & 1] + 64 * g);
             uint32_t sr[2][32];
-            tmem_ld32(sr[0], t_s + lanes + 64 * g);
-            tmem_ld32(sr[1], t_s + lanes + 64 * g + 32);
+            tmem_ld32(sr[0], t_s(i) + lanes + 64 * g);
+            tmem_ld32(sr[1], t_s(i) + lanes + 64 * g + 32);
             tmem_wait_ld(sr[0]);
             tmem_wait_ld(sr[1]);
             const bool edge = row_of(i) < from_last;
@@ -643,7 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         const ulonglong2 l2 = nl[(16 * b + e) >> 1];
-                        uint64_t z[2], keep[2];
+                        uint64_t z[2];
+                    [[maybe_unused]] uint64_t keep[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             z[i] = pair(__uint_as_float(sr[b][2 * (e + i)]), __uint_as_float(sr[b][2 * (e + i) + 1]));
@@ -665,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (BENDS & h3qk_core::kCapped) pp[b][e + i] = mul_pair(pp[b][e + i], keep[i]);
                         }
                     }
-                    tmem_st16(t_s + lanes + 64 * g + 16 * b, w);
+                    tmem_st16(t_s(i) + lanes + 64 * g + 16 * b, w);
                 }
             };
             if (edge) probabilities(std::true_type{});
@@ -673,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(p_ready);
+            if (lane == 0) bar_arrive(p_ready + 8 * (i & 1));
             ok = bar_wait(dp_full, i & 1, stop);
             if (!ok) break;
             tc_fence_after();
@@ -721,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *stop) atomicAdd(p.stuck, 1u);
     if (warp == 8) {
         tc_fence_after();
-        tmem_free(tmem, 512);
+        tmem_free(sh.tmem, 512);
     }
 }
 

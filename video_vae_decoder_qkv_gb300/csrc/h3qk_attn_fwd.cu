@@ -53,7 +53,7 @@ struct FwdShape {
 struct FwdShared {
     uint64_t full[8], empty[8];
     uint64_t q_full, fixed;
-    uint64_t s_full[2], p_ready[2], o_done[2], all_done[2], drain;
+    uint64_t s_full[4], p_ready[4], o_done[2], all_done[2], drain;
     uint32_t tmem;
     int stop;
 };
@@ -104,8 +104,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(empty + 8 * i, 1);
         }
         for (int g = 0; g < 2; ++g) {
-            bar_init(s_full + 8 * g, 1);
-            bar_init(p_ready + 8 * g, 4);
+            // Two of these for each group, taken in turn by its tiles: with S done
+            // ahead, one side may come to a phase before the other has left the last.
+            for (int i = 0; i < 2; ++i) {
+                bar_init(s_full + 8 * (2 * g + i), 1);
+                bar_init(p_ready + 8 * (2 * g + i), 4);
+            }
             bar_init(o_done + 8 * g, 1);
             bar_init(all_done + 8 * g, 1);
         }
@@ -119,8 +123,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    // The block holds all of TMEM, so its first column is 0: a constant, which
+    // keeps the products' addresses in uniform registers.
+    constexpr uint32_t tmem = 0;
     volatile int* stop = &sh.stop;
+    auto turn = [](uint32_t bar, int g, int j) { return bar + 8 * (2 * g + (j & 1)); };
+    auto phase = [](int j) { return static_cast<uint32_t>(j >> 1) & 1u; };
 
     if (warp > 9) {
         regs_down<h3qk_core::kOtherRegs>();
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint32_t off = (k >> 2) * kNext + (k & 3) * kStep;
                                 mma_ss(s_next, a + off, b + off, shape_s, k > 0);
                             }
-                        mma_commit(s_full + 8 * g);
+                        mma_commit(turn(s_full, g, j));
                     }
                     __syncwarp();
                 }
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (g == 0 && !loaded(2 * j + 1)) return false;
                 if (g == 0 && fix && j + 1 == n_all && !bar_wait(fixed, 0, stop)) return false;
                 if (j < n[g]) {
-                    if (!bar_wait(p_ready + 8 * g, j & 1, stop)) return false;
+                    if (!bar_wait(turn(p_ready, g, j), phase(j), stop)) return false;
                     tc_fence_after();
                     const uint64_t b = tile_desc(tile_at(2 * j + 1), kBlockBytes);
                     const uint32_t d = tmem + Shape::kOut + g * DP;
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum2 = pair(0.0f, 0.0f);
         bool ok = true;
         for (int j = 0; j < n[g] && ok; ++j) {
-            ok = bar_wait(s_full + 8 * g, j & 1, stop);
+            ok = bar_wait(turn(s_full, g, j), phase(j), stop);
             if (!ok) break;
             tc_fence_after();
             const uint32_t s_cols = tmem + (2 * j + g) % Shape::kScores * 128 + lanes;
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(p_ready + 8 * g);
+            if (lane == 0) bar_arrive(turn(p_ready, g, j));
         }
         if (ok && n[g] > 0) ok = bar_wait(all_done + 8 * g, 0, stop);
         tc_fence_after();
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *stop) atomicAdd(p.stuck, 1u);
     if (warp == 8) {
         tc_fence_after();
-        tmem_free(tmem, 512);
+        tmem_free(sh.tmem, 512);
     }
 }
 
