@@ -8,7 +8,11 @@
 // reductions leave the memory idle otherwise.  A row of up to 512 columns
 // belongs to one warp (eight rows a block, shuffles only); a longer one to a
 // block of its own.  Blocks walk many rows with every thread on fixed
-// columns, so weights are read once and stay in registers.
+// columns, so weights are read once and stay in registers.  65,280 rows of
+// 5,120 in bf16: forward 0.25 ms (5.4 TB/s), backward 0.35 ms (5.8 TB/s);
+// loading each row when its turn came, they took 0.36 and 0.53.  Rows off
+// 16-byte boundaries cost more instructions than bytes: 2 to 4 TB/s in pairs,
+// 1.5 to 3 in single 16-bit elements.
 // The variance is the sum of squared deviations from the mean just found,
 // not E[x^2] - mean^2, which loses all digits where |mean| >> deviation.
 //
