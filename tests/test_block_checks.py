@@ -106,6 +106,25 @@ def test_attention_refuses(q, k, v, kw, error):
         attention(q, k, v, **kw)
 
 
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan")])
+def test_attention_refuses_a_scale_that_is_not_positive(scale):
+    q = t(1, 4, 9, 64)
+    with pytest.raises(ValueError, match="scale"):
+        attention(q, q, q, scale=scale)
+    with pytest.raises(ValueError, match="scale"):
+        attention_backward(q, q, q, q, q, t(1, 4, 9, dtype=F32), scale=scale)
+
+
+def test_operators_refuse_host_tensors():
+    """The library would read host addresses on the device."""
+    x, w = torch.ones(4, 8), torch.ones(8)
+    q = torch.zeros(1, 2, 100, 64, dtype=F16)
+    for call in (lambda: layer_norm(x, w), lambda: layer_norm_backward(x, x, None, torch.ones(4, 2)),
+                 lambda: attention(q, q, q)):
+        with pytest.raises((ValueError, RuntimeError, AssertionError)):
+            call()
+
+
 @pytest.mark.parametrize("name,bad,error", [
     ("grad_out", t(1, 4, 9, 64, dtype=F32), TypeError), ("grad_out", t(1, 4, 8, 64), ValueError),
     ("out", t(1, 4, 9, 32), ValueError), ("lse", t(1, 4, 8, dtype=F32), ValueError), ("lse", None, ValueError),

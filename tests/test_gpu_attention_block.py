@@ -55,3 +55,31 @@ def test_its_gradient_against_binary64():
     B.assert_rel(out, want.detach(), 16 * 2.0 ** -11, "out")
     for name, g in got.items():
         B.assert_rel(g, (xd if name == "x" else par[name]).grad, 16 * 2.0 ** -11, name)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_workspaces_belong_to_the_stream_of_the_call(raw):
+    """Calls on a side stream without workspaces of their own, while the current stream takes and fills memory."""
+    from video_vae_decoder_qkv_gb300 import attention, attention_backward, layer_norm, layer_norm_backward
+
+    q, k, v = (torch.randn(1, 8, 1500, 64, device="cuda").half() for _ in range(3))
+    token, dout = q[:, :, :1].contiguous(), torch.randn_like(q)
+    x, w = torch.randn(4000, 640, device="cuda").half(), torch.ones(640, device="cuda")
+
+    def all_of(**kw):
+        out, lse = attention(q, k, v, **kw)
+        one = attention(token, k, v, **kw)
+        _, stats = layer_norm(x, w, w, **kw)
+        return [out, lse, *one, *attention_backward(dout, q, k, v, out, lse, **kw), *layer_norm_backward(x, x, w, stats, **kw)]
+
+    want = all_of()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        got.append(all_of(stream=side.cuda_stream if raw else side))
+        for n in (1 << 12, 1 << 16, 1 << 20, 1 << 22):
+            torch.empty(n, device="cuda").fill_(float("nan"))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))

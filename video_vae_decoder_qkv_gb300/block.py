@@ -2,12 +2,14 @@
 gradient, the gradient of the fused QK preparation, and attention.
 
 As in ``h3qk``, this only checks tensors and passes their addresses: each
-operator runs in the library's CUDA kernels on the caller's stream, and
-workspaces come from torch's allocator unless the caller passes one.
+operator runs in the library's CUDA kernels on the current stream, or on the
+one passed as ``stream`` (the call then behaves as if it were the current
+one), and workspaces come from torch's allocator unless the caller passes one.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -54,18 +56,35 @@ def _fn(name):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream, dev):
-    if stream is None:
-        if _raw_stream is not None and dev.index is not None:
-            return _raw_stream(dev.index)
-        return torch.cuda.current_stream(dev).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+def _stream(dev):
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _on_stream(f):
+    """Runs an operator with ``stream`` (a torch stream or a raw address) as
+    torch's current one, so that what it allocates, its workspace above all,
+    belongs to that stream and is not given away while the kernels still run."""
+
+    @functools.wraps(f)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+
+    return run
 
 
 def _call(name, dev, *args):
     """A library call with the tensors' device current (the library keys its
     caches on it)."""
     f = _fn(name)
+    if dev.type != "cuda":
+        raise ValueError(f"{name} takes CUDA tensors, got {dev}")
     if dev.index == torch.cuda.current_device():
         st = f(*args)
     else:
@@ -127,7 +146,8 @@ def _need_affine(w, name, width, batch, dev):
     return 1 if w.dim() == 1 else batch
 
 
-def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6, batch: int = 1, out=None, stats=None, stream=None):
+@_on_stream
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6, batch: int = 1, out=None, stats=None):
     """Layer norm of the rows of x [rows, width] (float16, bfloat16 or
     float32; any row stride >= width).  ``weight`` and ``bias`` are float32
     [width], or [batch, width] with one row per item of rows / batch rows (an
@@ -155,12 +175,13 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6, batch: int = 1, 
     else:
         _need(stats, "stats", device=dev, dtypes=(torch.float32,), numel=2 * rows)
     _call("h3qk_layer_norm", dev, x.data_ptr(), _DTYPES[x.dtype], rows, width, _row_stride(x), _ptr(weight), _ptr(bias),
-          groups or 1, eps, out.data_ptr(), stats.data_ptr(), _stream(stream, dev))
+          groups or 1, eps, out.data_ptr(), stats.data_ptr(), _stream(dev))
     return out, stats
 
 
+@_on_stream
 def layer_norm_backward(grad_out, x, weight, stats, *, batch: int = 1, need_weight_grad: bool = True, out=None,
-                        grad_weight=None, grad_bias=None, workspace=None, stream=None):
+                        grad_weight=None, grad_bias=None, workspace=None):
     """The gradient of ``layer_norm``: grad_out [rows, width] of x's type, x
     and weight as the forward took them, stats as it returned them.  Returns
     (grad_x, grad_weight, grad_bias); the last two are float32 of the
@@ -195,14 +216,15 @@ def layer_norm_backward(grad_out, x, weight, stats, *, batch: int = 1, need_weig
         grad_weight = grad_bias = workspace = None
     _call("h3qk_layer_norm_backward", dev, grad_out.data_ptr(), _row_stride(grad_out), x.data_ptr(), _DTYPES[x.dtype],
           rows, width, _row_stride(x), _ptr(weight), groups, stats.data_ptr(), out.data_ptr(), _ptr(grad_weight),
-          _ptr(grad_bias), _ptr(workspace), ws_bytes, _stream(stream, dev))
+          _ptr(grad_bias), _ptr(workspace), ws_bytes, _stream(dev))
     return out, grad_weight, grad_bias
 
 
+@_on_stream
 def prepare_backward(grad_q, grad_k, grad_v, qkv, norm_wq, norm_wk, positions, *, heads: int, head_dim: int,
                      rotary_dim: int, batch: int = 1, valid_len: int | None = None, n_axes: int | None = None,
                      axis_dims=None, theta: float = 10000.0, eps: float = 1e-6, out=None, grad_wq=None, grad_wk=None,
-                     workspace=None, stream=None, layout: str = "head_major", valid_lens=None):
+                     workspace=None, layout: str = "head_major", valid_lens=None):
     """The gradient of a 16-bit ``prepare`` call.  grad_q, grad_k, grad_v are
     contiguous [batch, heads, S, head_dim] (or [batch, S, heads, head_dim]
     with ``layout="token_major"``) of qkv's type; the other arguments are the
@@ -245,7 +267,7 @@ def prepare_backward(grad_q, grad_k, grad_v, qkv, norm_wq, norm_wk, positions, *
     _call("h3qk_prepare_backward", dev, grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), qkv.data_ptr(),
           norm_wq.data_ptr(), norm_wk.data_ptr(), _ptr(positions), tokens, heads, head_dim, rotary_dim, valid_len,
           out.data_ptr(), grad_wq.data_ptr(), grad_wk.data_ptr(), workspace.data_ptr(), ws_bytes, ctypes.byref(o),
-          _stream(stream, dev))
+          _stream(dev))
     return out, grad_wq, grad_wk
 
 
@@ -279,12 +301,14 @@ def _need_lens(t, name, n, dev):
     return t.data_ptr()
 
 
-def _attn_common(q, k, v, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts):
+def _attn_common(q, k, v, scale, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts):
     """Checks shared by both directions: (batch, heads, kv_heads, q_rows, kv_rows, dim, docs, strides, pointers)."""
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("q must be float16 or bfloat16")
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must be [batch, heads, rows, head_dim]")
+    if scale is not None and not scale > 0:
+        raise ValueError(f"scale must be positive, got {scale}")
     dev = q.device
     batch, heads, sq, dim = q.shape
     _, kv_heads, sk, _ = k.shape
@@ -312,9 +336,10 @@ def _attn_common(q, k, v, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_s
     return batch, heads, kv_heads, sq, sk, dim, docs, strides, lists
 
 
+@_on_stream
 def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slopes=None, causal: bool = False,
               prefix_lens=None, doc_offsets=None, q_lens=None, kv_lens=None, q_starts=None, out=None, lse=None,
-              workspace=None, stream=None):
+              workspace=None):
     """Attention on head rows as ``prepare`` writes them.
 
     q: float16/bfloat16 [batch, heads, Sq, D]; k, v: [batch, kv_heads, Sk, D]
@@ -339,7 +364,7 @@ def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slop
     (tokens produced one by one) splits the keys over the GPU and joins the
     parts (h3qk_attention)."""
     batch, heads, kv_heads, sq, sk, dim, docs, strides, lists = _attn_common(
-        q, k, v, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
+        q, k, v, scale, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
     dev = q.device
     if out is None:
         out = torch.empty_like(q)
@@ -364,13 +389,14 @@ def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slop
     if need:
         workspace, ws_bytes = _workspace(workspace, need, dev)
         ws = workspace.data_ptr()
-    _call("h3qk_attention", dev, args(ws, ws_bytes), _stream(stream, dev))
+    _call("h3qk_attention", dev, args(ws, ws_bytes), _stream(dev))
     return out, lse
 
 
+@_on_stream
 def attention_backward(grad_out, q, k, v, out, lse, *, scale: float | None = None, softcap: float = 0.0, slopes=None,
                        causal: bool = False, prefix_lens=None, doc_offsets=None, q_lens=None, kv_lens=None,
-                       q_starts=None, grad_q=None, grad_k=None, grad_v=None, workspace=None, stream=None):
+                       q_starts=None, grad_q=None, grad_k=None, grad_v=None, workspace=None):
     """The gradient of ``attention``: grad_out like out, the forward's q, k, v
     and keyword arguments, out and lse as it returned them.  Returns (grad_q,
     grad_k, grad_v) like q, k and v; heads that share a K/V head add to one
@@ -378,7 +404,7 @@ def attention_backward(grad_out, q, k, v, out, lse, *, scale: float | None = Non
     gives the same bits every time.  The slopes get no gradient
     (h3qk_attention_backward)."""
     batch, heads, kv_heads, sq, sk, dim, docs, strides, lists = _attn_common(
-        q, k, v, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
+        q, k, v, scale, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
     dev = q.device
     row, key = (batch, heads, sq, dim), (batch, kv_heads, sk, dim)
     out_strides = _need_heads(out, "out", row, q.dtype, dev)
@@ -397,5 +423,5 @@ def attention_backward(grad_out, q, k, v, out, lse, *, scale: float | None = Non
                         grad_out.data_ptr(), grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), *lists,
                         workspace.data_ptr(), ws_bytes, *strides[0], *strides[1], *strides[2], *out_strides, *do_strides,
                         *dq_strides, *dk_strides, *dv_strides)
-    _call("h3qk_attention_backward", dev, packed, _stream(stream, dev))
+    _call("h3qk_attention_backward", dev, packed, _stream(dev))
     return grad_q, grad_k, grad_v
