@@ -111,6 +111,29 @@ def test_capped_scores_and_distance(dtype, dim, sq, sk):
     check(q, k, v, slopes=slopes, softcap=30.0, causal=True, kv_lens=[sk, sk // 2 + 1])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("heads,sq,sk,dim,masks", [
+    (2, 300, 3000, 64, {}),                                  # few tiles: all of them cut along the keys
+    (3, 700, 2100, 128, dict(causal=True)),
+    (16, 2600, 2600, 64, {}),                                # 176 tiles: a last round of 24
+    (7, 1800, 1800, 72, dict(causal=True, prefix_lens=[700])),
+    (2, 1700, 1700, 128, dict(q_lens=[1111], kv_lens=[1290])),
+    (16, 2600, 2600, 64, dict(kv_lens=[2222])),
+    (2, 300, 1500, 64, dict(kv_lens=[130])),                 # most parts without a key
+    (2, 300, 1500, 64, dict(kv_lens=[0])),
+    (4, 2000, 2000, 64, dict(doc_offsets=[0, 1100, 1101, 1500], causal=True)),
+])
+def test_tiles_cut_along_the_keys(dtype, heads, sq, sk, dim, masks):
+    q, k, v = make(dtype, 1, heads, heads, sq, sk, dim, seed=8)
+    offsets = masks.get("doc_offsets")
+    pointers = [0] * 11 + [q.data_ptr() if offsets else 0] + [0] * 4  # doc_offsets alone is looked at
+    call = block._ATTN.pack(block._DTYPES[dtype], 1, heads, heads, dim, 0, len(offsets) - 1 if offsets else 0, 0, 0.0, 0.0,
+                            sq, sk, *pointers, 0, *[0] * 24)
+    assert block._fn("h3qk_attention_workspace_bytes")(call) > 0
+    check(q, k, v, **masks)
+    check(q, k, v, softcap=15.0, slopes=torch.linspace(0.01, 0.3, heads, device="cuda"), **masks)
+
+
 @pytest.mark.parametrize("sq", [1, 300])
 def test_scores_far_apart(sq):
     """Rows whose weights sit on one key, or are all alike, or rise along the keys (the maximum keeps moving)."""

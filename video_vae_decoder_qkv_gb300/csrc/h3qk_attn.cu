@@ -97,6 +97,33 @@ void split_of(const h3qk_attn& a, int32_t* splits, int32_t* chunk)
     *splits = static_cast<int32_t>(a.kv_rows > 0 ? (a.kv_rows + c - 1) / c : 1);
 }
 
+// The tail is worth a second kernel (about 5 us) where it saves some eight key
+// tiles of 128 (about 1 us each) of the last round; a part keeps at least
+// four.  16 heads of 4896 x 64 are 2.1 rounds of tiles: 118 us whole, 104 cut;
+// 10 heads of 4096 x 128, 1.05 rounds: 106 and 75; 2 heads of 2000 x 64: 23
+// and 16.  Row lengths and documents on the device leave tiles empty: after a
+// first full round nothing is known of the last one then, and it stays whole
+// (16 heads whose lengths made two rounds exactly: 89 us whole, 102 cut).
+h3qk_core::TilePlan tile_plan(const h3qk_attn& a)
+{
+    constexpr int64_t kRows = h3qk_core::kRowTile;
+    h3qk_core::TilePlan t;
+    t.tiles = (a.q_rows + kRows - 1) / kRows + a.docs;
+    const int64_t total = t.tiles * a.heads * a.batch, sms = h3qk_internal_sm_count();
+    t.tail = total % sms;
+    t.parts = 1;
+    if (t.tail > 0 && (total < sms || !(a.q_lens || a.docs))) {
+        const int64_t keys = (a.kv_rows + 127) / 128;
+        t.parts = sms / t.tail;
+        if (t.parts > keys / 4) t.parts = keys / 4;
+        if (t.parts > 16) t.parts = 16;
+        if (t.parts < 2 || keys - keys / t.parts < 8) t.parts = 1;
+    }
+    if (t.parts == 1) t.tail = 0;
+    t.whole = total - t.tail;
+    return t;
+}
+
 h3qk_status check_sizes(const h3qk_attn& a)
 {
     if (a.dtype != H3QK_FP16 && a.dtype != H3QK_BF16) return H3QK_ERR_INVALID_ARG;
@@ -210,8 +237,12 @@ void fill(Params& p, const h3qk_attn& a)
 
 extern "C" size_t h3qk_attention_workspace_bytes(const h3qk_attn* call)
 {
-    if (!call || check_sizes(*call) != H3QK_OK || !use_split(*call)) return 0;
+    if (!call || check_sizes(*call) != H3QK_OK) return 0;
     const h3qk_attn& a = *call;
+    if (!use_split(a)) {
+        const h3qk_core::TilePlan t = tile_plan(a);
+        return static_cast<size_t>(t.tail * t.parts) * h3qk_core::tile_part_floats(a.head_dim) * 4;
+    }
     int32_t splits, chunk;
     split_of(a, &splits, &chunk);
     if (splits == 1) return 0;
@@ -267,6 +298,13 @@ extern "C" h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t strea
         split_of(a, &p.splits, &p.chunk);
         return h3qk_ops::status_of(h3qk_core::forward_split(bf16, p, st));
     }
+    const h3qk_core::TilePlan plan = tile_plan(a);
+    if (plan.whole + plan.tail * plan.parts > INT32_MAX) return H3QK_ERR_INVALID_ARG;
+    p.tiles = static_cast<int32_t>(plan.tiles);
+    p.whole = static_cast<int32_t>(plan.whole);
+    p.tail = static_cast<int32_t>(plan.tail);
+    p.parts = static_cast<int32_t>(plan.parts);
+    p.part = static_cast<float*>(a.workspace);
     Maps m;
     // Without keys no tile is loaded; the maps then describe q instead.
     for (int i = 1; i < 3; ++i)

@@ -35,8 +35,9 @@ struct Params {
     uint16_t *dq, *dk, *dv;
     Strides dqs, dks, dvs;
     float* delta;             // [batch][heads][q_rows]
-    float* part;              // split: partial results
-    int32_t splits, chunk;    // split: keys per block
+    float* part;              // partial results
+    int32_t splits, chunk;    // few rows: keys per block
+    int32_t tiles, whole, tail, parts;  // many rows: see TilePlan
     unsigned int* stuck;      // counts blocks whose waits ran out
 };
 
@@ -210,6 +211,17 @@ cudaError_t ready(K* kernel, int smem, bool (&done)[64])
     done[dev] = e == cudaSuccess;
     return e;
 }
+
+// Many rows: the blocks' tiles (256 query rows of a head) in one row, `tiles`
+// a head.  A last round of tiles that would leave most SMs idle is cut along
+// the keys: the first `whole` tiles have a block each, the `tail` ones after
+// them `parts`, whose results a second kernel joins.
+constexpr int kRowTile = 256;
+struct TilePlan {
+    int64_t tiles, whole, tail, parts;  // tail 0: nothing is cut
+};
+// Floats that a part leaves: per row O[dim], then m and sum of every row.
+__host__ __device__ inline int64_t tile_part_floats(int dim) { return static_cast<int64_t>(kRowTile) * (dim + 2); }
 
 // Host side: the kernels' launchers.
 struct Maps {

@@ -65,6 +65,22 @@ struct FwdShared {
     int stop;
 };
 
+// Where tile number t of a call lies.  Causal rows see more keys the later
+// they are: a head's longest tiles go first.
+struct Place {
+    int tile, head, item;
+};
+__device__ __forceinline__ Place place_of(const Params& p, int t)
+{
+    Place at;
+    at.tile = t % p.tiles;
+    if (p.causal) at.tile = p.tiles - 1 - at.tile;
+    t /= p.tiles;
+    at.head = t % p.heads;
+    at.item = t / p.heads;
+    return at;
+}
+
 template <bool BF16, int DP, int BENDS>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -75,16 +91,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr float kShift = BF16 ? 0.0f : 7.0f;
     extern __shared__ uint8_t smem_raw[];
     __shared__ FwdShared sh;
+    h3qk_ops::allow_dependents();
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t q_smem = base, ring = base + 2 * Shape::kTileBytes;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int head = blockIdx.y;
-    const int kv_head = head / p.group;
+    const bool cut = blockIdx.x >= p.whole;  // one of the parts of a tail tile
+    const int part = cut ? (blockIdx.x - p.whole) % p.parts : 0;
+    const Place at = place_of(p, cut ? p.whole + (blockIdx.x - p.whole) / p.parts : blockIdx.x);
+    const int head = at.head, kv_head = head / p.group;
 
     Stretch s;
-    // Causal rows see more keys the later they are: the longest tiles go first.
-    const int block = p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-    if (!h3qk_core::find_stretch(s, p, block, blockIdx.z, 2 * kTile, false)) return;
+    if (!h3qk_core::find_stretch(s, p, at.tile, at.item, 2 * kTile, false)) return;
     const int tile_row = s.tile * 2 * kTile;
     int n[2], seen = 0;  // tiles of each group, keys that any row of the block sees
 #pragma unroll
@@ -95,11 +112,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         n[g] = (lim + kTile - 1) / kTile;
         seen = max(seen, lim);
     }
-    const int n_all = max(n[0], n[1]);
+    int n_all = max(n[0], n[1]), j0 = 0;  // tiles of this block; the first of them
+    if (cut) {
+        const int each = (n_all + p.parts - 1) / p.parts, last = n_all;
+        j0 = min(part * each, last);
+        n_all = min(last - j0, each);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) n[g] = min(max(n[g] - j0, 0), n_all);
+    }
+    const int key0 = j0 * kTile;
     // Rows of the last tile that no row of the block sees: unwritten cache
     // rows, another document's, later tokens.  They are cleared (0 * NaN is
     // NaN, even with p = 0); past the tensor's end the loads give zeros.
-    const bool fix = n_all * kTile > seen && s.k0 + seen < p.kv_rows;
+    const bool fix = n_all > 0 && key0 + n_all * kTile > seen && s.k0 + seen < p.kv_rows;
 
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
     const uint32_t s_full = smem_addr(sh.s_full), p_ready = smem_addr(sh.p_ready), o_done = smem_addr(sh.o_done);
@@ -157,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = bar_wait(empty + 8 * st, ((i / kStages) & 1) ^ 1, stop);
                 if (!ok) break;
                 bar_expect(full + 8 * st, Shape::kTileBytes);
-                const int row = s.k0 + (i >> 1) * kTile;
+                const int row = s.k0 + key0 + (i >> 1) * kTile;
                 for (int b = 0; b < Shape::kBlocks; ++b)
                     tma_load(ring + st * Shape::kTileBytes + b * kBlockBytes, (i & 1) ? &map_v : &map_k, 64 * b, row,
                              kv_head, s.item, full + 8 * st);
@@ -168,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (fix) {
             const int i = 2 * n_all - 1, st = i % kStages;
             if (bar_wait(full + 8 * st, (i / kStages) & 1, stop)) {
-                const int first = seen - (n_all - 1) * kTile;  // rows to keep
+                const int first = seen - key0 - (n_all - 1) * kTile;  // rows to keep
                 for (int b = 0; b < Shape::kBlocks; ++b)
                     for (int o = first * 128 + lane * 16; o < kBlockBytes; o += 512)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
@@ -296,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_wait_ld(sr[b]);
             if constexpr (BENDS != h3qk_core::kPlain) {
-                const float far = static_cast<float>(s.start + i_row - j * kTile);
+                const float far = static_cast<float>(s.start + i_row - key0 - j * kTile);
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -315,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
             }
-            if ((j + 1) * kTile > lim_first) {
-                const int left = lim - j * kTile;
+            if (key0 + (j + 1) * kTile > lim_first) {
+                const int left = lim - key0 - j * kTile;
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -381,7 +406,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpair(lo, hi, sum2);
         const float sum = lo + hi;
         const bool live = ok && i_row < s.rows && n[g] > 0 && sum > 0.0f;
-        const bool write = i_row < s.span;
+        if (cut) {
+            // A part's row: O, the maximum and the sum as they are.
+            float* to = p.part + static_cast<int64_t>(blockIdx.x - p.whole) * h3qk_core::tile_part_floats(p.dim);
+            const int tr = g * kTile + r;
+            const bool some = i_row < s.rows && n[g] > 0;
+            *reinterpret_cast<float2*>(to + 2 * kTile * p.dim + 2 * tr) =
+                make_float2(m == -INFINITY ? m : m * c, !ok ? __int_as_float(0x7fc00000) : some ? sum : 0.0f);
+#pragma unroll
+            for (int d = 0; d < DP; d += 32) {
+                uint32_t o[32];
+                if (n[g] > 0) {
+                    tmem_ld32(o, o_cols + d);
+                    tmem_wait_ld(o);
+                }
+                if (some)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        if (d + e < p.dim)
+                            *reinterpret_cast<uint4*>(to + tr * p.dim + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+        }
+        const bool write = !cut && i_row < s.span;
         const int64_t row = s.row0 + i_row;
         if (write)
             p.lse[(static_cast<int64_t>(s.item) * p.heads + head) * p.q_rows + row] =
@@ -395,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int d = 0; d < DP; d += 32) {
             uint32_t o[32];
-            if (n[g] > 0) {
+            if (n[g] > 0 && !cut) {
                 tmem_ld32(o, o_cols + d);
                 tmem_wait_ld(o);
             }
@@ -423,6 +469,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// One warp a row of a tail tile: its parts' O, weighted to their common
+// maximum, in order.
+template <bool BF16>
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ Params p)
+{
+    constexpr float kShift = BF16 ? 0.0f : 7.0f;
+    h3qk_ops::wait_for_previous();
+    const int lane = threadIdx.x & 31, d = 4 * lane;
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), tail = row / (2 * kTile), tr = row % (2 * kTile);
+    const Place at = place_of(p, p.whole + tail);
+    Stretch s;
+    const bool there = h3qk_core::find_stretch(s, p, at.tile, at.item, 2 * kTile, false);
+    const int i_row = s.tile * 2 * kTile + tr;
+    if (!there || i_row >= s.span) return;
+    const int64_t size = h3qk_core::tile_part_floats(p.dim);
+    const float* part = p.part + static_cast<int64_t>(tail) * p.parts * size;
+    float2 mine = make_float2(-INFINITY, 0.0f);
+    if (lane < p.parts) mine = __ldcg(reinterpret_cast<const float2*>(part + lane * size + 2 * kTile * p.dim + 2 * tr));
+    if (mine.y == 0.0f) mine.x = -INFINITY;  // no visible key: no O either
+    float top = mine.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = mine.y == 0.0f ? 0.0f : exp2_fast(mine.x - top);
+    float sum = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < p.parts; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, mine.y, i);
+        sum = fmaf(li, fi, sum);
+        if (li != 0.0f && d < p.dim) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(part + i * size + static_cast<int64_t>(tr) * p.dim + d));
+            v.x = fmaf(x.x, fi, v.x);
+            v.y = fmaf(x.y, fi, v.y);
+            v.z = fmaf(x.z, fi, v.z);
+            v.w = fmaf(x.w, fi, v.w);
+        }
+    }
+    const int64_t out_row = s.row0 + i_row;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (d < p.dim) {
+        uint2 w;
+        w.x = round_pair<BF16>(v.x * inv, v.y * inv);
+        w.y = round_pair<BF16>(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(p.out + s.item * p.os.item + at.head * p.os.head + out_row * p.os.row + d) = w;
+    }
+    if (lane == 0)
+        p.lse[(static_cast<int64_t>(s.item) * p.heads + at.head) * p.q_rows + out_row] =
+            sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * h3qk_core::kLn2;
+}
+
 template <bool BF16, int DP, int BENDS>
 cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
 {
@@ -431,10 +526,12 @@ cudaError_t launch(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
     static bool done[64] = {false};
     const cudaError_t e = h3qk_core::ready(kernel, smem, done);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(h3qk_core::tiles_of(p, p.q_rows, 2 * kTile)), p.heads, p.batch);
-    kernel<<<grid, kThreads, smem, st>>>(m.q, m.k, m.v, p);
+    kernel<<<p.whole + p.tail * p.parts, kThreads, smem, st>>>(m.q, m.k, m.v, p);
     h3qk_internal_count_launch();
-    return cudaGetLastError();
+    const cudaError_t launched = cudaGetLastError();
+    if (launched != cudaSuccess || p.tail == 0) return launched;
+    return h3qk_ops::launch_chained(join_parts_kernel<BF16>, dim3(static_cast<unsigned>(p.tail) * (2 * kTile / 8)), dim3(256), 0,
+                                    st, p);
 }
 
 template <bool BF16, int DP>
