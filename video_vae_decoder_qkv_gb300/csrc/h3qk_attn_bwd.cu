@@ -61,6 +61,27 @@ constexpr float kLift = BF16 ? 0.0f : 10.0f;
 template <bool BF16>
 constexpr float kDrop = BF16 ? 1.0f : 1.0f / 1024.0f;
 
+// The tile, head and item of a block.  The grid is [tiles][heads][items], so a
+// head's tiles follow one another and its streamed rows stay in L2.  Causal
+// tiles are of unequal length: the longest of all heads (late rows, early keys)
+// go first.
+struct Place3 {
+    int tile, head, item;
+};
+__device__ __forceinline__ Place3 place_of(bool causal, bool late_first, int heads, int items)
+{
+    if (!causal) return Place3{static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.z)};
+    const int tiles = gridDim.x;
+    int64_t t = (static_cast<int64_t>(blockIdx.z) * heads + blockIdx.y) * tiles + blockIdx.x;
+    Place3 at;
+    at.head = static_cast<int>(t % heads);
+    t /= heads;
+    at.item = static_cast<int>(t % items);
+    at.tile = static_cast<int>(t / items);
+    if (late_first) at.tile = tiles - 1 - at.tile;
+    return at;
+}
+
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int blocks, int row, int head, int item,
                                           uint32_t bar)
 {
@@ -181,11 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t q_smem = base, do_smem = base + Shape::kTileBytes, ring = base + 2 * Shape::kTileBytes;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int head = blockIdx.y, kv_head = head / p.group;
+    const Place3 block = place_of(p.causal, true, p.heads, p.batch);
+    const int head = block.head, kv_head = head / p.group;
 
     Stretch s;
-    const int block = p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-    if (!h3qk_core::find_stretch(s, p, block, blockIdx.z, kTile, false)) return;
+    if (!h3qk_core::find_stretch(s, p, block.tile, block.item, kTile, false)) return;
     const int tile_row = s.tile * kTile;
     const int last = min(tile_row + kTile, s.rows) - 1;
     const int seen = last < tile_row ? 0 : max(h3qk_core::limit_of(s, p.causal, last), 0);
@@ -491,10 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t k_smem = base, v_smem = base + Shape::kTileBytes, ring = base + 2 * Shape::kTileBytes;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int kv_head = blockIdx.y;
+    const Place3 block = place_of(p.causal, false, p.kv_heads, p.batch);
+    const int kv_head = block.head;
 
     Stretch s;
-    if (!h3qk_core::find_stretch(s, p, blockIdx.x, blockIdx.z, kTile, true)) return;
+    if (!h3qk_core::find_stretch(s, p, block.tile, block.item, kTile, true)) return;
     const int tile_key = s.tile * kTile;
     const int q_tiles = (s.rows + kTile - 1) / kTile;
     // First query tile that sees any of the keys; none if the keys do not exist.

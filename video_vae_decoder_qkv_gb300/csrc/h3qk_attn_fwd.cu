@@ -65,19 +65,26 @@ struct FwdShared {
     int stop;
 };
 
-// Where tile number t of a call lies.  Causal rows see more keys the later
-// they are: a head's longest tiles go first.
+// Where tile number t of a call lies.  A head's tiles follow one another, so
+// that its keys stay in L2.  Causal rows see more keys the later they are:
+// there the longest tiles of all heads go first, and the shortest fill the end.
 struct Place {
     int tile, head, item;
 };
 __device__ __forceinline__ Place place_of(const Params& p, int t)
 {
     Place at;
-    at.tile = t % p.tiles;
-    if (p.causal) at.tile = p.tiles - 1 - at.tile;
-    t /= p.tiles;
-    at.head = t % p.heads;
-    at.item = t / p.heads;
+    if (p.causal) {
+        at.head = t % p.heads;
+        t /= p.heads;
+        at.item = t % p.batch;
+        at.tile = p.tiles - 1 - t / p.batch;
+    } else {
+        at.tile = t % p.tiles;
+        t /= p.tiles;
+        at.head = t % p.heads;
+        at.item = t / p.heads;
+    }
     return at;
 }
 
