@@ -274,3 +274,28 @@ def test_workspace_sizes():
     assert 0 < f(10, 64, 1) <= f(1000, 64, 1) and f(10, 64, 3) == 0 and f(10, 0, 1) == 0 and f(-1, 64, 1) == 0
     f = block._fn("h3qk_prepare_backward_workspace_bytes")
     assert 0 < f(64) < f(128) and f(60) == 0 and f(512) == 0
+
+
+@pytest.mark.parametrize("q_rows,kv_rows", [(4896, 4896), (1, 4896), (300, 3000), (2600, 2600)])
+def test_a_calls_workspace_does_not_depend_on_earlier_ones(monkeypatch, q_rows, kv_rows):
+    """Every two calls of one shape, one after the other: each gets the workspace that the library asks for it."""
+    q = torch.empty(1, 16, q_rows, 64, dtype=F16)
+    k = torch.empty(1, 16, kv_rows, 64, dtype=F16)
+    one = torch.ones(1, dtype=I32)
+    calls = [dict(), dict(causal=True), dict(q_lens=one), dict(kv_lens=one), dict(q_lens=one, kv_lens=one),
+             dict(q_starts=one), dict(causal=True, prefix_lens=one), dict(slopes=torch.ones(16)), dict(softcap=3.0)]
+    if q_rows == kv_rows:
+        calls += [dict(doc_offsets=torch.zeros(2, dtype=I32)), dict(doc_offsets=torch.zeros(2, dtype=I32), causal=True)]
+    passed = []
+    monkeypatch.setattr(block, "_sizes", {})
+    monkeypatch.setattr(block, "_call", lambda name, dev, packed, stream: passed.append(packed))
+    monkeypatch.setattr(block, "_stream", lambda dev: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    for first in calls:
+        for second in calls:
+            block._sizes.clear()
+            for kw in (first, second):
+                attention(q, k, k, **kw)
+                packed = passed.pop()
+                given = block._ATTN.unpack(packed)[28]
+                assert given == block._fn("h3qk_attention_workspace_bytes")(packed), (list(first), list(second))

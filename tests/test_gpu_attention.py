@@ -251,3 +251,12 @@ def test_no_rows_or_no_keys():
         q, k, v = make(torch.float16, 2, 2, 2, sq, 0, 64)
         out, lse = attention(q, k, v)
         assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("ragged_first", [True, False])
+def test_ragged_and_full_calls_of_one_shape(ragged_first):
+    """More tiles than SMs, where lengths on the device decide about the workspace."""
+    q, k, v = make(torch.float16, 1, 16, 16, 2600, 2600, 64, seed=4)
+    block._sizes.clear()
+    for ragged in (ragged_first, not ragged_first):
+        check(q, k, v, **(dict(q_lens=[2311], kv_lens=[2400]) if ragged else {}))

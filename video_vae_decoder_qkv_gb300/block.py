@@ -380,8 +380,9 @@ def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slop
                           0, 0, 0, 0, *lists, ws, ws_bytes, *strides[0], *strides[1], *strides[2], *out_strides,
                           *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES)
 
-    # the size depends on the shape alone
-    shape = (batch, heads, kv_heads, sq, sk, dim, docs)
+    # The size depends on the sizes, the masks' kind and which lists there are
+    # (the library does not read them), not on any value.
+    shape = (batch, heads, kv_heads, sq, sk, dim, causal, docs, *(t != 0 for t in lists))
     need = _sizes.get(("h3qk_attention_workspace_bytes", dev.index, shape))
     if need is None:
         need = _size("h3qk_attention_workspace_bytes", dev, args(0, 0), key=shape)
