@@ -179,3 +179,38 @@ def test_gradient_against_differences(which):
     minus = f(tuple(at[n] - (1e-2 * v if n == which else 0) for n in at))
     slope = float((grad.double() * v.double()).sum())
     assert abs((plus - minus) / 2e-2 - slope) <= 1e-3 * slope
+
+
+_FIRST_CALLS = """
+import sys
+sys.path[:0] = sys.argv[1:]
+import torch
+import test_gpu_layer_norm as T
+from video_vae_decoder_qkv_gb300 import layer_norm, layer_norm_backward
+# Widths whose rows ahead take 48 KiB of shared memory or just under it, beside what the kernel holds
+# itself; by kind of row (chunks of 16 bytes, pairs, single elements) and direction.
+for dtype, forward, backward in ((torch.float16, (6000, 6110, 6127), (2880, 3050, 3047)),
+                                 (torch.bfloat16, (6144, 6114, 6113), (2576, 3038, 3061)),
+                                 (torch.float32, (2880, 3061), (2000, 2033))):
+    for width in backward:
+        x, dy, w, b = T._make(dtype, 9, width)
+        _, mean, rstd = T.B.layer_norm(x, None, None, T.EPS, 1)
+        layer_norm_backward(dy, x, w, torch.stack([mean, rstd], 1).float())
+    for width in forward:
+        x, dy, w, b = T._make(dtype, 9, width)
+        layer_norm(x, w, b)
+    for width in (*backward, *forward):
+        T._check(*T._make(dtype, 9, width), 1)
+"""
+
+
+def test_widths_at_the_shared_memory_limit_as_first_calls():
+    """A fresh process: a wider call would have raised a kernel's limit for good."""
+    import os
+    import subprocess
+    import sys
+
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS, here, os.path.dirname(here)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -668,17 +668,21 @@ int64_t max_parts(int64_t rows_per_group, int64_t groups)
     return rows_per_group < cap ? rows_per_group : cap;
 }
 
+// Shared memory a block may ask for at launch, beside the kernel's own arrays
+// (512 bytes at most): the largest ring is 192 KiB (196,704 bytes).
+constexpr int kMostDynamic = 200 * 1024;
+
+// Raises the limit once per kernel and device, whatever this call asks for:
+// the default of 48 KiB holds the kernel's own arrays too.
 template <typename K>
 cudaError_t launch_with(K* kernel, bool (&raised)[64], dim3 grid, int threads, int smem, const LnArgs& a, cudaStream_t st)
 {
-    if (smem > 48 * 1024) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-        if (!raised[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-            if (e != cudaSuccess) return e;
-            raised[dev] = true;
-        }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    if (!raised[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostDynamic);
+        if (e != cudaSuccess) return e;
+        raised[dev] = true;
     }
     kernel<<<grid, threads, smem, st>>>(a);
     h3qk_internal_count_launch();
