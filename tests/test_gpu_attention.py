@@ -260,3 +260,45 @@ def test_ragged_and_full_calls_of_one_shape(ragged_first):
     block._sizes.clear()
     for ragged in (ragged_first, not ragged_first):
         check(q, k, v, **(dict(q_lens=[2311], kv_lens=[2400]) if ragged else {}))
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("sq,dim", [(1, 64), (300, 64), (300, 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_unwritten_cache_rows_leave_no_mark_on_capped_scores(sq, dim, bad, slopes):
+    """Lengths that end 1, 2 and 3 past a multiple of 4."""
+    q, k, v = make(torch.float16, 3, 2, 2, sq, 1024, dim)
+    ends = (1001, 130, 643)
+    kw = dict(kv_lens=_i32(ends), softcap=20.0, slopes=torch.tensor([0.1, 0.01], device="cuda") if slopes else None)
+    want = attention(q, k, v, **kw)
+    assert want[0].isfinite().all()
+    for b, n in enumerate(ends):
+        k[b, :, n:] = bad
+        v[b, :, n:] = bad
+    got = attention(q, k, v, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_documents_do_not_leak_into_capped_scores(causal):
+    q, k, v = make(torch.bfloat16, 1, 2, 2, 600, 600, 128)
+    kw = dict(doc_offsets=_i32([0, 130, 201, 472]), softcap=20.0, causal=causal)
+    want = attention(q, k, v, **kw)
+    for t in (q, k, v):
+        t[:, :, 130:201] = float("nan")
+        t[:, :, 472:] = float("inf")
+    got = attention(q, k, v, **kw)
+    keep = [*range(130), *range(201, 600)]
+    assert torch.equal(got[0][:, :, keep], want[0][:, :, keep]) and torch.equal(got[1][:, :, keep], want[1][:, :, keep])
+    assert got[0][:, :, 130:201].isnan().all()
+
+
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_a_key_concerns_only_the_rows_that_see_it(softcap):
+    """A NaN in a key: its own and later rows, none before."""
+    q, k, v = make(torch.float16, 1, 2, 2, 300, 300, 64)
+    want = attention(q, k, v, causal=True, softcap=softcap)
+    k[:, :, 77] = float("nan")
+    got = attention(q, k, v, causal=True, softcap=softcap)
+    assert torch.equal(got[0][:, :, :77], want[0][:, :, :77]) and torch.equal(got[1][:, :, :77], want[1][:, :, :77])
+    assert got[0][:, :, 77:].isnan().all()

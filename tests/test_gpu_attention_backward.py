@@ -202,3 +202,23 @@ def test_gradient_against_differences_of_the_forward(which, softcap):
     f = lambda t: float((dout.double() * attention(*t, **kw)[0].double()).sum())  # noqa: E731
     want = float((grad * (plus[which].double() - minus[which].double())).sum())
     assert abs((f(plus) - f(minus)) - want) <= 0.03 * abs(want)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_unseen_rows_leave_no_mark_on_capped_scores(dim):
+    """Unwritten rows that follow 1, 2 and 3 past a multiple of 4, and documents that end there."""
+    q, k, v = make(torch.bfloat16, 3, 4, 2, 300, 300, dim)
+    ql, kl = [211, 300, 130], [171, 129, 130]
+    kw = dict(q_lens=_i32(ql), kv_lens=_i32(kl), softcap=20.0)
+    dout = torch.randn_like(q)
+    out, lse = attention(q, k, v, **kw)
+    want = attention_backward(dout, q, k, v, out, lse, **kw)
+    for b in range(3):
+        q[b, :, ql[b]:] = float("nan")
+        dout[b, :, ql[b]:] = float("inf")
+        k[b, :, kl[b]:] = float("nan")
+        v[b, :, kl[b]:] = float("nan")
+    out2, lse2 = attention(q, k, v, **kw)
+    got = attention_backward(dout, q, k, v, out2, lse2, **kw)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

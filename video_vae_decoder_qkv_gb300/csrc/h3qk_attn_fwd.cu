@@ -327,6 +327,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < 4; ++b) tmem_ld32(sr[b], s_cols + 32 * b);
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_wait_ld(sr[b]);
+            const bool edge = key0 + (j + 1) * kTile > lim_first;
+            const int left = lim - key0 - j * kTile;
+            if constexpr (BENDS & h3qk_core::kCapped) {
+                // Hidden scores may be NaN, and four scores share a reciprocal.
+                if (edge)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * b + e >= left) sr[b][e] = 0u;
+            }
             if constexpr (BENDS != h3qk_core::kPlain) {
                 const float far = static_cast<float>(s.start + i_row - key0 - j * kTile);
 #pragma unroll
@@ -347,8 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
             }
-            if (key0 + (j + 1) * kTile > lim_first) {
-                const int left = lim - key0 - j * kTile;
+            if (edge) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
