@@ -445,8 +445,8 @@ h3qk_status h3qk_layer_norm_backward(const void* grad_out, int64_t grad_stride, 
  * contiguous (the input type) and the weight gradients grad_wq, grad_wk
  * (float[head_dim], each NULL when not wanted):
  *   dn = R^T dy (the rotation by minus the angle of the forward call),
- *   grad_w = sum over rows and heads of dn x inv,
- *   grad_x = inv dn w - x inv^3 (sum_d dn w x) / D,  inv = (sum x^2 / D + eps)^-1/2;
+ *   grad_w = sum over rows and heads of dn xh,  xh = x inv,
+ *   grad_x = inv (dn w - xh (sum_d dn w xh) / D),  inv = (sum x^2 / D + eps)^-1/2;
  * the V part of grad_qkv is grad_v.  The forward's 16-bit rounding points
  * count as the identity.  Rows past the valid prefix get zeros and their
  * gradients are not read.

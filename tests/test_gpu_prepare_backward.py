@@ -162,3 +162,19 @@ def test_gradient_against_differences_of_the_forward(which):
 
     want = float((grad * (plus[which].double() - minus[which].double())).sum())
     assert abs((f(plus) - f(minus)) - want) <= 0.03 * abs(want)
+
+
+@pytest.mark.parametrize("size,eps", [(1e13, 1e-6), (1e15, 1e-6), (1e17, 1e-6), (1.0, 0.0), (1e-14, 0.0), (1e-17, 0.0)])
+def test_rows_of_any_size(monkeypatch, size, eps):
+    """Rows whose inverse norm has a cube outside binary32's range."""
+    import sys
+
+    monkeypatch.setattr(sys.modules[__name__], "EPS", eps)
+    qkv, wq, wk, pos, grads = _make(torch.bfloat16, 1, 48, 3, 64, 3)
+    qkv = (qkv.double() * size).to(torch.bfloat16)
+    got, gq, gk = prepare_backward(*grads, qkv, wq, wk, pos, heads=3, head_dim=64, rotary_dim=48, eps=eps)
+    want, terms, dws, dw_terms = _want(qkv, wq, wk, pos, grads, 3, 64, 48, (16, 16, 16), 1, 48)
+    dtype = torch.bfloat16
+    B.assert_within(got, want, B.U[dtype] * want.abs() + B.TINY[dtype] + 32 * B.U32 * terms, "grad_qkv")
+    for g, w, s in ((gq, dws[0], dw_terms[0]), (gk, dws[1], dw_terms[1])):
+        B.assert_within(g, w, (48 * 3 + 64) * B.U32 * s + 1e-30, "grad_w")

@@ -4,7 +4,7 @@
 // xh = x inv, inv = (sum x^2 / D + eps)^-1/2 (the forward's 16-bit rounding
 // points count as the identity):
 //   dn = R^T dy (the rotation by minus the angle),  dw = sum dn xh,
-//   g = dn w,  dx = inv g - x inv^3 (sum g x) / D;   V: dx = dy.
+//   g = dn w,  dx = inv (g - xh mean(g xh));   V: dx = dy.
 //
 // Bound by HBM: 16 bytes of x, dy and dx per 8 channels of Q and K, 32 per 8
 // of V, and about 120 instructions a warp for 32 such chunks, a third of the
@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) prepare_backward_kernel(const 
                     gx += __shfl_xor_sync(0xffffffffu, gx, o);
                 }
                 const float inv = 1.0f / sqrtf(ss * inv_d + p.eps);
-                const float k = inv * inv * inv * gx * inv_d;
+                // xh and this mean stay near 1 for rows of any size; inv^3 would not.
+                const float mean = inv * gx * inv_d;
                 uint32_t ow[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -149,9 +150,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) prepare_backward_kernel(const 
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int e = 2 * i + j;
-                        const float dni = dn[e] * inv;
-                        if (live) dw[t][e] = fmaf(dni, xf[e], dw[t][e]);
-                        o[j] = fmaf(-k, xf[e], dni * w[t][e]);
+                        const float xh = xf[e] * inv;
+                        if (live) dw[t][e] = fmaf(dn[e], xh, dw[t][e]);
+                        o[j] = inv * fmaf(-mean, xh, dn[e] * w[t][e]);
                     }
                     ow[i] = live ? h3qk::round2<BF16>(o[0], o[1]) : 0u;
                 }
