@@ -327,23 +327,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < 4; ++b) tmem_ld32(sr[b], s_cols + 32 * b);
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_wait_ld(sr[b]);
-            const bool edge = key0 + (j + 1) * kTile > lim_first;
+            const bool edge = key0 + (j + 1) * kTile > lim_first;  // some row sees the tile only in part
             const int left = lim - key0 - j * kTile;
-            if constexpr (BENDS & h3qk_core::kCapped) {
-                // Hidden scores may be NaN, and four scores share a reciprocal.
-                if (edge)
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * b + e >= left) sr[b][e] = 0u;
-            }
-            if constexpr (BENDS != h3qk_core::kPlain) {
+            auto hide = [&](int b, int e, uint32_t as) {
+                if (32 * b + e >= left) sr[b][e] = as;
+            };
+            auto bend_all = [&](auto at_edge) {
                 const float far = static_cast<float>(s.start + i_row - key0 - j * kTile);
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
+                        // Hidden scores may be NaN, and under a cap four share a reciprocal.
+                        if constexpr (decltype(at_edge)::value)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) hide(b, e + i, 0u);
                         uint64_t z[2], keep[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -356,14 +354,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sr[b][e + 2 * i] = __float_as_uint(lo);
                             sr[b][e + 2 * i + 1] = __float_as_uint(hi);
                         }
+                        if constexpr (decltype(at_edge)::value)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) hide(b, e + i, 0xff800000u);
                     }
-            }
-            if (edge) {
+            };
+            if constexpr (BENDS & h3qk_core::kCapped) {
+                if (edge) bend_all(std::true_type{});
+                else bend_all(std::false_type{});
+            } else {
+                if constexpr (BENDS != h3qk_core::kPlain) bend_all(std::false_type{});
+                if (edge) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                    for (int b = 0; b < 4; ++b)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * b + e >= left) sr[b][e] = 0xff800000u;
+                        for (int e = 0; e < 32; ++e) hide(b, e, 0xff800000u);
+                }
             }
             float mx[4];
 #pragma unroll
