@@ -540,7 +540,11 @@ h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t stream);
  * grad_v:
  *   delta = sum_d grad_out out,  ds = p (grad_out.v - delta) (1 - (z/softcap)^2),
  *   grad_v = sum_i p grad_out,  grad_q = scale sum_j ds k,  grad_k = scale sum_i ds q,
- * grad_k and grad_v summed over the heads that share them.  p and ds are
+ * grad_k and grad_v summed over the heads that share them.  out and lse may
+ * stem from this call's keys or be joined from calls over several parts of the
+ * keys, each of which then gets its share of the gradients: delta is that of
+ * the given out (grad_k takes sum_j p grad_out.v over the call's keys, which
+ * lacks the rounding of out, as far as it lies within that rounding).  p and ds are
  * rounded to the input type for their products, sums are binary32, results
  * are rounded once.  Rows that attend to nothing get grad_q = 0, keys that no
  * row sees grad_k = grad_v = 0.  In fp16, ds below 2^-14 loses digits as any

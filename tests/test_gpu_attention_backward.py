@@ -222,3 +222,39 @@ def test_unseen_rows_leave_no_mark_on_capped_scores(dim):
     got = attention_backward(dout, q, k, v, out2, lse2, **kw)
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("softcap", [0.0, 8.0])
+@pytest.mark.parametrize("cut", [1, 200, 333])
+def test_keys_in_two_calls_joined_by_lse(dtype, dim, softcap, cut):
+    """The keys in two parts: out and lse joined, and each part's backward from the joined ones.  The joined out is
+    off by its own rounding, and by that of the parts and of their weights (each at most u sum p |v|): what
+    out_bound holds.  Each part's dq is rounded once."""
+    q, k, v = make(dtype, 2, 4, 2, 150, 400, dim, seed=12)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(13), device="cuda").to(dtype)
+    parts = [(k[:, :, a:b], v[:, :, a:b]) for a, b in ((0, cut), (cut, 400))]
+    (o1, l1), (o2, l2) = (attention(q, *p, softcap=softcap) for p in parts)
+    lse = torch.logaddexp(l1, l2)
+    out = ((l1 - lse).exp()[..., None] * o1.float() + (l2 - lse).exp()[..., None] * o2.float()).to(dtype)
+    (q1, k1, v1), (q2, k2, v2) = (attention_backward(dout, q, *p, out, lse, softcap=softcap) for p in parts)
+    vis, dist = B.visible(150, 400, 2)
+    want = B.attention(q, k, v, vis, dist, dout=dout, softcap=softcap)
+    B.assert_within(q1.double() + q2.double(), want["dq"],
+                    want["dq_bound"] + B.U[dtype] * (q1.double().abs() + q2.double().abs()) + 2 * B.TINY[dtype], "dq")
+    B.assert_within(torch.cat([k1, k2], 2), want["dk"], want["dk_bound"], "dk")
+    B.assert_within(torch.cat([v1, v2], 2), want["dv"], want["dv_bound"], "dv")
+
+
+def test_out_and_lse_of_more_keys_than_the_call_has():
+    """Keys that hold all but a little of the weight elsewhere: delta is that of the given out."""
+    q, k, v = make(torch.float16, 1, 2, 2, 200, 300, 64, seed=14)
+    v[:, :, 150:] += 3  # the other part's values lean one way
+    dout = torch.randn_like(q)
+    out, lse = attention(q, k, v)
+    _, dk, dv = attention_backward(dout, q, k[:, :, :150], v[:, :, :150], out, lse)
+    vis, dist = B.visible(200, 300, 1)
+    want = B.attention(q, k, v, vis, dist, dout=dout)
+    B.assert_within(dk, want["dk"][:, :, :150], want["dk_bound"][:, :, :150], "dk")
+    B.assert_within(dv, want["dv"][:, :, :150], want["dv_bound"][:, :, :150], "dv")

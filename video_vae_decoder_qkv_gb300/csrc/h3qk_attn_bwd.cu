@@ -50,7 +50,7 @@ struct BwdShared {
     uint64_t s_full[2], s_free[2], dp_full[2], p_ready[2], ds_ready[2], st_full[2], st_empty[2];
     uint32_t tmem;
     int stop;
-    alignas(16) float lse[2][kTile];
+    alignas(16) float lse[2][kTile];  // (dq: how far out's rounding moves delta)
     alignas(16) float delta[2][kTile];
 };
 
@@ -60,6 +60,12 @@ template <bool BF16>
 constexpr float kLift = BF16 ? 0.0f : 10.0f;
 template <bool BF16>
 constexpr float kDrop = BF16 ? 1.0f : 1.0f / 1024.0f;
+
+// A rounding to the type: relative, and absolute among fp16's smallest numbers.
+template <bool BF16>
+constexpr float kRound = BF16 ? 1.0f / 256.0f : 1.0f / 2048.0f;
+template <bool BF16>
+constexpr float kTiny = BF16 ? 0.0f : 1.0f / 33554432.0f;
 
 // The tile, head and item of a block.  The grid is [tiles][heads][items], so a
 // head's tiles follow one another and its streamed rows stay in L2.  Causal
@@ -345,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // delta = dout . out of the row; each half of the warps takes every other
         // 8 channels.  (out is rounded to its type, which is most of dq's error
         // on rows with a few heavy keys; the exact delta is known only after the
-        // loop, in time for dk and dv.)
-        float part = 0.0f;
+        // loop, in time for dk.)
+        float part = 0.0f, off = 0.0f;
         if (has) {
             const uint16_t* o = p.out + s.item * p.os.item + head * p.os.head + row * p.os.row;
             const uint16_t* d = p.dout + s.item * p.dos.item + head * p.dos.head + row * p.dos.row;
@@ -359,12 +365,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 a = widen_pair<BF16>(ow[e]), b = widen_pair<BF16>(dw[e]);
                     part = fmaf(a.x, b.x, part);
                     part = fmaf(a.y, b.y, part);
+                    off = fmaf(fmaf(fabsf(a.x), kRound<BF16>, kTiny<BF16>), fabsf(b.x), off);
+                    off = fmaf(fmaf(fabsf(a.y), kRound<BF16>, kTiny<BF16>), fabsf(b.y), off);
                 }
             }
         }
         sh.delta[g][r] = part;
+        sh.lse[g][r] = off;
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const float delta = sh.delta[0][r] + sh.delta[1][r];
+        const float most = 2.0f * (sh.lse[0][r] + sh.lse[1][r]);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (g == 0) reinterpret_cast<float2*>(sh.lse)[r] = make_float2(delta - most, delta + most);
         const int64_t stat = (static_cast<int64_t>(s.item) * p.heads + head) * p.q_rows + row;
         float lse = INFINITY;  // p = 0
         if (has) {
@@ -466,13 +478,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && n > 0) ok = bar_wait(done, 0, stop);
         tc_fence_after();
-        // delta = sum_j p dp without the rounding of out, for dk and dv.
+        // For dk, delta = sum_j p dp without the rounding of out.  That needs all
+        // the keys that out and lse stem from; where other calls took some of
+        // them, the sum differs from dout . out by more than out's rounding (and as
+        // much again for that of p) explains, and is held to that.
         float lo, hi;
         unpair(lo, hi, add_pair(add_pair(exact[0], exact[1]), add_pair(exact[2], exact[3])));
         asm volatile("bar.sync 1, 256;" ::: "memory");  // all have read the first delta
         sh.delta[g][r] = lo + hi;
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (g == 0 && has) p.delta[stat] = sh.delta[0][r] + sh.delta[1][r];
+        if (g == 0 && has) {
+            const float2 within = reinterpret_cast<const float2*>(sh.lse)[r];
+            p.delta[stat] = fminf(fmaxf(sh.delta[0][r] + sh.delta[1][r], within.x), within.y);
+        }
         uint16_t* dst = p.dq + s.item * p.dqs.item + head * p.dqs.head + row * p.dqs.row;
         write_row<BF16, DP / 2>(dst, t_dq + lanes + g * (DP / 2), g * (DP / 2), p.dim, p.scale, !(ok && has && n > 0),
                                 i_row < s.span);
