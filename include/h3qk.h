@@ -528,8 +528,9 @@ typedef struct h3qk_attn {
  * their own.  Errors and asynchrony as for h3qk_prepare.
  *
  * The tile kernels' waits are bounded: should one ever run out (it cannot in
- * a working program), the kernel ends, the rows concerned have lse = NaN and
- * h3qk_attention_stuck() counts the blocks.
+ * a working program), the kernel ends, the rows concerned have lse = NaN
+ * (backward: NaN in grad_q, and in grad_k and grad_v of the keys concerned)
+ * and h3qk_attention_stuck() counts the blocks.
  */
 size_t h3qk_attention_workspace_bytes(const h3qk_attn* call);
 h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t stream);

@@ -67,6 +67,10 @@ constexpr float kRound = BF16 ? 1.0f / 256.0f : 1.0f / 2048.0f;
 template <bool BF16>
 constexpr float kTiny = BF16 ? 0.0f : 1.0f / 33554432.0f;
 
+// What a block whose waits ran out leaves in its rows (by way of delta, also in
+// the gradients of the keys that they see).
+__device__ __forceinline__ float given_up() { return __int_as_float(0x7fc00000); }
+
 // The tile, head and item of a block.  The grid is [tiles][heads][items], so a
 // head's tiles follow one another and its streamed rows stay in L2.  Causal
 // tiles are of unequal length: the longest of all heads (late rows, early keys)
@@ -485,15 +489,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lo, hi;
         unpair(lo, hi, add_pair(add_pair(exact[0], exact[1]), add_pair(exact[2], exact[3])));
         asm volatile("bar.sync 1, 256;" ::: "memory");  // all have read the first delta
-        sh.delta[g][r] = lo + hi;
+        sh.delta[g][r] = ok ? lo + hi : given_up();
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (g == 0 && has) {
             const float2 within = reinterpret_cast<const float2*>(sh.lse)[r];
-            p.delta[stat] = fminf(fmaxf(sh.delta[0][r] + sh.delta[1][r], within.x), within.y);
+            const float sum = sh.delta[0][r] + sh.delta[1][r];
+            p.delta[stat] = sum == sum ? fminf(fmaxf(sum, within.x), within.y) : sum;
         }
         uint16_t* dst = p.dq + s.item * p.dqs.item + head * p.dqs.head + row * p.dqs.row;
-        write_row<BF16, DP / 2>(dst, t_dq + lanes + g * (DP / 2), g * (DP / 2), p.dim, p.scale, !(ok && has && n > 0),
-                                i_row < s.span);
+        write_row<BF16, DP / 2>(dst, t_dq + lanes + g * (DP / 2), g * (DP / 2), p.dim, ok ? p.scale : given_up(),
+                                !(has && n > 0), i_row < s.span);
         tc_fence_before();
     } else {
         regs_down<h3qk_core::kOtherRegs>();
@@ -803,13 +808,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && n > 0) ok = bar_wait(done, 0, stop);
         tc_fence_after();
         const int64_t row = s.k0 + key;
-        const bool zero = !(ok && n > 0 && key < s.keys);
+        const bool zero = !(n > 0 && key < s.keys);
         if (g == 0)
             write_row<BF16, DP>(p.dv + s.item * p.dvs.item + kv_head * p.dvs.head + row * p.dvs.row, t_dv + lanes, 0,
-                                p.dim, kDrop<BF16>, zero, key < s.span);
+                                p.dim, ok ? kDrop<BF16> : given_up(), zero, key < s.span);
         else
             write_row<BF16, DP>(p.dk + s.item * p.dks.item + kv_head * p.dks.head + row * p.dks.row, t_dk + lanes, 0,
-                                p.dim, p.scale, zero, key < s.span);
+                                p.dim, ok ? p.scale : given_up(), zero, key < s.span);
         tc_fence_before();
     } else {
         regs_down<h3qk_core::kOtherRegs>();
