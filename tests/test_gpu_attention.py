@@ -302,3 +302,19 @@ def test_a_key_concerns_only_the_rows_that_see_it(softcap):
     got = attention(q, k, v, causal=True, softcap=softcap)
     assert torch.equal(got[0][:, :, :77], want[0][:, :, :77]) and torch.equal(got[1][:, :, :77], want[1][:, :, :77])
     assert got[0][:, :, 77:].isnan().all()
+
+
+@pytest.mark.parametrize("sq", [1, 300])
+def test_distances_past_24_bits(sq):
+    """Positions that binary32 cannot hold, whose distances it can."""
+    n, near = (1 << 24) + 40, 2000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(1, 1, n, 8, generator=g, device="cuda", dtype=torch.float16) for _ in range(2))
+    q = torch.randn(1, 2, sq, 8, generator=g, device="cuda", dtype=torch.float16)
+    slopes = torch.tensor([0.5, 1.0], device="cuda")
+    got = attention(q, k, v, slopes=slopes, causal=True)
+    # what is further away than `near` weighs less than e^-800
+    vis, dist = B.visible(sq, near, 1, causal=True)
+    want = B.attention(q, k[:, :, n - near:], v[:, :, n - near:], vis, dist, slopes=slopes)
+    B.assert_within(got[1], want["lse"], want["lse_bound"], "lse")
+    B.assert_within(got[0], want["out"], want["out_bound"], "out")

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
     // The two rows of this lane.
     int lim[2], head[2], row[2];
     bool has[2];
-    float far[2];
+    int at[2];  // positions among the keys
     Bend bend[2];
     int most = 0;
 #pragma unroll
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
         row[h] = has[h] ? t % p.q_rows : 0;
         lim[h] = has[h] && row[h] < s.rows ? max(h3qk_core::limit_of(s, p.causal, row[h]), 0) : 0;
         most = max(most, lim[h]);
-        far[h] = static_cast<float>(s.start + row[h]);
+        at[h] = s.start + row[h];
         bend[h] = h3qk_core::bend_of(p, head[h]);
     }
 #pragma unroll
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
                         const int key = j + 8 * t + 2 * c + e;
                         float v = sc[t][2 * h + e] * bend[h].in;
                         if (capped) v = fmaf(-2.0f * bend[h].cap, rcp_fast(exp2_fast(v) + 1.0f), bend[h].cap);
-                        v = fmaf(-bend[h].slope, fabsf(far[h] - static_cast<float>(key)), v);
+                        v = fmaf(-bend[h].slope, fabsf(static_cast<float>(at[h] - key)), v);
                         v = key < lim[h] ? v : -INFINITY;
                         sc[t][2 * h + e] = v;
                         top = fmaxf(top, v);
