@@ -258,3 +258,13 @@ def test_out_and_lse_of_more_keys_than_the_call_has():
     want = B.attention(q, k, v, vis, dist, dout=dout)
     B.assert_within(dk, want["dk"][:, :, :150], want["dk_bound"][:, :, :150], "dk")
     B.assert_within(dv, want["dv"][:, :, :150], want["dv_bound"][:, :, :150], "dv")
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1), (2, 1, 150, 64), (2, 4, 1, 64), (1, 4, 150, 1)])
+def test_an_expanded_gradient(shape):
+    """What the sum of the output gives, or of some of its dimensions."""
+    q, k, v = make(torch.bfloat16, 2, 4, 2, 150, 150, 64)
+    out, lse = attention(q, k, v)
+    dout = torch.randn(shape, device="cuda").to(q.dtype).expand(q.shape)
+    want = attention_backward(dout.contiguous(), q, k, v, out, lse)
+    assert all(torch.equal(a, b) for a, b in zip(attention_backward(dout, q, k, v, out, lse), want))

@@ -214,3 +214,13 @@ def test_widths_at_the_shared_memory_limit_as_first_calls():
     r = subprocess.run([sys.executable, "-c", _FIRST_CALLS, here, os.path.dirname(here)], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (1, 640), (30, 1)])
+def test_an_expanded_gradient(shape):
+    """What the sum of the output gives, or of its rows or columns."""
+    x, _, w, b = _make(torch.float16, 30, 640)
+    _, stats = layer_norm(x, w, b)
+    dy = torch.randn(shape, device="cuda").half().expand(30, 640)
+    want = layer_norm_backward(dy.contiguous(), x, w, stats)
+    assert all(torch.equal(p, q) for p, q in zip(layer_norm_backward(dy, x, w, stats), want))

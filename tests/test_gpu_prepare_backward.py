@@ -178,3 +178,12 @@ def test_rows_of_any_size(monkeypatch, size, eps):
     B.assert_within(got, want, B.U[dtype] * want.abs() + B.TINY[dtype] + 32 * B.U32 * terms, "grad_qkv")
     for g, w, s in ((gq, dws[0], dw_terms[0]), (gk, dws[1], dw_terms[1])):
         B.assert_within(g, w, (48 * 3 + 64) * B.U32 * s + 1e-30, "grad_w")
+
+
+def test_expanded_gradients():
+    """What the sum of an output gives."""
+    qkv, wq, wk, pos, grads = _make(torch.float16, 2, 21, 3, 64, 3)
+    kw = dict(heads=3, head_dim=64, rotary_dim=48, batch=2)
+    grads = [g[:1, :1, :1, :1].expand(g.shape) for g in grads]
+    want = prepare_backward(*(g.contiguous() for g in grads), qkv, wq, wk, pos, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(prepare_backward(*grads, qkv, wq, wk, pos, **kw), want))

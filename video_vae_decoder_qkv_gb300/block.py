@@ -5,6 +5,11 @@ As in ``h3qk``, this only checks tensors and passes their addresses: each
 operator runs in the library's CUDA kernels on the current stream, or on the
 one passed as ``stream`` (the call then behaves as if it were the current
 one), and workspaces come from torch's allocator unless the caller passes one.
+
+The results carry no autograd graph: in training the forward and its
+``..._backward`` are the two halves of a torch.autograd.Function
+(examples/attention_block.py has one for each operator).  Incoming gradients
+may be expanded tensors, as autograd makes them; such are copied first.
 """
 from __future__ import annotations
 
@@ -118,6 +123,12 @@ def _workspace(workspace, nbytes, dev):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _spread(grad):
+    """A gradient that autograd hands over expanded (one value for many
+    elements, as the sum of an output gives), written out; others as they are."""
+    return grad.contiguous() if grad is not None and 0 in grad.stride() else grad
+
+
 def _need_rows(x, name, dtypes):
     if x.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {x.dtype}")
@@ -187,6 +198,7 @@ def layer_norm_backward(grad_out, x, weight, stats, *, batch: int = 1, need_weig
     (grad_x, grad_weight, grad_bias); the last two are float32 of the
     weight's shape, summed over the rows that share them, or None without a
     weight or with ``need_weight_grad=False`` (h3qk_layer_norm_backward)."""
+    grad_out = _spread(grad_out)
     _need_rows(x, "x", _DTYPES)
     _need_rows(grad_out, "grad_out", (x.dtype,))
     rows, width = x.shape
@@ -248,6 +260,7 @@ def prepare_backward(grad_q, grad_k, grad_v, qkv, norm_wq, norm_wk, positions, *
     _need_common(qkv, norm_wq, norm_wk, positions, tokens=tokens, heads=heads, head_dim=head_dim,
                  rotary_dim=rotary_dim, n_axes=n_axes, batch=batch, valid_lens=valid_lens, device=dev)
     n = tokens * heads * head_dim
+    grad_q, grad_k, grad_v = _spread(grad_q), _spread(grad_k), _spread(grad_v)
     for t, name in ((grad_q, "grad_q"), (grad_k, "grad_k"), (grad_v, "grad_v")):
         _need(t, name, device=dev, dtypes=(qkv.dtype,), numel=n)
     if out is None:
@@ -406,6 +419,7 @@ def attention_backward(grad_out, q, k, v, out, lse, *, scale: float | None = Non
     (h3qk_attention_backward)."""
     batch, heads, kv_heads, sq, sk, dim, docs, strides, lists = _attn_common(
         q, k, v, scale, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
+    grad_out = _spread(grad_out)
     dev = q.device
     row, key = (batch, heads, sq, dim), (batch, kv_heads, sk, dim)
     out_strides = _need_heads(out, "out", row, q.dtype, dev)
