@@ -299,3 +299,16 @@ def test_a_calls_workspace_does_not_depend_on_earlier_ones(monkeypatch, q_rows, 
                 packed = passed.pop()
                 given = block._ATTN.unpack(packed)[28]
                 assert given == block._fn("h3qk_attention_workspace_bytes")(packed), (list(first), list(second))
+
+
+@pytest.mark.parametrize("masks,cut", [(dict(), True), (dict(causal=1), False), (dict(causal=1, prefix_lens=A), True),
+                                       (dict(q_lens=A), False)])
+def test_which_last_rounds_are_cut(masks, cut):
+    """176 tiles: a round and a bit of them.  Causal tiles go longest first, and what is left at the end is short."""
+    f = dict(dtype=h3qk.FP16, batch=1, heads=16, kv_heads=16, head_dim=64, causal=0, docs=0, reserved=0, scale=0.0,
+             softcap=0.0, q_rows=2600, kv_rows=2600, q=A, k=A, v=A, out=A, lse=A, grad_out=0, grad_q=0, grad_k=0,
+             grad_v=0, slopes=0, prefix_lens=0, doc_offsets=0, q_lens=0, kv_lens=0, q_starts=0, workspace=0,
+             workspace_bytes=0)
+    f.update(masks)
+    size = block._fn("h3qk_attention_workspace_bytes")(block._ATTN.pack(*f.values(), *[0] * 24))
+    assert (size > 0) == cut

@@ -395,7 +395,7 @@ def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slop
 
     # The size depends on the sizes, the masks' kind and which lists there are
     # (the library does not read them), not on any value.
-    shape = (batch, heads, kv_heads, sq, sk, dim, causal, docs, *(t != 0 for t in lists))
+    shape = (batch, heads, kv_heads, sq, sk, dim, bool(causal), docs, *(t != 0 for t in lists))
     need = _sizes.get(("h3qk_attention_workspace_bytes", dev.index, shape))
     if need is None:
         need = _size("h3qk_attention_workspace_bytes", dev, args(0, 0), key=shape)
