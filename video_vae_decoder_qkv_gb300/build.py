@@ -10,6 +10,7 @@ statically so the library needs nothing but the driver.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -45,6 +46,28 @@ LINK_FLAGS = ["-shared", "-cudart", "static", "-gencode", "arch=compute_103a,cod
 NVCC_FLAGS = COMPILE_FLAGS + ["--threads", "0", "-shared", "-cudart", "static"]
 
 
+# The attention tile kernels share their launch's registers out among their
+# warps, and are refused at run time when the compiler gave them any other
+# number (kLaunchRegs in csrc/h3qk_attn.cuh).
+TILE_KERNELS = re.compile(r"attention_(dq_|dkv_)?kernelI")
+TILE_KERNEL_REGS = 168
+
+
+def refused_kernels(ptxas_log: str) -> list[str]:
+    """Tile kernels in ptxas' report (-Xptxas -v) that would be refused at run time."""
+    found, name = [], None
+    for line in ptxas_log.splitlines():
+        entry = re.search(r"Compiling entry function '(\S+)'", line)
+        if entry:
+            name = entry.group(1)
+        used = re.search(r"Used (\d+) registers", line)
+        if used and name:
+            if TILE_KERNELS.search(name) and int(used.group(1)) != TILE_KERNEL_REGS:
+                found.append(f"{name}: {used.group(1)} registers instead of {TILE_KERNEL_REGS}")
+            name = None
+    return found
+
+
 def nvcc_path() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -73,13 +96,14 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     def compile_one(src_obj):
         src, obj = src_obj
         cmd = [nvcc_path(), *COMPILE_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC, "-c", "-o", obj, src]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
+        cmd.insert(1, "-Xptxas=-v")
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode:
             sys.stdout.write(r.stdout)
             sys.stderr.write(r.stderr)
         r.check_returncode()
+        for kernel in refused_kernels(r.stdout + r.stderr):
+            sys.stderr.write(f"warning: attention will be refused at run time: {kernel}\n")
 
     try:
         with ThreadPoolExecutor(len(SOURCES)) as ex:
