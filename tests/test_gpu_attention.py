@@ -318,3 +318,28 @@ def test_distances_past_24_bits(sq):
     want = B.attention(q, k[:, :, n - near:], v[:, :, n - near:], vis, dist, slopes=slopes)
     B.assert_within(got[1], want["lse"], want["lse_bound"], "lse")
     B.assert_within(got[0], want["out"], want["out_bound"], "out")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("sq,dim", [(1, 64), (300, 64), (300, 128)])
+@pytest.mark.parametrize("softcap,gain", [(1025.0, 1.0), (1025.0, 8.0), (3e4, 1.0), (1e6, 1.0), (1e6, 4.0), (1e30, 1.0)])
+def test_large_caps(dtype, sq, dim, softcap, gain):
+    """A cap far above the scores leaves them their digits: the scores' bounds without the cap's share."""
+    q, k, v = make(dtype, 1, 2, 2, sq, 700, dim, seed=15, gain=gain)
+    slopes = torch.tensor([0.02, 0.0], device="cuda")
+    vis, dist = B.visible(sq, 700, 1)
+    for s in (None, slopes):
+        out, lse = attention(q, k, v, softcap=softcap, slopes=s)
+        want = B.attention(q, k, v, vis, dist, softcap=softcap, slopes=s)
+        bound = B.attention(q, k, v, vis, dist, slopes=s)
+        B.assert_within(lse, want["lse"], bound["lse_bound"], "lse")
+        B.assert_within(out, want["out"], bound["out_bound"], "out")
+
+
+@pytest.mark.parametrize("sq", [1, 300])
+@pytest.mark.parametrize("softcap", [1e-3, 1e-30, 1e-38, 1e-40])
+def test_small_caps(sq, softcap):
+    """A cap far below the scores makes all weights alike, those of scores of 0 too."""
+    q, k, v = make(torch.float16, 1, 2, 2, sq, 300, 64, seed=16)
+    k[:, :, ::5] = 0
+    check(q, k, v, softcap=softcap)

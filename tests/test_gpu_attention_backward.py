@@ -268,3 +268,21 @@ def test_an_expanded_gradient(shape):
     dout = torch.randn(shape, device="cuda").to(q.dtype).expand(q.shape)
     want = attention_backward(dout.contiguous(), q, k, v, out, lse)
     assert all(torch.equal(a, b) for a, b in zip(attention_backward(dout, q, k, v, out, lse), want))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("softcap,gain", [(1025.0, 1.0), (1025.0, 6.0), (3e4, 1.0), (1e6, 1.0), (1e30, 1.0)])
+def test_large_caps(dtype, dim, softcap, gain):
+    """A cap far above the scores: the gradients' bounds without the cap's share."""
+    q, k, v = make(dtype, 1, 2, 1, 300, 300, dim, seed=15, gain=gain)
+    dout = torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(17), device="cuda").to(dtype)
+    vis, dist = B.visible(300, 300, 1, causal=True)
+    for slopes in (None, torch.tensor([0.02, 0.0], device="cuda")):
+        kw = dict(softcap=softcap, slopes=slopes, causal=True)
+        out, lse = attention(q, k, v, **kw)
+        grads = attention_backward(dout, q, k, v, out, lse, **kw)
+        want = B.attention(q, k, v, vis, dist, dout=dout, softcap=softcap, slopes=slopes)
+        bound = B.attention(q, k, v, vis, dist, dout=dout, slopes=slopes)
+        for name, got in zip(("dq", "dk", "dv"), grads):
+            B.assert_within(got, want[name], bound[name + "_bound"], name)

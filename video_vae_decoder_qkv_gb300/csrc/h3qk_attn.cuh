@@ -133,10 +133,19 @@ inline int64_t tiles_of(const Params& p, int64_t rows, int size)
 // 2^x, 16 a cycle and SM, and would bound the capped kernels; a reciprocal
 // from multiply-adds measured slower).
 // Which bends a call has is fixed at compile time.
-enum Bends { kPlain = 0, kCapped = 1, kSloped = 2 };
+//
+// The error is absolute in tanh, so a cap far above the scores costs them
+// digits: cap 2^-21.  Beyond kWideCap, where that passes 2^-11 (fp16 rounds p
+// to 2^-12), scores below a quarter of the cap take tanh's series instead, to
+// a relative 2^-22.  That is an instance of its own: 16 heads of 4096 x 128,
+// bf16, take 319 us forward and
+// 777 backward with a cap of 2000, 184 and 559 with one of 30.
+enum Bends { kPlain = 0, kCapped = 1, kSloped = 2, kWide = 4 };
+constexpr float kWideCap = 1024.0f;
 
 struct Bend {
     float in;     // scale * 2 log2(e) / cap, or scale * log2(e) without a cap
+    float plain;  // scale * log2(e)
     float cap;    // cap * log2(e)
     float slope;  // slope * log2(e)
 };
@@ -144,10 +153,28 @@ struct Bend {
 __device__ __forceinline__ Bend bend_of(const Params& p, int head)
 {
     Bend b;
-    b.in = p.cap > 0.0f ? p.scale * 2.0f * kLog2e / p.cap : p.scale * kLog2e;
+    b.plain = p.scale * kLog2e;
+    // (the smallest caps would make this infinite, and a score of 0 NaN)
+    b.in = p.cap > 0.0f ? fminf(p.scale * 2.0f * kLog2e / p.cap, 3.0e38f) : b.plain;
     b.cap = p.cap * kLog2e;
     b.slope = p.slopes ? __ldg(p.slopes + head) * kLog2e : 0.0f;
     return b;
+}
+
+// tanh(u) / u for |u| < 1/4, given w = (2 u log2 e)^2, to 2^-26: 1 - u^2/3 +
+// 2u^4/15 - 17u^6/315 + 62u^8/2835, tanh's Taylor series.  kSmall is the bound
+// on |2 u log2 e|.
+constexpr float kSmall = 0.72f;
+constexpr float kHalfLn2Sq = 0.25f * kLn2 * kLn2;
+__device__ __forceinline__ uint64_t tanh_series(uint64_t w)
+{
+    using namespace h3qk_tc;
+    auto both = [](float v) { return pair(v, v); };
+    const uint64_t t = mul_pair(w, both(kHalfLn2Sq));
+    uint64_t p = fma_pair(t, both(62.0f / 2835.0f), both(-17.0f / 315.0f));
+    p = fma_pair(t, p, both(2.0f / 15.0f));
+    p = fma_pair(t, p, both(-1.0f / 3.0f));
+    return fma_pair(t, p, both(1.0f));
 }
 
 // The exponents of four raw scores (two pairs) at distances far, far + dir,
@@ -157,8 +184,12 @@ __device__ __forceinline__ void bend_four(uint64_t (&z)[2], const Bend& b, float
 {
     using namespace h3qk_tc;
     const uint64_t in = pair(b.in, b.in);
+    [[maybe_unused]] uint64_t flat[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) z[i] = mul_pair(z[i], in);
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (BENDS & kWide) flat[i] = mul_pair(z[i], pair(b.plain, b.plain));
+        z[i] = mul_pair(z[i], in);
+    }
     if constexpr (BENDS & kCapped) {
         const uint64_t one = pair(1.0f, 1.0f), cap = pair(b.cap, b.cap), less = pair(-b.cap, -b.cap);
         float lo[2], hi[2];
@@ -180,7 +211,16 @@ __device__ __forceinline__ void bend_four(uint64_t (&z)[2], const Bend& b, float
             if constexpr (KEEP) keep[i] = mul_pair(mul_pair(e[i], pair(4.0f, 4.0f)), mul_pair(r[i], r[i]));
             float t_lo, t_hi;
             unpair(t_lo, t_hi, mul_pair(fma_pair(e[i], less, cap), r[i]));
-            z[i] = pair(copysignf(t_lo, lo[i]), copysignf(t_hi, hi[i]));
+            t_lo = copysignf(t_lo, lo[i]);
+            t_hi = copysignf(t_hi, hi[i]);
+            if constexpr (BENDS & kWide) {
+                const uint64_t both_in = pair(lo[i], hi[i]);
+                float f_lo, f_hi;
+                unpair(f_lo, f_hi, mul_pair(flat[i], tanh_series(mul_pair(both_in, both_in))));
+                if (fabsf(lo[i]) < kSmall) t_lo = f_lo;
+                if (fabsf(hi[i]) < kSmall) t_hi = f_hi;
+            }
+            z[i] = pair(t_lo, t_hi);
         }
     }
     if constexpr (BENDS & kSloped) {

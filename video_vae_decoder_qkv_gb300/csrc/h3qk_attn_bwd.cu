@@ -857,6 +857,7 @@ template <bool BF16, int DP>
 cudaError_t by_bends(const Params& p, const h3qk_core::Maps& m, cudaStream_t st)
 {
     using namespace h3qk_core;
+    if (p.cap > kWideCap) return launch<BF16, DP, kCapped | kSloped | kWide>(p, m, st);  // (slopes of 0 where there are none)
     if (p.cap > 0.0f) return p.slopes ? launch<BF16, DP, kCapped | kSloped>(p, m, st) : launch<BF16, DP, kCapped>(p, m, st);
     return p.slopes ? launch<BF16, DP, kSloped>(p, m, st) : launch<BF16, DP, kPlain>(p, m, st);
 }

@@ -194,17 +194,27 @@ __global__ void __launch_bounds__(32 * kWarps) attention_split_kernel(const __gr
             for (int h = 0; h < 2; ++h) {
                 float top = m[h];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t) {
+                    float small[2];
+                    if (capped) {
+                        const uint64_t raw = pair(sc[t][2 * h], sc[t][2 * h + 1]), z = mul_pair(raw, pair(bend[h].in, bend[h].in));
+                        const uint64_t flat = mul_pair(raw, pair(bend[h].plain, bend[h].plain));
+                        unpair(small[0], small[1], mul_pair(flat, h3qk_core::tanh_series(mul_pair(z, z))));
+                    }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int key = j + 8 * t + 2 * c + e;
                         float v = sc[t][2 * h + e] * bend[h].in;
-                        if (capped) v = fmaf(-2.0f * bend[h].cap, rcp_fast(exp2_fast(v) + 1.0f), bend[h].cap);
+                        if (capped) {
+                            const float bent = fmaf(-2.0f * bend[h].cap, rcp_fast(exp2_fast(v) + 1.0f), bend[h].cap);
+                            v = fabsf(v) < h3qk_core::kSmall ? small[e] : bent;
+                        }
                         v = fmaf(-bend[h].slope, fabsf(static_cast<float>(at[h] - key)), v);
                         v = key < lim[h] ? v : -INFINITY;
                         sc[t][2 * h + e] = v;
                         top = fmaxf(top, v);
                     }
+                }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 f[h] = top == -INFINITY ? 1.0f : exp2_fast(m[h] - top);
