@@ -286,3 +286,16 @@ def test_large_caps(dtype, dim, softcap, gain):
         bound = B.attention(q, k, v, vis, dist, dout=dout, slopes=slopes)
         for name, got in zip(("dq", "dk", "dv"), grads):
             B.assert_within(got, want[name], bound[name + "_bound"], name)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_keys_past_the_last_row_get_zeros_whatever_they_hold(softcap, bad):
+    """Causal rows that end before the keys do, and items whose rows all come before the first key."""
+    q, k, v = make(torch.float16, 4, 4, 2, 70, 300, 64, seed=18)
+    starts = [20, 229, 240, -80]
+    for b, start in enumerate(starts):
+        k[b, :, max(start + 70, 0):] = bad
+        v[b, :, max(start + 70, 0):] = bad
+    check(q, k, v, causal=True, q_starts=starts, softcap=softcap)
+    check(q, k, v, causal=True, q_starts=starts, softcap=softcap, kv_lens=[299, 256, 300, 300])

@@ -808,7 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && n > 0) ok = bar_wait(done, 0, stop);
         tc_fence_after();
         const int64_t row = s.k0 + key;
-        const bool zero = !(n > 0 && key < s.keys);
+        // keys that some row sees; others get zeros, whatever they hold
+        const bool zero = !(n > 0 && key < s.keys && from < s.rows);
         if (g == 0)
             write_row<BF16, DP>(p.dv + s.item * p.dvs.item + kv_head * p.dvs.head + row * p.dvs.row, t_dv + lanes, 0,
                                 p.dim, ok ? kDrop<BF16> : given_up(), zero, key < s.span);
