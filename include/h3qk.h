@@ -409,7 +409,7 @@ h3qk_status h3qk_scaled_residual(const float* residual, const void* branch, h3qk
  *              rows that start on 16-byte boundaries are read fastest.
  *   width      1 to 16384.
  *   weight, bias  float [groups, width], each NULL for 1 and 0.  Rows are
- *              cut into `groups` equal runs, run g using row g (an adaptive
+ *              cut into `groups` (1 to 65535) equal runs, run g using row g (an adaptive
  *              norm with a scale and shift per item); groups 1 shares one.
  *   out        [rows, width] contiguous, of dtype; may not overlap an input.
  *   stats      float [rows, 2], 8-byte aligned.
@@ -548,8 +548,8 @@ h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t stream);
  * lacks the rounding of out, as far as it lies within that rounding).  p and ds are
  * rounded to the input type for their products, sums are binary32, results
  * are rounded once.  Rows that attend to nothing get grad_q = 0, keys that no
- * row sees grad_k = grad_v = 0.  In fp16, ds below 2^-14 loses digits as any
- * fp16 value does: scale the loss where gradients are that small.  The
+ * row sees grad_k = grad_v = 0.  In fp16, ds below 2^-14 loses digits and above
+ * 65504 is infinite, as any fp16 value: scale the loss to stay between.  The
  * slopes get no gradient.  The workspace holds one float per query row.
  */
 size_t h3qk_attention_backward_workspace_bytes(const h3qk_attn* call);

@@ -138,8 +138,8 @@ inline int64_t tiles_of(const Params& p, int64_t rows, int size)
 // digits: cap 2^-21.  Beyond kWideCap, where that passes 2^-11 (fp16 rounds p
 // to 2^-12), scores below a quarter of the cap take tanh's series instead, to
 // a relative 2^-22.  That is an instance of its own: 16 heads of 4096 x 128,
-// bf16, take 319 us forward and
-// 777 backward with a cap of 2000, 184 and 559 with one of 30.
+// bf16, take 319 us forward and 777 backward with a cap of 2000, 184 and 559
+// with one of 30.
 enum Bends { kPlain = 0, kCapped = 1, kSloped = 2, kWide = 4 };
 constexpr float kWideCap = 1024.0f;
 

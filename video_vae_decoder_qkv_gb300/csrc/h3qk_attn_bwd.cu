@@ -11,9 +11,10 @@
 // 40 heads of 8160 x 8160 x 128, bf16: dq 1.25 ms, dk and dv 1.53 ms: the
 // tensor unit bounds both, at 1.63 and 1.78 PFLOP/s of products run (1.23 of
 // the 10 D a pair that the gradient needs).  32 heads of 8192 x 8192 x 64,
-// fp16: 0.74 and 0.90 ms; there the arithmetic bounds them (about 1,000 and
-// 1,300 cycles a tile of 128 x 128 against 768 and 1,024 of products).  Twice
-// as many warps on the same arithmetic measured 7 % slower.
+// fp16: 0.76 and 0.92 ms; there the arithmetic takes longer (about 1,000 and
+// 1,300 cycles a tile of 128 x 128 against 768 and 1,024 of products), mostly
+// in waits: counters show the tensor unit at 44 and 49 %, 2^x at 29 and 26 %.
+// Twice as many warps on the same arithmetic measured 7 % slower.
 //
 // Both keep scores and dp in TMEM with the block's own rows as lanes, eight
 // warps turn them into p and ds (one thread a row and half the columns), and

@@ -23,11 +23,16 @@
 //
 // Bound: at head_dim 128 by the tensor unit (2 x 512 cycles a tile and group;
 // a group's softmax takes about 1,100 and overlaps the other group's products).
-// 40 heads of 8160 x 8160 x 128, bf16: 0.80 ms, 1.70 PFLOP/s, 91 % of the
-// measured product rate.  Up to 64 the softmax bounds it (per score one 2^x at
-// 32 a cycle and SM, and about four instructions): 32 heads of 8192 x 8192 x
-// 64, fp16: 0.46 ms, 1.19 PFLOP/s.  With a cap, two 2^x and a quarter of a
-// reciprocal a score: 0.90 PFLOP/s at 128.
+// 40 heads of 8160 x 8160 x 128, bf16: 0.79 ms in short runs, 1.73 PFLOP/s, 93 %
+// of the rate that short products measured; 0.86 ms where passes follow one
+// another under the power cap, 93 % of the rate of products that do.
+// Up to 64 the softmax takes longer than the products (per score one 2^x at 32 a
+// cycle and SM, and about four instructions), but neither is busy all the time:
+// counters show the tensor unit and 2^x at 48 % each, for a warp's turn is a chain
+// of waits (TMEM read, maximum, 2^x, TMEM write, arrival) with one other warp to
+// fill it.  32 heads of 8192 x 8192 x 64, fp16: 0.47 ms, 1.17 PFLOP/s.  With a
+// cap, two 2^x and a quarter of a reciprocal a score and the same chain: 0.91
+// PFLOP/s at 128, 0.53 at 64.
 // The issuing warp runs its loop converged: with one lane inside a divergent
 // branch the products' operands left the uniform registers and issuing them
 // took longer than computing them (1.01 instead of 1.64 PFLOP/s).
