@@ -74,7 +74,8 @@ typedef enum h3qk_dtype {
     H3QK_FP16 = 1,          /* IEEE binary16 */
     H3QK_BF16 = 2,          /* bfloat16 */
     H3QK_E4M3 = 3,          /* OCP 8-bit E4M3FN codes (output only) */
-    H3QK_FP32 = 4           /* IEEE binary32 (layer norm only) */
+    H3QK_FP32 = 4,          /* IEEE binary32 (layer norm only) */
+    H3QK_E2M1 = 5           /* 4-bit codes with e4m3 scales (h3qk_cache only) */
 } h3qk_dtype;
 
 typedef enum h3qk_scale_mode {
@@ -555,10 +556,118 @@ h3qk_status h3qk_attention(const h3qk_attn* call, h3qk_stream_t stream);
 size_t h3qk_attention_backward_workspace_bytes(const h3qk_attn* call);
 h3qk_status h3qk_attention_backward(const h3qk_attn* call, h3qk_stream_t stream);
 
-/* Blocks of attention kernels on the current device that gave up waiting
+/* Blocks of attention kernels (h3qk_cache_attention's among them) on the current device that gave up waiting
  * since the library was loaded (synchronous: waits for the device); -1 when
  * the count cannot be read. */
 int64_t h3qk_attention_stuck(void);
+
+/*
+ * A cache of keys and values in pages, for serving: rows are appended as they
+ * are prepared, attention reads them, and they can be read back.
+ *
+ * A page holds page_size consecutive rows of one sequence, for all K/V heads;
+ * row n of sequence b is row n mod page_size of page block_table[b][n / page_size].
+ * Pages may be handed out in any order, and be shared by sequences that only
+ * read them.  A page number outside [0, pages) is never followed: rows on it
+ * are not written, and read as zeros.
+ *
+ * format H3QK_FP16 / H3QK_BF16: rows of head_dim values (a multiple of 8 up to
+ *   128), strides as for attention (multiples of 8 elements, row >= head_dim).
+ * format H3QK_E2M1: 4.5 bits a value.  Each group of 16 channels has a scale g
+ *   (e4m3, one byte) and 16 e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *   negatives; channel 2i in the low half of byte i), and a value is
+ *   code * g * k_scale (v_scale).  head_dim is a multiple of 32 up to 128.
+ *   Codes are rows of head_dim / 2 bytes, scales rows of head_dim / 16 bytes,
+ *   without gaps between a page's rows; their page and head strides are in
+ *   bytes, multiples of 16.  From a group's 16-bit values y:
+ *     g = e4m3(max|y| / (6 k_scale)), at least 2^-9, at most 448,
+ *     code = e2m1(y * (1 / (g k_scale))), both to nearest even, saturating;
+ *   a group with an infinite or NaN value gets a NaN scale.  code * g is exact
+ *   in either 16-bit type, so with a k_scale of 1 no reader rounds.
+ */
+typedef struct h3qk_cache {
+    int32_t format;          /* H3QK_FP16, H3QK_BF16 or H3QK_E2M1 */
+    int32_t kv_heads;        /* 1 to 65535 */
+    int32_t head_dim;
+    int32_t page_size;       /* rows: a power of two from 16 to 65536 */
+    int64_t pages;           /* of the pool, below 2^31 */
+    void *k, *v;             /* [pages, kv_heads, page_size, head_dim], or codes [..., head_dim / 2]; 16-byte aligned */
+    void *k_scales, *v_scales;  /* E2M1 only: e4m3 [pages, kv_heads, page_size, head_dim / 16]; 16-byte aligned */
+    h3qk_strides k_strides, v_strides, k_scale_strides, v_scale_strides;  /* item: from page to page */
+    float k_scale, v_scale;  /* E2M1 only: finite, > 0; 0 means 1 */
+    int32_t batch;           /* sequences, 1 to 65535 */
+    int32_t max_pages;       /* entries of a sequence in the table; max_pages * page_size < 2^30 */
+    const int32_t* block_table;  /* [batch, max_pages], sequences table_stride entries apart */
+    int64_t table_stride;    /* 0: max_pages */
+    const int32_t* kv_lens;  /* [batch] rows of each sequence; with those that a call appends */
+} h3qk_cache;
+
+/*
+ * h3qk_cache_append: h3qk_prepare's 16-bit path for the new rows of several
+ * sequences, with K and V going into the cache.
+ *   qkv        16-bit [tokens, row_stride], row r = [Q | K | V] of heads,
+ *              kv_heads and kv_heads head rows; opts->in_dtype names its type
+ *              (DEFAULT: the cache's, or BF16), which a 16-bit cache shares.
+ *   q_offsets  int32 [batch + 1], ascending: rows [q_offsets[b], q_offsets[b+1])
+ *              are sequence b's last rows, so that its row i becomes cache row
+ *              kv_lens[b] - n_b + i.  NULL: tokens / batch rows each.  Rows of
+ *              no sequence are not read, and leave out_q and the cache as they
+ *              were; so do rows whose place lies outside the table in the cache.
+ *   positions  as for h3qk_prepare; NULL with n_axes 1: each row's place in
+ *              its sequence.
+ *   out_q      [tokens, heads, head_dim] contiguous.
+ * Q and K are normalised, rotated and rounded as h3qk_prepare does it, bit for
+ * bit.  A place belongs to one row: which of two rows that name the same place
+ * is kept is not defined, and with E2M1 neither may be.  opts' batch,
+ * out_layout, valid_lens, static_scales, workspace and sat_counts are ignored.
+ * No output may overlap an input or another output (K and V may share pages of
+ * a pool).  Errors and asynchrony as for h3qk_prepare.
+ */
+h3qk_status h3qk_cache_append(const h3qk_cache* cache, const void* qkv, const float* norm_wq, const float* norm_wk,
+                              const int32_t* positions, int64_t tokens, int32_t heads, int32_t rotary_dim,
+                              const int32_t* q_offsets, void* out_q, const h3qk_opts* opts, h3qk_stream_t stream);
+
+/*
+ * h3qk_cache_attention: h3qk_attention's formula with the keys and values of
+ * a cache.  Row i of sequence b stands at position kv_lens[b] - n_b + i and
+ * sees its kv_lens[b] keys; with causal, of those the ones up to its own
+ * position and the first prefix_lens[b].  Rows that see no key get out = 0 and
+ * lse = -infinity; rows of no sequence, and rows past max_rows of one, are left
+ * as they were.  Scores, sums and outputs are binary32.  p is rounded for its
+ * product with v: to the type of q, over 4-bit caches of few rows always to
+ * binary16.  The same call gives the same bits every time.
+ * Fill the struct from zeros.
+ */
+typedef struct h3qk_cache_attn {
+    int32_t dtype;           /* H3QK_FP16 or H3QK_BF16, of q and out; a 16-bit cache's own */
+    int32_t heads;           /* a multiple of the cache's kv_heads */
+    int32_t causal;          /* 0 or 1 */
+    int32_t max_rows;        /* no sequence has more rows; 0: tokens (without q_offsets: tokens / batch) */
+    float scale, softcap;    /* as for h3qk_attention */
+    int64_t tokens;          /* rows of q, below 2^30 */
+    const void* q;           /* [tokens, heads, head_dim] */
+    void* out;               /* as q */
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;  /* elements, multiples of 8 */
+    float* lse;              /* [heads, tokens] contiguous */
+    const float* slopes;     /* [heads] or NULL */
+    const int32_t* prefix_lens;  /* [batch] or NULL; only with causal */
+    const int32_t* q_offsets;    /* [batch + 1] as for h3qk_cache_append, or NULL */
+    void* workspace;         /* device memory, 16-byte aligned, of the size the function below gives */
+    size_t workspace_bytes;
+} h3qk_cache_attn;
+
+size_t h3qk_cache_attention_workspace_bytes(const h3qk_cache* cache, const h3qk_cache_attn* call);
+h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_cache_attn* call, h3qk_stream_t stream);
+
+/*
+ * h3qk_cache_read: rows [starts[b], kv_lens[b]) of each sequence, at most
+ * `rows` of them, as dense 16-bit out_k, out_v [batch, kv_heads, rows,
+ * head_dim] (contiguous, 16-byte aligned, of dtype: a 16-bit cache's own; what
+ * 4 bits stand for, rounded once), with zeros after them.  starts NULL: from
+ * row 0.  The result serves h3qk_attention and its gradient, or another cache.
+ */
+h3qk_status h3qk_cache_read(const h3qk_cache* cache, const int32_t* starts, int64_t rows, h3qk_dtype dtype,
+                            void* out_k, void* out_v, h3qk_stream_t stream);
 
 /* A static, human-readable name of a status. */
 const char* h3qk_status_string(h3qk_status status);

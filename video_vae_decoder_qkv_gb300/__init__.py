@@ -11,7 +11,9 @@ transfers overlapped.  The library also
 carries the two adjacent streaming operations of the decoder block
 (``silu_and_mul``, ``scaled_residual``), and the attention block around the
 path: ``layer_norm`` before the projection, and the gradients
-``layer_norm_backward`` and ``prepare_backward``.
+``layer_norm_backward`` and ``prepare_backward``; and a paged cache for
+serving, 16-bit or 4-bit (``Cache``, ``cache_append``, ``cache_attention``,
+``cache_read``).
 """
 
 from .h3qk import (H3QKError, amax, cast, norm_rope_tensor, prepare,  # noqa: F401
@@ -19,9 +21,10 @@ from .h3qk import (H3QKError, amax, cast, norm_rope_tensor, prepare,  # noqa: F4
 
 __all__ = ["prepare", "prepare_host", "prepare_sage", "norm_rope_tensor", "amax", "cast", "prepare_dynamic_sharded",
            "silu_and_mul", "scaled_residual", "layer_norm", "layer_norm_backward", "prepare_backward", "attention",
-           "attention_backward", "H3QKError"]
+           "attention_backward", "Cache", "cache_append", "cache_attention", "cache_read", "H3QKError"]
 
 _BLOCK = ("layer_norm", "layer_norm_backward", "prepare_backward", "attention", "attention_backward")
+_CACHE = ("Cache", "cache_append", "cache_attention", "cache_read")
 
 
 def __getattr__(name):
@@ -31,5 +34,10 @@ def __getattr__(name):
         from . import block
 
         globals().update({n: getattr(block, n) for n in _BLOCK})
+        return globals()[name]
+    if name in _CACHE:
+        from . import cache
+
+        globals().update({n: getattr(cache, n) for n in _CACHE})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -29,9 +29,11 @@ LIB_DEBUG = os.path.join(PKG, "libh3qk_debug.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("h3qk_api.cu", "h3qk_host.cu", "h3qk_launch_bf16.cu",
                                            "h3qk_launch_fp16.cu", "h3qk_vae_ops.cu", "h3qk_layer_norm.cu",
                                            "h3qk_backward.cu", "h3qk_attn.cu", "h3qk_attn_fwd.cu", "h3qk_attn_split.cu",
-                                           "h3qk_attn_bwd.cu")]
+                                           "h3qk_attn_bwd.cu", "h3qk_cache.cu", "h3qk_cache_attn.cu",
+                                           "h3qk_cache_few.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("h3qk_kernels.cuh", "h3qk_launch.cuh", "h3qk_internal.h",
-                                                      "h3qk_ops.cuh", "h3qk_attn.cuh", "h3qk_tc.cuh")] + \
+                                                      "h3qk_ops.cuh", "h3qk_attn.cuh", "h3qk_tc.cuh", "h3qk_cache.cuh",
+                                                      "h3qk_cache_attn.cuh", "h3qk_cache_host.h")] + \
     [os.path.join(INCLUDE, "h3qk.h")]
 
 COMPILE_FLAGS = [

@@ -1,0 +1,819 @@
+// Attention over a paged cache, few rows (tokens and drafts produced one by
+// one, over 4-bit or 16-bit pages).
+//
+// Bound by reading the cache once: 144 bytes a key and K/V head of 128 in
+// 4 bits, 512 in 16.  The packed rows of a sequence (its query rows times the
+// heads that share a K/V head) form tiles of 8 or 16.
+//
+// All keys of the call, sequence after sequence, K/V head after head, row tile
+// after tile, are one line of units of 64 keys, cut into equal shares, one a
+// block: caches of any mix of lengths keep every SM busy to the end.  A
+// block's share may hold the end of one run, whole ones, and the beginning of
+// another; whole runs are finished in place, and cut ones leave a partial
+// result (O, maximum, sum) that a second, chained kernel joins in order.
+//
+// Inside a share the block's warps take turns of keys in round robin, each
+// with its own copies in flight (cp.async into a ring of its own: no barrier
+// between warps), its own running maximum, sum and O, and meet in shared
+// memory at the end of the run.
+//
+// The products are the warp-wide 16 x 8 x 16 ones with the keys as rows:
+// S^T = K Q^T takes 16 keys x 8 packed rows, O^T += V^T P^T 16 channels x 8
+// rows.  (One tcgen05 tile has 128 rows, of which a token's heads would fill
+// five.)  The contraction over channels may run in any order, so that a lane
+// takes neighbouring channels of its key, and those of O^T likewise.  P^T
+// comes out of the softmax with a key a lane group and is turned by two
+// 8 x 8 transposes in registers.
+//
+// 4 bits: e2m1 codes become binary16 in one conversion for two, times their
+// group's scale, exactly.  The products are binary16's whatever the type of
+// q: bfloat16 rows are first scaled by a power of two so that their largest
+// value is near 2^14, which loses nothing that binary32 sums would keep, and P
+// is held 2^11 larger.  V's codes of two neighbouring keys are interleaved by
+// nibbles before their conversion, which makes the pairs that the product
+// takes.
+#include "h3qk_cache_attn.cuh"
+
+namespace {
+
+using namespace h3qk_tc;
+using namespace h3qk_pages;
+using h3qk_core::Bend;
+
+// The maximum serves on while it grows by less than 2^kSlack, and binary16's P
+// is held 2^kRaise larger: at most 2^15, and what falls below 2^-14 keeps an
+// absolute 2^-36 of the row's largest.
+constexpr float kSlack = 4.0f, kRaise = 11.0f;
+
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values, a row's neighbouring pair a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Where a warp's keys come from: one sequence and K/V head.
+struct Source {
+    const uint8_t *k, *v, *ks, *vs;  // the head's rows in page 0
+    const int32_t* table;
+    int end;  // keys of the run that are looked at
+};
+
+// 4-bit pages.  A turn is 32 keys: codes of K and V, DP / 2 bytes a key, and
+// their scales.  16-byte pieces are spread over a 128-byte line's slots so
+// that the lanes that read K (4 of a key, 8 keys) and V (8 of a key, 4 keys)
+// meet no bank twice.
+template <int DP, int NB>
+struct Codes {
+    static constexpr bool kE2m1 = true;
+    static constexpr int kDim = DP;
+    static constexpr int kTurn = 32, kWarps = NB == 1 ? 8 : 4, kStages = 3;
+    static constexpr int kPitch = DP / 2;
+    static constexpr int kScales = 2 * kTurn * kPitch;  // where the scales begin
+    static constexpr int kStage = kScales + 2 * kTurn * (DP / 16);
+    static constexpr int kBlocks = NB == 1 ? 2 : 3;  // an SM
+
+    __device__ static uint32_t slot(int row, int piece)
+    {
+        if constexpr (DP == 128) return row / 2 * 128 + ((((row & 1) * 4 + piece) ^ ((row >> 1 & 3) * 2)) * 16);
+        else return row / 4 * 128 + ((((row & 3) * 2 + piece) ^ ((row >> 2 & 1) * 2)) * 16);
+    }
+    // The channel where a lane's share of a K row (and of Q) begins, and of piece i of 8.
+    __device__ static int k_channel(int c, int i) { return DP / 4 * c + 8 * i; }
+    // The channel of rows g and g + 8 of product m of O^T: this and the next.
+    __device__ static int v_channel(int g, int m) { return DP / 8 * g + 2 * m; }
+
+    __device__ static void fetch(const Pool& c, const Source& s, uint32_t to, int j, const int (&page)[2], int lane)
+    {
+        constexpr int kPieces = DP / 32, kPer = kTurn * kPieces / 32;  // pieces a row; copies a lane
+        const int mask = (1 << c.page_shift) - 1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int at = lane + 32 * i, row = at / kPieces, piece = at % kPieces;
+            const int pg = page[i / (kPer / 2)];
+            const bool there = pg >= 0;
+            const int64_t in_page = (j + row) & mask;
+            if (32 * piece < c.dim) {
+                copy16(to + slot(row, piece), there ? s.k + pg * c.k_page + in_page * c.k_row + 16 * piece : s.k, there);
+                copy16(to + kTurn * kPitch + slot(row, piece),
+                       there ? s.v + pg * c.v_page + in_page * c.v_row + 16 * piece : s.v, there);
+            }
+        }
+        // 16 rows' scales lie together: dim bytes.
+        const int half = lane >> 3 & 1, piece = lane & 7;
+        if (16 * piece < c.dim) {
+            const int pg = half ? page[1] : page[0];
+            const bool there = pg >= 0, v = lane >= 16;
+            const int64_t in_page = (j + 16 * half) & mask;
+            const uint8_t* from = v ? s.vs + pg * c.vs_page : s.ks + pg * c.ks_page;
+            copy16(to + kScales + (v ? kTurn * (DP / 16) : 0) + half * DP + 16 * piece,
+                   there ? from + in_page * (c.dim / 16) + 16 * piece : s.ks, there);
+        }
+    }
+
+    // Rows 16 kb + g and + 8 of K as the products' A, steps of 4 channels a lane, for f(step, a).
+    template <class F>
+    __device__ static void keys(const Pool& c, uint32_t at, int kb, int g, int cc, int left, F&& f)
+    {
+        constexpr int kWords = DP / 32;
+        uint32_t w[2][kWords], sc[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int row = 16 * kb + 8 * t + g;
+            const uint32_t scales = at + kScales + kb * DP + (row & 15) * (c.dim / 16);
+            uint32_t two;
+            if constexpr (DP == 128) {
+                const uint4 v = lds128(at + slot(row, cc));
+                w[t][0] = v.x, w[t][1] = v.y, w[t][2] = v.z, w[t][3] = v.w;
+                two = lds16(scales + 2 * cc);
+            } else {
+                const uint2 v = lds64(at + slot(row, cc >> 1) + 8 * (cc & 1));
+                w[t][0] = v.x, w[t][1] = v.y;
+                two = lds8(scales + cc);
+            }
+            const bool there = row < left && DP / 4 * cc < c.dim;
+            if (!there) two = 0;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                if (!there) w[t][i] = 0;
+            const uint32_t wide = widen_scales(two);
+            sc[t][0] = __byte_perm(wide, wide, 0x1010);
+            sc[t][1] = __byte_perm(wide, wide, 0x3232);
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            uint32_t v[2][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                widen_codes(w[t][i], v[t]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[t][e] = mul_half2(v[t][e], sc[t][i / 2]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t a[4] = {v[0][2 * e], v[1][2 * e], v[0][2 * e + 1], v[1][2 * e + 1]};
+                f(2 * i + e, a);
+            }
+        }
+    }
+
+    // Keys 16 kb + {2c, 2c + 1, 2c + 8, 2c + 9} of V as the products' A (channels as rows), for f(m, a).
+    template <class F>
+    __device__ static void values(const Pool& c, uint32_t at, int kb, int g, int cc, int left, F&& f)
+    {
+        constexpr int kWords = DP / 64;
+        uint32_t w[4][kWords], byte[4];
+        const uint32_t codes = at + kTurn * kPitch;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int in = 2 * cc + (t & 1) + 8 * (t >> 1), row = 16 * kb + in;
+            const uint32_t scales = at + kScales + kTurn * (DP / 16) + kb * DP + in * (c.dim / 16);
+            if constexpr (DP == 128) {
+                const uint2 v = lds64(codes + slot(row, g >> 1) + 8 * (g & 1));
+                w[t][0] = v.x, w[t][1] = v.y;
+                byte[t] = lds8(scales + g);
+            } else {
+                w[t][0] = lds32(codes + slot(row, g >> 2) + 4 * (g & 3));
+                byte[t] = lds8(scales + (g >> 1));
+            }
+            if (row >= left) byte[t] = 0;
+        }
+        const uint32_t s01 = widen_scales(byte[0] | byte[1] << 8), s23 = widen_scales(byte[2] | byte[3] << 8);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            constexpr uint32_t kLow = 0x0f0f0f0fu;
+            uint32_t v[4][4];  // channels 0, 2, 4, 6 and 1, 3, 5, 7 of keys 0, 1; of keys 2, 3
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t x = w[2 * t][i], y = w[2 * t + 1][i];
+                widen_codes((x & kLow) | ((y << 4) & ~kLow), v[2 * t]);
+                widen_codes(((x >> 4) & kLow) | (y & ~kLow), v[2 * t + 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a[4] = {mul_half2(v[0][e], s01), mul_half2(v[1][e], s01), mul_half2(v[2][e], s23),
+                                       mul_half2(v[3][e], s23)};
+                f(4 * i + e, a);
+            }
+        }
+    }
+};
+
+// 16-bit pages.  A turn is 16 keys; each lane copies just the 16-byte pieces
+// that it uses itself, into slots of its own.
+template <int DP, int NB>
+struct Halves {
+    static constexpr bool kE2m1 = false;
+    static constexpr int kDim = DP;
+    static constexpr int kTurn = 16, kWarps = 4, kStages = 3;
+    static constexpr int kStage = 2 * kTurn * DP * 2;
+    static constexpr int kBlocks = 2;
+    static constexpr int kK = DP / 32, kV = DP / 64;  // pieces of a lane's K row and V row
+
+    __device__ static int k_channel(int c, int i) { return 8 * (c + 4 * i); }
+    __device__ static int v_channel(int g, int m) { return m / 4 * 64 + 8 * g + 2 * (m % 4); }
+
+    __device__ static void fetch(const Pool& c, const Source& s, uint32_t to, int j, const int (&page)[2], int lane)
+    {
+        const int g = lane >> 2, cc = lane & 3;
+        const int64_t in_page = j & ((1 << c.page_shift) - 1);
+        const bool there = page[0] >= 0;
+        const uint8_t* k = s.k + page[0] * c.k_page + in_page * c.k_row;
+        const uint8_t* v = s.v + page[0] * c.v_page + in_page * c.v_row;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < kK; ++i) {
+                const int channel = k_channel(cc, i);
+                const bool ok = there && channel < c.dim && j + 8 * t + g < s.end;
+                copy16(to + ((t * kK + i) * 32 + lane) * 16, ok ? k + (8 * t + g) * c.k_row + 2 * channel : s.k, ok);
+            }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const int channel = 64 * i + 8 * g, row = 2 * cc + (t & 1) + 8 * (t >> 1);
+                const bool ok = there && channel < c.dim && j + row < s.end;
+                copy16(to + ((2 * kK + t * kV + i) * 32 + lane) * 16, ok ? v + row * c.v_row + 2 * channel : s.v, ok);
+            }
+    }
+
+    template <class F>
+    __device__ static void keys(const Pool&, uint32_t at, int, int g, int cc, int, F&& f)
+    {
+        const uint32_t mine = at + (4 * g + cc) * 16;
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            const uint4 x = lds128(mine + i * 512), y = lds128(mine + (kK + i) * 512);
+            const uint32_t a[4] = {x.x, y.x, x.y, y.y}, b[4] = {x.z, y.z, x.w, y.w};
+            f(2 * i, a);
+            f(2 * i + 1, b);
+        }
+    }
+
+    template <class F>
+    __device__ static void values(const Pool&, uint32_t at, int, int g, int cc, int, F&& f)
+    {
+        const uint32_t mine = at + (4 * g + cc) * 16;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            uint4 x[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) x[t] = lds128(mine + (2 * kK + t * kV + i) * 512);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a[4] = {__byte_perm(word(x[0], e), word(x[1], e), 0x5410),
+                                       __byte_perm(word(x[0], e), word(x[1], e), 0x7632),
+                                       __byte_perm(word(x[2], e), word(x[3], e), 0x5410),
+                                       __byte_perm(word(x[2], e), word(x[3], e), 0x7632)};
+                f(4 * i + e, a);
+            }
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The line of work
+// ---------------------------------------------------------------------------
+// A sequence's part of the line: `runs` (K/V heads x row tiles) of `per` units.
+struct Part {
+    Sequence s;
+    int64_t packed;  // packed rows, 0: not in this kernel's line
+    int tiles, per;
+    __device__ int64_t units(const Attn& p) const { return packed ? static_cast<int64_t>(p.c.kv_heads) * tiles * per : 0; }
+};
+template <int ROWS>
+__device__ __forceinline__ Part part_of(const Attn& p, int item)
+{
+    Part t;
+    t.s = sequence_of(p, item);
+    t.packed = static_cast<int64_t>(t.s.n) * p.group;
+    if (t.packed > p.few) t.packed = 0;
+    t.tiles = static_cast<int>((t.packed + ROWS - 1) / ROWS);
+    t.per = max((t.s.keys + kUnit - 1) / kUnit, 1);  // a row without keys is a unit of its own
+    return t;
+}
+
+// Warp-wide: all units of the call, and with `place` >= 0 the sequence that
+// holds unit `place` and the units before it.
+template <int ROWS>
+__device__ __forceinline__ int64_t all_units(const Attn& p)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t sum = 0;
+    for (int b = lane; b < p.c.batch; b += 32) sum += part_of<ROWS>(p, b).units(p);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+template <int ROWS>
+__device__ __forceinline__ int find_unit(const Attn& p, int64_t place, int64_t& before)
+{
+    const int lane = threadIdx.x & 31;
+    before = 0;
+    for (int b0 = 0; b0 < p.c.batch; b0 += 32) {
+        const int64_t mine = b0 + lane < p.c.batch ? part_of<ROWS>(p, b0 + lane).units(p) : 0;
+        int64_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        const unsigned vote = __ballot_sync(0xffffffffu, place < before + sum);
+        if (vote) {
+            const int src = __ffs(vote) - 1;
+            before += __shfl_sync(0xffffffffu, sum - mine, src);
+            return b0 + src;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return -1;
+}
+__device__ __forceinline__ int64_t share_of(const Attn& p, int64_t total, int blocks)
+{
+    const int64_t even = (total + blocks - 1) / blocks;
+    return even > p.least ? even : p.least;
+}
+
+// A block leaves at most two partial results: of the run that its share
+// begins in the middle of (or fills), and of the one that it breaks off.
+__host__ __device__ inline int64_t part_floats(int rows, int dim) { return static_cast<int64_t>(rows) * (dim + 2); }
+
+template <bool BF16>
+__device__ __forceinline__ void finish_row(const Attn& p, const Sequence& s, int kv, int64_t r, int d, float4 v, float top,
+                                           float sum, float shift, float v_scale)
+{
+    const int head = kv * p.group + static_cast<int>(r % p.group);
+    const int64_t token = s.first + r / p.group;
+    const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
+    if (d < p.c.dim) {
+        uint2 w;
+        w.x = round_pair<BF16>(v.x * inv, v.y * inv);
+        w.y = round_pair<BF16>(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(p.out + token * p.out_token + head * p.out_head + d) = w;
+    }
+    if (d == 0)
+        p.lse[static_cast<int64_t>(head) * p.tokens + token] =
+            sum == 0.0f ? -INFINITY : (top - shift + log2f(sum)) * h3qk_core::kLn2;
+}
+
+template <class T, bool BF16, int NB>
+__global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const __grid_constant__ Attn p)
+{
+    constexpr int ROWS = 8 * NB, DP = T::kDim;
+    constexpr int kWarps = T::kWarps, KB = T::kTurn / 16, kSteps = DP / 16, kOut = DP / 16;
+    constexpr bool kHalf = T::kE2m1 || !BF16;  // the products are binary16's
+    constexpr float kShift = kHalf ? kRaise : 0.0f;
+    static_assert(T::kWarps * T::kStages * T::kStage >= kWarps * ROWS * (DP + 4) * 4, "the warps' O fits the rings");
+    extern __shared__ __align__(128) uint8_t dynamic[];
+    __shared__ float sh_m[kWarps][ROWS], sh_l[kWarps][ROWS];
+    h3qk_ops::allow_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = lane & 3, g = lane >> 2;
+    const uint32_t ring = smem_addr(dynamic) + warp * T::kStages * T::kStage;
+    float(*sh_o)[ROWS][DP + 4] = reinterpret_cast<float(*)[ROWS][DP + 4]>(dynamic);
+    const bool capped = p.cap > 0.0f;
+
+    const int64_t total = all_units<ROWS>(p), share = share_of(p, total, gridDim.x);
+    const int64_t begin = blockIdx.x * share, end = min(begin + share, total);
+    if (begin >= end) return;
+    int64_t before;
+    int item = find_unit<ROWS>(p, begin, before);
+    Part part = part_of<ROWS>(p, item);
+
+    for (int64_t pos = begin; pos < end;) {
+        while (pos >= before + part.units(p)) {  // (every unit up to `end` has a sequence)
+            before += part.units(p);
+            part = part_of<ROWS>(p, ++item);
+        }
+        const Sequence& s = part.s;
+        const int64_t run = (pos - before) / part.per;
+        const int unit = static_cast<int>((pos - before) - run * part.per);
+        const int units = static_cast<int>(min(static_cast<int64_t>(part.per - unit), end - pos));
+        const int kv = static_cast<int>(run / part.tiles), row_tile = static_cast<int>(run % part.tiles);
+        pos += units;
+
+        // This lane's packed row of each block of 8 for Q, and the two whose scores it holds.
+        float o[kOut][NB][4], m[NB][2], l[NB][2];
+        float in[NB][2], plain[NB][2], slope[NB][2];
+        int lim[NB][2], at[NB][2];
+        uint32_t q[NB][2 * kSteps];
+        int most = 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int64_t r = static_cast<int64_t>(row_tile) * ROWS + 8 * b + g;
+            const bool has = r < part.packed;
+            const int i = has ? static_cast<int>(r / p.group) : 0, head = kv * p.group + (has ? static_cast<int>(r % p.group) : 0);
+            const uint16_t* from = p.q + (s.first + i) * p.q_token + head * p.q_head;
+#pragma unroll
+            for (int e = 0; e < kSteps / 2; ++e) {
+                const int channel = T::k_channel(c, e);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (has && channel < p.c.dim) v = __ldg(reinterpret_cast<const uint4*>(from + channel));
+                q[b][4 * e] = v.x, q[b][4 * e + 1] = v.y, q[b][4 * e + 2] = v.z, q[b][4 * e + 3] = v.w;
+            }
+            float raw = 1.0f;
+            if constexpr (T::kE2m1) {
+                raw = p.c.k_scale;
+                if constexpr (BF16) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < 2 * kSteps; ++e) top = __vmaxu2(top, q[b][e] & 0x7fff7fffu);
+                    top = max(top & 0xffffu, top >> 16);
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // times 2^(141 - e) with e the largest exponent field; rows with an infinity or NaN as they are
+                    int e = top >> 7;
+                    e = e == 255 ? 141 : max(e, 15);
+                    const float up = __int_as_float((127 + 141 - e) << 23);
+                    raw *= __int_as_float((127 + e - 141) << 23);
+#pragma unroll
+                    for (int k = 0; k < 2 * kSteps; ++k) {
+                        const float2 f = widen_pair<true>(q[b][k]);
+                        q[b][k] = round_pair<false>(f.x * up, f.y * up);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int src = (2 * c + h) * 4;
+                const float raw_of = __shfl_sync(0xffffffffu, raw, src);
+                const int i_of = __shfl_sync(0xffffffffu, i, src), head_of = __shfl_sync(0xffffffffu, head, src);
+                const bool has_of = __shfl_sync(0xffffffffu, static_cast<int>(has), src) != 0;
+                const Bend bend = h3qk_pages::bend_of(p, head_of, raw_of);
+                in[b][h] = bend.in;
+                plain[b][h] = bend.plain;
+                slope[b][h] = bend.slope;
+                at[b][h] = s.start + i_of;
+                lim[b][h] = has_of ? limit_of(s, p.causal, i_of) : 0;
+                most = max(most, lim[b][h]);
+                m[b][h] = -INFINITY;
+                l[b][h] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kOut; ++k) o[k][b][0] = o[k][b][1] = o[k][b][2] = o[k][b][3] = 0.0f;
+        }
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        const float cap2 = p.cap * h3qk_core::kLog2e;
+
+        Source src;
+        src.k = p.c.k + kv * p.c.k_head;
+        src.v = p.c.v + kv * p.c.v_head;
+        src.ks = p.c.k_scales + kv * p.c.ks_head;
+        src.vs = p.c.v_scales + kv * p.c.vs_head;
+        src.table = p.c.table + item * p.c.table_stride;
+        const int k_first = unit * kUnit;
+        src.end = min(k_first + units * kUnit, most);
+        constexpr int kStep = T::kTurn * kWarps;
+
+        // The pages of a turn's two halves (-1: nothing to read).
+        auto pages = [&](int j, int (&pg)[2]) {
+            pg[0] = j < src.end ? page_of(p.c, src.table, j) : -1;
+            pg[1] = T::kTurn == 32 && j + 16 < src.end ? page_of(p.c, src.table, j + 16) : -1;
+        };
+        int j = k_first + T::kTurn * warp;
+        if (j < src.end) {
+            int pg[2];
+#pragma unroll
+            for (int i = 0; i < T::kStages - 1; ++i) {
+                pages(j + i * kStep, pg);
+                if (j + i * kStep < src.end) T::fetch(p.c, src, ring + i * T::kStage, j + i * kStep, pg, lane);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
+            pages(j + (T::kStages - 1) * kStep, pg);
+            int stage = 0;
+            for (; j < src.end; j += kStep) {
+                const int next = j + (T::kStages - 1) * kStep;
+                __syncwarp();  // the stage that is filled now has been read by all lanes
+                if (next < src.end) T::fetch(p.c, src, ring + (stage == 0 ? T::kStages - 1 : stage - 1) * T::kStage, next, pg, lane);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                pages(next + kStep, pg);
+                asm volatile("cp.async.wait_group %0;" ::"n"(T::kStages - 1) : "memory");
+                __syncwarp();
+                const uint32_t here = ring + stage * T::kStage;
+                stage = stage + 1 == T::kStages ? 0 : stage + 1;
+                const int left = src.end - j;
+
+                float sc[KB][NB][4];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) sc[kb][b][0] = sc[kb][b][1] = sc[kb][b][2] = sc[kb][b][3] = 0.0f;
+                    T::keys(p.c, here, kb, g, c, left, [&](int step, const uint32_t (&a)[4]) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) mma16<!kHalf>(sc[kb][b], a, q[b][2 * step], q[b][2 * step + 1]);
+                    });
+                }
+                float top[NB][2];
+                bool grows = false;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float t = -INFINITY;
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = j + 16 * kb + 8 * e + g;
+                                const float raw = sc[kb][b][2 * e + h];
+                                float v = raw * in[b][h];
+                                if (capped) {
+                                    float flat, other;
+                                    const uint64_t z = pair(v, v);
+                                    unpair(flat, other, mul_pair(pair(raw * plain[b][h], 0.0f), h3qk_core::tanh_series(mul_pair(z, z))));
+                                    const float bent = fmaf(-2.0f * cap2, rcp_fast(exp2_fast(v) + 1.0f), cap2);
+                                    v = fabsf(v) < h3qk_core::kSmall ? flat : bent;
+                                }
+                                if (p.slopes) v = fmaf(-slope[b][h], fabsf(static_cast<float>(at[b][h] - key)), v);
+                                v = key < lim[b][h] ? v : -INFINITY;
+                                sc[kb][b][2 * e + h] = v;
+                                t = fmaxf(t, v);
+                            }
+                        top[b][h] = t;
+                        grows = grows || t > m[b][h] + kSlack;
+                    }
+                if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float t = top[b][h];
+                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                            t = fmaxf(t, m[b][h]);
+                            const float f = t == -INFINITY ? 1.0f : exp2_fast(m[b][h] - t);
+                            m[b][h] = t;
+                            l[b][h] *= f;
+#pragma unroll
+                            for (int k = 0; k < kOut; ++k) {
+                                o[k][b][h] *= f;
+                                o[k][b][2 + h] *= f;
+                            }
+                        }
+                }
+                uint32_t pt[KB][NB][2];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float off[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) off[h] = (m[b][h] == -INFINITY ? 0.0f : m[b][h]) - kShift;
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float p0 = exp2_fast(sc[kb][b][2 * e] - off[0]), p1 = exp2_fast(sc[kb][b][2 * e + 1] - off[1]);
+                            l[b][0] += p0;
+                            l[b][1] += p1;
+                            pt[kb][b][e] = transpose8(round_pair<!kHalf>(p0, p1));
+                        }
+                }
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+                    T::values(p.c, here, kb, g, c, left, [&](int k, const uint32_t (&a)[4]) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) mma16<!kHalf>(o[k][b], a, pt[kb][b][0], pt[kb][b][1]);
+                    });
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        // Join the block's warps.
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float sum = l[b][h];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int row = 8 * b + 2 * c + h;
+                if (g == 0) {
+                    sh_m[warp][row] = m[b][h];
+                    sh_l[warp][row] = sum;
+                }
+#pragma unroll
+                for (int k = 0; k < kOut; ++k)
+                    *reinterpret_cast<float2*>(&sh_o[warp][row][T::v_channel(g, k)]) = make_float2(o[k][b][h], o[k][b][2 + h]);
+            }
+        __syncthreads();
+        const bool whole = units == part.per;
+        float* to = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (unit == 0 ? 1 : 0)) * part_floats(ROWS, p.c.dim);
+        const int per = p.c.dim / 4;
+        for (int i = threadIdx.x; i < ROWS * per; i += 32 * kWarps) {
+            const int row = i / per, d = 4 * (i - row * per);
+            const int64_t r = static_cast<int64_t>(row_tile) * ROWS + row;
+            if (r >= part.packed) break;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][row]);
+            float sum = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                // a warp that saw no key; but a NaN is passed on
+                const float f = sh_m[w][row] == -INFINITY ? (sh_l[w][row] == 0.0f ? 0.0f : 1.0f) : exp2_fast(sh_m[w][row] - top);
+                const float4 x = *reinterpret_cast<const float4*>(&sh_o[w][row][d]);
+                sum = fmaf(sh_l[w][row], f, sum);
+                v.x = fmaf(x.x, f, v.x);
+                v.y = fmaf(x.y, f, v.y);
+                v.z = fmaf(x.z, f, v.z);
+                v.w = fmaf(x.w, f, v.w);
+            }
+            if (whole) {
+                finish_row<BF16>(p, s, kv, r, d, v, top, sum, kShift, T::kE2m1 ? p.c.v_scale : 1.0f);
+            } else {
+                *reinterpret_cast<float4*>(to + row * p.c.dim + d) = v;
+                if (d == 0) *reinterpret_cast<float2*>(to + ROWS * p.c.dim + 2 * row) = make_float2(top, sum);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// One block a packed row of a run that was cut: its warps take the blocks'
+// parts in turn, in order, and are joined in order.
+constexpr int kJoinWarps = 4;
+template <bool BF16, int ROWS>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_few_kernel(const __grid_constant__ Attn p, int blocks,
+                                                                   unsigned rows, float shift, float v_scale)
+{
+    __shared__ float4 sh_v[kJoinWarps][32];
+    __shared__ float sh_sum[kJoinWarps], sh_top[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = 4 * lane;
+    const int64_t r = blockIdx.x % rows;  // packed row of the sequence
+    const int kv = static_cast<int>(blockIdx.x / rows % p.c.kv_heads), item = static_cast<int>(blockIdx.x / rows / p.c.kv_heads);
+    const Part part = part_of<ROWS>(p, item);
+    h3qk_ops::wait_for_previous();
+    if (r >= part.packed) return;
+    // The units before this sequence, and of all.
+    int64_t before = 0, total = 0;
+    for (int b = lane; b < p.c.batch; b += 32) {
+        const int64_t u = part_of<ROWS>(p, b).units(p);
+        total += u;
+        if (b < item) before += u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    const int64_t share = share_of(p, total, blocks);
+    const int64_t u0 = before + (static_cast<int64_t>(kv) * part.tiles + r / ROWS) * part.per, u1 = u0 + part.per;
+    const int first = static_cast<int>(u0 / share), last = static_cast<int>((u1 - 1) / share);
+    if (first == last) return;  // finished in place
+    const int row = static_cast<int>(r % ROWS), n = last - first + 1;
+    const int64_t size = part_floats(ROWS, p.c.dim);
+    // the first block's part is the one that it broke off, the others' the one that they began in
+    auto slot = [&](int i) { return p.part + (2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0)) * size; };
+    auto stat = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(slot(i) + ROWS * p.c.dim + 2 * row)); };
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += 32 * kJoinWarps) top = fmaxf(top, stat(i).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh_top[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sh_top[w]);
+    float sum = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < n; i0 += 32 * kJoinWarps) {
+        const int mine_at = i0 + lane * kJoinWarps + warp;
+        float2 mine = make_float2(-INFINITY, 0.0f);
+        if (mine_at < n) mine = stat(mine_at);
+        const float f = mine.x == -INFINITY ? (mine.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(mine.x - top);
+        const int count = min(32, (n - i0 - warp + kJoinWarps - 1) / kJoinWarps);
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) {
+            const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, mine.y, i);
+            sum = fmaf(li, fi, sum);
+            if (d < p.c.dim) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(slot(i0 + i * kJoinWarps + warp) + row * p.c.dim + d));
+                v.x = fmaf(x.x, fi, v.x);
+                v.y = fmaf(x.y, fi, v.y);
+                v.z = fmaf(x.z, fi, v.z);
+                v.w = fmaf(x.w, fi, v.w);
+            }
+        }
+    }
+    sh_v[warp][lane] = v;
+    if (lane == 0) sh_sum[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+        const float4 x = sh_v[w][lane];
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+        sum += sh_sum[w];
+    }
+    finish_row<BF16>(p, part.s, kv, r, d, v, top, sum, shift, v_scale);
+}
+
+template <class T, bool BF16, int NB>
+cudaError_t launch(const Attn& p, int blocks, cudaStream_t st)
+{
+    constexpr int smem = T::kWarps * T::kStages * T::kStage;
+    auto* kernel = few_kernel<T, BF16, NB>;
+    static bool raised[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    if (!raised[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        raised[dev] = true;
+    }
+    kernel<<<blocks, 32 * T::kWarps, smem, st>>>(p);
+    h3qk_internal_count_launch();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || blocks == 1) return e;
+    const int64_t rows = p.few < static_cast<int64_t>(p.max_rows) * p.group ? p.few : static_cast<int64_t>(p.max_rows) * p.group;
+    const dim3 grid(static_cast<unsigned>(rows * p.c.kv_heads * p.c.batch));
+    const float shift = T::kE2m1 || !BF16 ? kRaise : 0.0f;
+    return h3qk_ops::launch_chained(join_few_kernel<BF16, 8 * NB>, grid, dim3(32 * kJoinWarps), 0, st, p, blocks,
+                                    static_cast<unsigned>(rows), shift, T::kE2m1 ? p.c.v_scale : 1.0f);
+}
+
+template <template <int, int> class T, bool BF16>
+cudaError_t by_shape(int row_tile, int blocks, const Attn& p, cudaStream_t st)
+{
+    if (p.c.dim <= 64)
+        return row_tile == 8 ? launch<T<64, 1>, BF16, 1>(p, blocks, st) : launch<T<64, 2>, BF16, 2>(p, blocks, st);
+    return row_tile == 8 ? launch<T<128, 1>, BF16, 1>(p, blocks, st) : launch<T<128, 2>, BF16, 2>(p, blocks, st);
+}
+
+}  // namespace
+
+int64_t h3qk_pages::few_floats(int blocks, int rows, int dim) { return blocks == 1 ? 0 : 2 * blocks * part_floats(rows, dim); }
+int h3qk_pages::few_blocks(bool e2m1, int row_tile)
+{
+    const int an_sm = e2m1 ? (row_tile == 8 ? Codes<128, 1>::kBlocks : Codes<128, 2>::kBlocks) : Halves<128, 1>::kBlocks;
+    return an_sm * h3qk_internal_sm_count();
+}
+
+cudaError_t h3qk_pages::cache_few(bool bf16, bool e2m1, int row_tile, int blocks, const Attn& p, cudaStream_t st)
+{
+    if (e2m1) return bf16 ? by_shape<Codes, true>(row_tile, blocks, p, st) : by_shape<Codes, false>(row_tile, blocks, p, st);
+    return bf16 ? by_shape<Halves, true>(row_tile, blocks, p, st) : by_shape<Halves, false>(row_tile, blocks, p, st);
+}
