@@ -30,10 +30,12 @@ SOURCES = [os.path.join(CSRC, f) for f in ("h3qk_api.cu", "h3qk_host.cu", "h3qk_
                                            "h3qk_launch_fp16.cu", "h3qk_vae_ops.cu", "h3qk_layer_norm.cu",
                                            "h3qk_backward.cu", "h3qk_attn.cu", "h3qk_attn_fwd.cu", "h3qk_attn_split.cu",
                                            "h3qk_attn_bwd.cu", "h3qk_cache.cu", "h3qk_cache_attn.cu",
-                                           "h3qk_cache_few.cu")]
+                                           "h3qk_cache_few.cu", "h3qk_cache_tiles_e2m1_fp16.cu",
+                                           "h3qk_cache_tiles_e2m1_bf16.cu", "h3qk_cache_tiles_fp16.cu",
+                                           "h3qk_cache_tiles_bf16.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("h3qk_kernels.cuh", "h3qk_launch.cuh", "h3qk_internal.h",
                                                       "h3qk_ops.cuh", "h3qk_attn.cuh", "h3qk_tc.cuh", "h3qk_cache.cuh",
-                                                      "h3qk_cache_attn.cuh", "h3qk_cache_host.h")] + \
+                                                      "h3qk_cache_attn.cuh", "h3qk_cache_host.h", "h3qk_cache_tiles.cuh")] + \
     [os.path.join(INCLUDE, "h3qk.h")]
 
 COMPILE_FLAGS = [
@@ -51,7 +53,7 @@ NVCC_FLAGS = COMPILE_FLAGS + ["--threads", "0", "-shared", "-cudart", "static"]
 # The attention tile kernels share their launch's registers out among their
 # warps, and are refused at run time when the compiler gave them any other
 # number (kLaunchRegs in csrc/h3qk_attn.cuh).
-TILE_KERNELS = re.compile(r"attention_(dq_|dkv_)?kernelI")
+TILE_KERNELS = re.compile(r"(attention_(dq_|dkv_)?|cache_tiles_)kernelI")
 TILE_KERNEL_REGS = 168
 
 

@@ -186,42 +186,13 @@ Encode encoder()
     return fn;
 }
 
-// Boxes of 128 rows by 64 channels, 128-byte swizzle, zeros past the ends.
 bool encode(CUtensorMap* m, const Tensor& t, bool bf16, int64_t batch, int64_t dim)
 {
-    const Encode fn = encoder();
-    if (!fn) return false;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(t.rows),
-                                static_cast<cuuint64_t>(t.heads), static_cast<cuuint64_t>(batch)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(t.s.row) * 2, static_cast<cuuint64_t>(t.s.head) * 2,
-                                   static_cast<cuuint64_t>(t.s.item) * 2};
-    const cuuint32_t box[4] = {64, 128, 1, 1}, ones[4] = {1, 1, 1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-              const_cast<void*>(t.data), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return h3qk_core::encode_map(m, t.data, bf16, dim, t.rows, t.heads, batch, t.s.row * 2, t.s.head * 2, t.s.item * 2, 128);
 }
 
-unsigned int* stuck_addr()
-{
-    static unsigned int* addr[64] = {nullptr};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    if (!addr[dev]) {
-        void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_stuck) != cudaSuccess) return nullptr;
-        addr[dev] = static_cast<unsigned int*>(p);
-    }
-    return addr[dev];
-}
-
-// The runtime could not give the stuck counter or a tensor map.
-h3qk_status no_maps()
-{
-    const cudaError_t e = cudaGetLastError();
-    return h3qk_internal_fail_cuda(e != cudaSuccess ? e : cudaErrorInvalidValue);
-}
-
+using h3qk_core::no_maps;
+using h3qk_core::stuck_addr;
 void fill(Params& p, const h3qk_attn& a)
 {
     p.batch = a.batch;
@@ -245,6 +216,41 @@ void fill(Params& p, const h3qk_attn& a)
 }
 
 }  // namespace
+
+bool h3qk_core::encode_map(CUtensorMap* m, const void* data, bool bf16, int64_t dim, int64_t rows, int64_t heads, int64_t items,
+                           int64_t row_bytes, int64_t head_bytes, int64_t item_bytes, int box_rows)
+{
+    const Encode fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(items)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(head_bytes),
+                                   static_cast<cuuint64_t>(item_bytes)};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1}, ones[4] = {1, 1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(data), dims,
+              strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+unsigned int* h3qk_core::stuck_addr()
+{
+    static unsigned int* addr[64] = {nullptr};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    if (!addr[dev]) {
+        void* p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_stuck) != cudaSuccess) return nullptr;
+        addr[dev] = static_cast<unsigned int*>(p);
+    }
+    return addr[dev];
+}
+
+// The runtime could not give the stuck counter or a tensor map.
+h3qk_status h3qk_core::no_maps()
+{
+    const cudaError_t e = cudaGetLastError();
+    return h3qk_internal_fail_cuda(e != cudaSuccess ? e : cudaErrorInvalidValue);
+}
 
 extern "C" size_t h3qk_attention_workspace_bytes(const h3qk_attn* call)
 {

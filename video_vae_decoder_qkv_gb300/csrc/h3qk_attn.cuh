@@ -267,6 +267,14 @@ __host__ __device__ inline int64_t tile_part_floats(int dim) { return static_cas
 struct Maps {
     CUtensorMap q, k, v, dout;
 };
+// A tensor's map [items][heads][rows][dim]: boxes of box_rows by 64 channels,
+// 128-byte swizzle, zeros past the ends.
+H3QK_HIDDEN bool encode_map(CUtensorMap* m, const void* data, bool bf16, int64_t dim, int64_t rows, int64_t heads, int64_t items,
+                            int64_t row_bytes, int64_t head_bytes, int64_t item_bytes, int box_rows);
+// The current device's count of blocks that gave up waiting.
+H3QK_HIDDEN unsigned int* stuck_addr();
+// The runtime could not give the stuck counter or a tensor map.
+H3QK_HIDDEN h3qk_status no_maps();
 H3QK_HIDDEN cudaError_t forward_tiles(bool bf16, const Params& p, const Maps& m, cudaStream_t st);
 H3QK_HIDDEN cudaError_t forward_split(bool bf16, const Params& p, cudaStream_t st);
 H3QK_HIDDEN cudaError_t backward_tiles(bool bf16, const Params& p, const Maps& m, cudaStream_t st);

@@ -15,23 +15,48 @@ using h3qk_detail::range_of;
 
 constexpr int kLeastUnits = 4;
 
+// Sequences of up to kFew packed rows go to the kernel for few rows, which
+// reads (and converts) their keys once for each 16 of them; longer ones to the
+// tiles of 256.
+constexpr int64_t kFew = 32;
+
 // How a call is cut, from its sizes alone.
 struct Cut {
+    bool few, tiles;       // which kernels run: both where only the device knows the sequences' rows
     int row_tile, blocks;  // few rows
-    int64_t floats;        // of partial results
+    TileGrid grid;         // many rows
+    int64_t few_floats, tile_floats;  // of partial results
 };
 Cut cut_of(const h3qk_cache& c, const h3qk_cache_attn& a, int64_t max_rows)
 {
     Cut t = {};
-    const int64_t packed = max_rows * (a.heads / c.kv_heads);
-    t.row_tile = packed <= 8 ? 8 : 16;
-    const int64_t tiles = (packed + t.row_tile - 1) / t.row_tile;
-    const int64_t per = (static_cast<int64_t>(c.max_pages) * c.page_size + kUnit - 1) / kUnit;
-    const double units = static_cast<double>(c.batch) * c.kv_heads * tiles * (per > 0 ? per : 1);
-    const int most = few_blocks(c.format == H3QK_E2M1, t.row_tile);
-    const double want = std::ceil(units / kLeastUnits);
-    t.blocks = want < most ? static_cast<int>(want) : most;
-    t.floats = few_floats(t.blocks, t.row_tile, c.head_dim);
+    const int64_t group = a.heads / c.kv_heads, packed = max_rows * group;
+    const int sms = h3qk_internal_sm_count();
+    t.tiles = packed > kFew;
+    t.few = !t.tiles || a.q_offsets;
+    if (t.few) {
+        const int64_t rows = packed < kFew ? packed : kFew;
+        t.row_tile = rows <= 8 ? 8 : 16;
+        const int64_t tiles = (rows + t.row_tile - 1) / t.row_tile;
+        const int64_t per = (static_cast<int64_t>(c.max_pages) * c.page_size + kUnit - 1) / kUnit;
+        const double units = static_cast<double>(c.batch) * c.kv_heads * tiles * (per > 0 ? per : 1);
+        const int most = few_blocks(c.format == H3QK_E2M1, t.row_tile);
+        const double want = std::ceil(units / kLeastUnits);
+        t.blocks = want < most ? static_cast<int>(want) : most;
+        t.few_floats = (few_floats(t.blocks, t.row_tile, c.head_dim) + 3) / 4 * 4;
+    }
+    if (t.tiles) {
+        // Tiles of 256 at most: of all rows in full ones, and a partial one a sequence; or of sequences as long as may be.
+        const int64_t by_rows = a.tokens * group / h3qk_core::kRowTile + c.batch;
+        const int64_t by_batch = (packed + h3qk_core::kRowTile - 1) / h3qk_core::kRowTile * c.batch;
+        t.grid.blocks = (by_rows < by_batch ? by_rows : by_batch) * c.kv_heads;
+        if (a.q_offsets || 2 * t.grid.blocks <= sms) {
+            // (the device may find few enough to share out)
+            t.grid.join = t.grid.blocks < sms / 2 ? t.grid.blocks : sms / 2;
+            if (t.grid.blocks < sms) t.grid.blocks = sms;
+            t.tile_floats = sms * tile_floats(c.head_dim);
+        }
+    }
     return t;
 }
 
@@ -76,7 +101,8 @@ extern "C" size_t h3qk_cache_attention_workspace_bytes(const h3qk_cache* cache, 
 {
     int64_t rows;
     if (!cache || !call || check_call(*cache, *call, &rows) != H3QK_OK || rows == 0) return 0;
-    return static_cast<size_t>(cut_of(*cache, *call, rows).floats) * 4;
+    const Cut cut = cut_of(*cache, *call, rows);
+    return static_cast<size_t>(cut.few_floats + cut.tile_floats) * 4;
 }
 
 extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_cache_attn* call, h3qk_stream_t stream)
@@ -105,7 +131,8 @@ extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_
     if (!aligned(a.lse, 4) || !aligned(a.slopes, 4) || !aligned(a.prefix_lens, 4) || !aligned(a.q_offsets, 4))
         return H3QK_ERR_MISALIGNED;
     const Cut cut = cut_of(c, a, rows);
-    const size_t need = static_cast<size_t>(cut.floats) * 4;
+    if (cut.grid.blocks > INT32_MAX) return H3QK_ERR_INVALID_ARG;
+    const size_t need = static_cast<size_t>(cut.few_floats + cut.tile_floats) * 4;
     if (need && (!a.workspace || a.workspace_bytes < need)) return H3QK_ERR_INVALID_ARG;
     if (need && !aligned(a.workspace, 16)) return H3QK_ERR_MISALIGNED;
     const Range outs[3] = {out, range_of(a.lse, a.heads * a.tokens * 4), range_of(a.workspace, need)};
@@ -135,9 +162,37 @@ extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_
     p.q_token = a.q_token_stride, p.q_head = a.q_head_stride;
     p.out_token = a.out_token_stride, p.out_head = a.out_head_stride;
     p.lse = a.lse;
-    p.part = static_cast<float*>(a.workspace);
-    p.few = INT64_MAX;
+    p.few = kFew;
     p.least = kLeastUnits;
+    p.sms = h3qk_internal_sm_count();
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return h3qk_ops::status_of(cache_few(a.dtype == H3QK_BF16, c.format == H3QK_E2M1, cut.row_tile, cut.blocks, p, st));
+    const bool bf16 = a.dtype == H3QK_BF16, e2m1 = c.format == H3QK_E2M1;
+    cudaError_t e = cudaSuccess;
+    if (cut.few) {
+        p.part = static_cast<float*>(a.workspace);
+        e = cache_few(bf16, e2m1, cut.row_tile, cut.blocks, p, st);
+    }
+    if (e == cudaSuccess && cut.tiles) {
+        p.part = static_cast<float*>(a.workspace) + cut.few_floats;
+        p.stuck = h3qk_core::stuck_addr();
+        Maps m = {};
+        bool ok = p.stuck != nullptr;
+        if (!e2m1) {
+            // A pool without pages is described as its rows' own tensor: no page of it is ever named.
+            const bool none = c.pages == 0;
+            const int64_t row = c.head_dim * 2, rows_a_page = none ? 16 : c.page_size;
+            const int box = static_cast<int>(c.page_size < 128 ? c.page_size : 128);
+            const void* data[2] = {none ? a.q : c.k, none ? a.q : c.v};
+            CUtensorMap* maps[2] = {&m.k, &m.v};
+            const int64_t strides[2][3] = {{p.c.k_row, p.c.k_head, p.c.k_page}, {p.c.v_row, p.c.v_head, p.c.v_page}};
+            for (int i = 0; i < 2; ++i)
+                ok = ok && h3qk_core::encode_map(maps[i], data[i], bf16, c.head_dim, rows_a_page, none ? 1 : c.kv_heads,
+                                                 none ? 1 : c.pages, none ? row : strides[i][0], none ? 16 * row : strides[i][1],
+                                                 none ? 16 * row : strides[i][2], none ? 16 : box);
+        }
+        if (!ok) return h3qk_core::no_maps();
+        if (e2m1) e = bf16 ? cache_tiles_e2m1_bf16(p, m, cut.grid, st) : cache_tiles_e2m1_fp16(p, m, cut.grid, st);
+        else e = bf16 ? cache_tiles_bf16(p, m, cut.grid, st) : cache_tiles_fp16(p, m, cut.grid, st);
+    }
+    return h3qk_ops::status_of(e);
 }

@@ -22,10 +22,10 @@ struct Attn {
     uint16_t* out;
     int64_t q_token, q_head, out_token, out_head;  // elements
     float* lse;                  // [heads][tokens]
-    float* part;                 // partial results
+    float* part;                 // partial results of the kernel that is launched
     int64_t few;                 // sequences of at most so many packed rows go to the kernel for few rows
     int32_t least;               // few rows: units that a block takes at least
-    int32_t tiles, parts;        // many rows: tiles of the longest sequence; blocks that share a tile's keys
+    int32_t sms;                 // many rows: the SMs, to share out few tiles' keys among
     unsigned int* stuck;
 };
 
@@ -62,10 +62,53 @@ __device__ __forceinline__ h3qk_core::Bend bend_of(const Attn& p, int head, floa
     return b;
 }
 
+// A row of bfloat16 becomes one of binary16 without loss that binary32 sums
+// would keep: times 2^(141 - e), e the exponent field of its largest magnitude
+// (given as bits), so that this comes to lie in [2^14, 2^15).  Rows with an
+// infinity or NaN stay as they are.
+__device__ __forceinline__ float raise_of(uint32_t top, int& e)
+{
+    e = top >> 7;
+    e = e == 255 ? 141 : max(e, 15);
+    return __int_as_float((127 + 141 - e) << 23);
+}
+
+// Writes 4 channels of one joined packed row (d = 0: its lse too).
+template <bool BF16>
+__device__ __forceinline__ void finish_row(const Attn& p, const Sequence& s, int kv, int64_t r, int d, float4 v, float top,
+                                           float sum, float shift, float v_scale)
+{
+    using h3qk_tc::round_pair;
+    const int head = kv * p.group + static_cast<int>(r % p.group);
+    const int64_t token = s.first + r / p.group;
+    const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
+    if (d < p.c.dim) {
+        uint2 w;
+        w.x = round_pair<BF16>(v.x * inv, v.y * inv);
+        w.y = round_pair<BF16>(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(p.out + token * p.out_token + head * p.out_head + d) = w;
+    }
+    if (d == 0)
+        p.lse[static_cast<int64_t>(head) * p.tokens + token] =
+            sum == 0.0f ? -INFINITY : (top - shift + log2f(sum)) * h3qk_core::kLn2;
+}
+
 // Host side: the kernels' launchers.
+struct Maps {
+    CUtensorMap k, v;  // 16-bit pages
+};
+struct TileGrid {
+    int64_t blocks, join;  // blocks of tiles or their parts; tiles that may have been shared (0: none)
+};
+// Floats that a block leaves which shares a tile: per packed row O[dim], then m and sum.
+inline int64_t tile_floats(int dim) { return h3qk_core::tile_part_floats(dim); }
 constexpr int kUnit = 64;  // keys of a unit of work of the kernel for few rows
 H3QK_HIDDEN int few_blocks(bool e2m1, int row_tile);
 H3QK_HIDDEN int64_t few_floats(int blocks, int rows, int dim);
 H3QK_HIDDEN cudaError_t cache_few(bool bf16, bool e2m1, int row_tile, int blocks, const Attn& p, cudaStream_t st);
+H3QK_HIDDEN cudaError_t cache_tiles_e2m1_fp16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st);
+H3QK_HIDDEN cudaError_t cache_tiles_e2m1_bf16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st);
+H3QK_HIDDEN cudaError_t cache_tiles_fp16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st);
+H3QK_HIDDEN cudaError_t cache_tiles_bf16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st);
 
 }  // namespace h3qk_pages

@@ -396,24 +396,6 @@ __device__ __forceinline__ int64_t share_of(const Attn& p, int64_t total, int bl
 // begins in the middle of (or fills), and of the one that it breaks off.
 __host__ __device__ inline int64_t part_floats(int rows, int dim) { return static_cast<int64_t>(rows) * (dim + 2); }
 
-template <bool BF16>
-__device__ __forceinline__ void finish_row(const Attn& p, const Sequence& s, int kv, int64_t r, int d, float4 v, float top,
-                                           float sum, float shift, float v_scale)
-{
-    const int head = kv * p.group + static_cast<int>(r % p.group);
-    const int64_t token = s.first + r / p.group;
-    const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
-    if (d < p.c.dim) {
-        uint2 w;
-        w.x = round_pair<BF16>(v.x * inv, v.y * inv);
-        w.y = round_pair<BF16>(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(p.out + token * p.out_token + head * p.out_head + d) = w;
-    }
-    if (d == 0)
-        p.lse[static_cast<int64_t>(head) * p.tokens + token] =
-            sum == 0.0f ? -INFINITY : (top - shift + log2f(sum)) * h3qk_core::kLn2;
-}
-
 template <class T, bool BF16, int NB>
 __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const __grid_constant__ Attn p)
 {
@@ -479,10 +461,8 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                     top = max(top & 0xffffu, top >> 16);
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // times 2^(141 - e) with e the largest exponent field; rows with an infinity or NaN as they are
-                    int e = top >> 7;
-                    e = e == 255 ? 141 : max(e, 15);
-                    const float up = __int_as_float((127 + 141 - e) << 23);
+                    int e;
+                    const float up = raise_of(top, e);
                     raw *= __int_as_float((127 + e - 141) << 23);
 #pragma unroll
                     for (int k = 0; k < 2 * kSteps; ++k) {

@@ -1,0 +1,8 @@
+// The instances of the paged tile kernel for 4-bit pages, bf16 rows, in a unit of
+// their own so that they compile in parallel.
+#include "h3qk_cache_tiles.cuh"
+
+cudaError_t h3qk_pages::cache_tiles_e2m1_bf16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st)
+{
+    return by_shape<true, true>(p, m, grid, st);
+}
