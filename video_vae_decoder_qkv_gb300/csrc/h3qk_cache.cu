@@ -301,7 +301,7 @@ h3qk_status check_strides(const h3qk_cache& c, const void* data, h3qk_strides s,
                           Span* out)
 {
     if (!data && c.pages > 0) return H3QK_ERR_INVALID_ARG;
-    const int64_t most = INT64_C(1) << 38;
+    const int64_t most = (INT64_C(1) << 36) / size;
     if (c.kv_heads == 1) s.head = c.page_size * s.row;
     if (c.pages <= 1) s.item = c.kv_heads * s.head;
     if (s.row * size < row_bytes || s.head <= 0 || s.item <= 0) return H3QK_ERR_INVALID_ARG;
@@ -402,6 +402,8 @@ h3qk_status h3qk_pages::check_pool(const h3qk_cache* cache, bool written, Pool* 
     p.v_page = s[1].page, p.v_head = s[1].head, p.v_row = s[1].row;
     p.ks_page = s[2].page, p.ks_head = s[2].head;
     p.vs_page = s[3].page, p.vs_head = s[3].head;
+    p.k_page16 = static_cast<uint32_t>(s[0].page / 16), p.v_page16 = static_cast<uint32_t>(s[1].page / 16);
+    p.ks_page16 = static_cast<uint32_t>(s[2].page / 16), p.vs_page16 = static_cast<uint32_t>(s[3].page / 16);
     p.table = c.block_table;
     p.table_stride = stride;
     p.kv_lens = c.kv_lens;

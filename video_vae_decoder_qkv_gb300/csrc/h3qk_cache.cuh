@@ -11,6 +11,7 @@ struct Pool {
     uint8_t *k, *v, *k_scales, *v_scales;
     int64_t k_page, k_head, k_row, v_page, v_head, v_row;
     int64_t ks_page, ks_head, vs_page, vs_head;
+    uint32_t k_page16, v_page16, ks_page16, vs_page16;  // the page strides in pieces of 16 bytes
     const int32_t* table;
     int64_t table_stride;
     const int32_t* kv_lens;

@@ -153,6 +153,7 @@ extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_
     p.heads = a.heads;
     p.group = a.heads / c.kv_heads;
     p.causal = a.causal;
+    p.bf16 = a.dtype == H3QK_BF16;
     p.scale = a.scale > 0.0f ? a.scale : 1.0f / std::sqrt(static_cast<float>(c.head_dim));
     p.cap = a.softcap;
     p.slopes = a.slopes;
@@ -166,11 +167,11 @@ extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_
     p.least = kLeastUnits;
     p.sms = h3qk_internal_sm_count();
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const bool bf16 = a.dtype == H3QK_BF16, e2m1 = c.format == H3QK_E2M1;
+    const bool bf16 = p.bf16 != 0, e2m1 = c.format == H3QK_E2M1;
     cudaError_t e = cudaSuccess;
     if (cut.few) {
         p.part = static_cast<float*>(a.workspace);
-        e = cache_few(bf16, e2m1, cut.row_tile, cut.blocks, p, st);
+        e = cache_few(e2m1, cut.row_tile, cut.blocks, p, st);
     }
     if (e == cudaSuccess && cut.tiles) {
         p.part = static_cast<float*>(a.workspace) + cut.few_floats;

@@ -15,6 +15,7 @@ struct Attn {
     const int32_t* offsets;      // or null: `each` rows a sequence
     int32_t each, tokens, max_rows;
     int32_t heads, group, causal;
+    int32_t bf16;                // what q and out are
     float scale, cap;
     const float* slopes;
     const int32_t* prefix_lens;
@@ -55,7 +56,8 @@ __device__ __forceinline__ h3qk_core::Bend bend_of(const Attn& p, int head, floa
     // `raw`: what a raw score has to be multiplied with to be q.k.
     using namespace h3qk_core;
     Bend b;
-    b.plain = p.scale * kLog2e * raw;
+    // (positive and finite, so that it keeps a hidden score's -infinity)
+    b.plain = fminf(fmaxf(p.scale * kLog2e * raw, 0x1p-126f), 3.0e38f);
     b.in = p.cap > 0.0f ? fminf(p.scale * 2.0f * kLog2e / p.cap, 3.0e38f) * raw : b.plain;
     b.cap = p.cap * kLog2e;
     b.slope = p.slopes ? __ldg(p.slopes + head) * kLog2e : 0.0f;
@@ -74,7 +76,6 @@ __device__ __forceinline__ float raise_of(uint32_t top, int& e)
 }
 
 // Writes 4 channels of one joined packed row (d = 0: its lse too).
-template <bool BF16>
 __device__ __forceinline__ void finish_row(const Attn& p, const Sequence& s, int kv, int64_t r, int d, float4 v, float top,
                                            float sum, float shift, float v_scale)
 {
@@ -84,8 +85,8 @@ __device__ __forceinline__ void finish_row(const Attn& p, const Sequence& s, int
     const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
     if (d < p.c.dim) {
         uint2 w;
-        w.x = round_pair<BF16>(v.x * inv, v.y * inv);
-        w.y = round_pair<BF16>(v.z * inv, v.w * inv);
+        w.x = p.bf16 ? round_pair<true>(v.x * inv, v.y * inv) : round_pair<false>(v.x * inv, v.y * inv);
+        w.y = p.bf16 ? round_pair<true>(v.z * inv, v.w * inv) : round_pair<false>(v.z * inv, v.w * inv);
         *reinterpret_cast<uint2*>(p.out + token * p.out_token + head * p.out_head + d) = w;
     }
     if (d == 0)
@@ -105,7 +106,7 @@ inline int64_t tile_floats(int dim) { return h3qk_core::tile_part_floats(dim); }
 constexpr int kUnit = 64;  // keys of a unit of work of the kernel for few rows
 H3QK_HIDDEN int few_blocks(bool e2m1, int row_tile);
 H3QK_HIDDEN int64_t few_floats(int blocks, int rows, int dim);
-H3QK_HIDDEN cudaError_t cache_few(bool bf16, bool e2m1, int row_tile, int blocks, const Attn& p, cudaStream_t st);
+H3QK_HIDDEN cudaError_t cache_few(bool e2m1, int row_tile, int blocks, const Attn& p, cudaStream_t st);
 H3QK_HIDDEN cudaError_t cache_tiles_e2m1_fp16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st);
 H3QK_HIDDEN cudaError_t cache_tiles_e2m1_bf16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st);
 H3QK_HIDDEN cudaError_t cache_tiles_fp16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st);

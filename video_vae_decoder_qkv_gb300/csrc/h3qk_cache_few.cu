@@ -32,6 +32,8 @@
 // is held 2^11 larger.  V's codes of two neighbouring keys are interleaved by
 // nibbles before their conversion, which makes the pairs that the product
 // takes.
+#include <type_traits>
+
 #include "h3qk_cache_attn.cuh"
 
 namespace {
@@ -111,91 +113,112 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i)
 
 // Where a warp's keys come from: one sequence and K/V head.
 struct Source {
-    const uint8_t *k, *v, *ks, *vs;  // the head's rows in page 0
-    const int32_t* table;
-    int end;  // keys of the run that are looked at
+    const uint4 *k, *v, *ks, *vs;  // the head's rows in page 0, at this lane's first piece
+    int end;                       // keys of the run that are looked at
 };
 
-// 4-bit pages.  A turn is 32 keys: codes of K and V, DP / 2 bytes a key, and
-// their scales.  16-byte pieces are spread over a 128-byte line's slots so
-// that the lanes that read K (4 of a key, 8 keys) and V (8 of a key, 4 keys)
-// meet no bank twice.
-template <int DP, int NB>
+// 4-bit pages.  A turn is 32 keys: codes of K and V, DP / 2 bytes a key (of
+// which DIM / 2 are copied), and their scales.  Copies run through the rows
+// as they lie in memory; the 16-byte pieces are spread over a 128-byte line's
+// slots so that the lanes that read K (4 of a key, 8 keys) and V (8 of a key,
+// 4 keys) meet no bank twice.  Where a lane copies and reads is fixed but for
+// constants, and kept.
+template <int DIM, int NB>
 struct Codes {
     static constexpr bool kE2m1 = true;
-    static constexpr int kDim = DP;
-    static constexpr int kTurn = 32, kWarps = NB == 1 ? 8 : 4, kStages = 3;
+    static constexpr int kDim = DIM, DP = DIM <= 64 ? 64 : 128;
+    static constexpr int kTurn = 32, kWarps = NB == 1 ? 8 : 4, kStages = 3, kBlocks = NB == 1 ? 2 : 3;
     static constexpr int kPitch = DP / 2;
-    static constexpr int kScales = 2 * kTurn * kPitch;  // where the scales begin
+    static constexpr int kGroups = DIM / 16;            // scale bytes a row
+    static constexpr int kScales = 2 * kTurn * kPitch;  // where the scales begin; V's follow K's
     static constexpr int kStage = kScales + 2 * kTurn * (DP / 16);
-    static constexpr int kBlocks = NB == 1 ? 2 : 3;  // an SM
 
-    __device__ static uint32_t slot(int row, int piece)
+    int copy_to, copy_from;    // this lane's first piece: in a stage, in memory (bytes of a row of pieces)
+    int scale_to, scale_from;  // its piece of scales
+    int k_at, v_at, ks_at, vs_at;
+    bool copies, copies_scales, k_in;
+
+    __device__ static int slot(int row, int piece)
     {
         if constexpr (DP == 128) return row / 2 * 128 + ((((row & 1) * 4 + piece) ^ ((row >> 1 & 3) * 2)) * 16);
         else return row / 4 * 128 + ((((row & 3) * 2 + piece) ^ ((row >> 2 & 1) * 2)) * 16);
     }
-    // The channel where a lane's share of a K row (and of Q) begins, and of piece i of 8.
+    static constexpr int kPieces = DP / 32, kRowsEach = 32 / kPieces;  // pieces a row; rows of a warp-wide copy
+
+    __device__ Codes(const Pool&, int lane)
+    {
+        const int g = lane >> 2, c = lane & 3, row = lane / kPieces, piece = lane % kPieces;
+        copies = 32 * piece < DIM;
+        copy_to = slot(row, piece);
+        copy_from = row * (DIM / 2) + 16 * piece;
+        // 16 rows' scales lie together, DIM bytes: lanes 0-7 and 8-15 take K's two halves, 16-31 V's
+        copies_scales = 16 * (lane & 7) < DIM;
+        scale_to = kScales + (lane >> 4) * kTurn * (DP / 16) + (lane >> 3 & 1) * DP + 16 * (lane & 7);
+        scale_from = 16 * (lane & 7);
+        k_in = DP / 4 * c < DIM;
+        k_at = DP == 128 ? slot(g, c) : slot(g, c >> 1) + 8 * (c & 1);
+        v_at = kTurn * kPitch + (DP == 128 ? slot(2 * c, g >> 1) + 8 * (g & 1) : slot(2 * c, g >> 2) + 4 * (g & 3));
+        ks_at = kScales + g * kGroups + (DP == 128 ? 2 * c : c);
+        vs_at = kScales + kTurn * (DP / 16) + 2 * c * kGroups + (DP == 128 ? g : g >> 1);
+    }
+    // The channel where piece i of 8 of a lane's share of a Q row begins.
     __device__ static int k_channel(int c, int i) { return DP / 4 * c + 8 * i; }
     // The channel of rows g and g + 8 of product m of O^T: this and the next.
     __device__ static int v_channel(int g, int m) { return DP / 8 * g + 2 * m; }
 
-    __device__ static void fetch(const Pool& c, const Source& s, uint32_t to, int j, const int (&page)[2], int lane)
+    __device__ void fetch(const Pool& c, const Source& s, uint32_t to, int j, const int (&page)[2], int lane) const
     {
-        constexpr int kPieces = DP / 32, kPer = kTurn * kPieces / 32;  // pieces a row; copies a lane
         const int mask = (1 << c.page_shift) - 1;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = lane + 32 * i, row = at / kPieces, piece = at % kPieces;
-            const int pg = page[i / (kPer / 2)];
-            const bool there = pg >= 0;
-            const int64_t in_page = (j + row) & mask;
-            if (32 * piece < c.dim) {
-                copy16(to + slot(row, piece), there ? s.k + pg * c.k_page + in_page * c.k_row + 16 * piece : s.k, there);
-                copy16(to + kTurn * kPitch + slot(row, piece),
-                       there ? s.v + pg * c.v_page + in_page * c.v_row + 16 * piece : s.v, there);
+        for (int h = 0; h < 2; ++h) {
+            const bool there = page[h] >= 0;
+            const uint32_t pg = there ? page[h] : 0;
+            const int in_page = (j + 16 * h) & mask;
+            const uint8_t* k = reinterpret_cast<const uint8_t*>(s.k + static_cast<uint64_t>(pg) * c.k_page16) + in_page * (DIM / 2) + copy_from;
+            const uint8_t* v = reinterpret_cast<const uint8_t*>(s.v + static_cast<uint64_t>(pg) * c.v_page16) + in_page * (DIM / 2) + copy_from;
+            if (DIM == DP || copies) {
+#pragma unroll
+                for (int i = 0; i < 16 / kRowsEach; ++i) {
+                    const int dst = (h * 16 + i * kRowsEach) * kPitch;
+                    copy16(to + copy_to + dst, k + i * kRowsEach * (DIM / 2), there);
+                    copy16(to + copy_to + dst + kTurn * kPitch, v + i * kRowsEach * (DIM / 2), there);
+                }
             }
         }
-        // 16 rows' scales lie together: dim bytes.
-        const int half = lane >> 3 & 1, piece = lane & 7;
-        if (16 * piece < c.dim) {
-            const int pg = half ? page[1] : page[0];
-            const bool there = pg >= 0, v = lane >= 16;
-            const int64_t in_page = (j + 16 * half) & mask;
-            const uint8_t* from = v ? s.vs + pg * c.vs_page : s.ks + pg * c.ks_page;
-            copy16(to + kScales + (v ? kTurn * (DP / 16) : 0) + half * DP + 16 * piece,
-                   there ? from + in_page * (c.dim / 16) + 16 * piece : s.ks, there);
-        }
+        const int pick = lane & 8 ? page[1] : page[0];
+        const uint32_t pg = pick >= 0 ? pick : 0;
+        const int in_page = (j + 2 * (lane & 8)) & mask;
+        const uint4* base = lane & 16 ? s.vs + static_cast<uint64_t>(pg) * c.vs_page16 : s.ks + static_cast<uint64_t>(pg) * c.ks_page16;
+        if (DIM == 128 || copies_scales)
+            copy16(to + scale_to, reinterpret_cast<const uint8_t*>(base) + in_page * kGroups + scale_from, pick >= 0);
     }
 
-    // Rows 16 kb + g and + 8 of K as the products' A, steps of 4 channels a lane, for f(step, a).
-    template <class F>
-    __device__ static void keys(const Pool& c, uint32_t at, int kb, int g, int cc, int left, F&& f)
+    // Rows 16 kb + g and + 8 of K as the products' A, steps of 4 channels a
+    // lane, for f(step, a).  EDGE: rows from `left` on hold nothing.
+    template <bool EDGE, class F>
+    __device__ void keys(uint32_t at, int kb, int g, int left, F&& f) const
     {
         constexpr int kWords = DP / 32;
         uint32_t w[2][kWords], sc[2][2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int row = 16 * kb + 8 * t + g;
-            const uint32_t scales = at + kScales + kb * DP + (row & 15) * (c.dim / 16);
+            const uint32_t from = at + k_at + (16 * kb + 8 * t) * kPitch;
+            const uint32_t scales = at + ks_at + kb * DP + 8 * t * kGroups;
             uint32_t two;
             if constexpr (DP == 128) {
-                const uint4 v = lds128(at + slot(row, cc));
+                const uint4 v = lds128(from);
                 w[t][0] = v.x, w[t][1] = v.y, w[t][2] = v.z, w[t][3] = v.w;
-                two = lds16(scales + 2 * cc);
+                two = lds16(scales);
             } else {
-                const uint2 v = lds64(at + slot(row, cc >> 1) + 8 * (cc & 1));
+                const uint2 v = lds64(from);
                 w[t][0] = v.x, w[t][1] = v.y;
-                two = lds8(scales + cc);
+                two = lds8(scales);
             }
-            const bool there = row < left && DP / 4 * cc < c.dim;
-            if (!there) two = 0;
-#pragma unroll
-            for (int i = 0; i < kWords; ++i)
-                if (!there) w[t][i] = 0;
+            if (DIM < DP && !k_in) two = 0;
+            if (EDGE && 16 * kb + 8 * t + g >= left) two = 0;
             const uint32_t wide = widen_scales(two);
             sc[t][0] = __byte_perm(wide, wide, 0x1010);
-            sc[t][1] = __byte_perm(wide, wide, 0x3232);
+            if constexpr (DP == 128) sc[t][1] = __byte_perm(wide, wide, 0x3232);
         }
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
@@ -215,25 +238,24 @@ struct Codes {
     }
 
     // Keys 16 kb + {2c, 2c + 1, 2c + 8, 2c + 9} of V as the products' A (channels as rows), for f(m, a).
-    template <class F>
-    __device__ static void values(const Pool& c, uint32_t at, int kb, int g, int cc, int left, F&& f)
+    template <bool EDGE, class F>
+    __device__ void values(uint32_t at, int kb, int c, int left, F&& f) const
     {
         constexpr int kWords = DP / 64;
         uint32_t w[4][kWords], byte[4];
-        const uint32_t codes = at + kTurn * kPitch;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int in = 2 * cc + (t & 1) + 8 * (t >> 1), row = 16 * kb + in;
-            const uint32_t scales = at + kScales + kTurn * (DP / 16) + kb * DP + in * (c.dim / 16);
+            // (an odd row's pieces lie where the even one's would with the row's bit of the slot set)
+            const uint32_t flip = (t & 1) ? (DP == 128 ? 64 : 32) : 0;
+            const uint32_t from = at + ((v_at ^ flip) + (16 * kb + 8 * (t >> 1)) * kPitch);
+            byte[t] = lds8(at + vs_at + kb * DP + ((t & 1) + 8 * (t >> 1)) * kGroups);
             if constexpr (DP == 128) {
-                const uint2 v = lds64(codes + slot(row, g >> 1) + 8 * (g & 1));
+                const uint2 v = lds64(from);
                 w[t][0] = v.x, w[t][1] = v.y;
-                byte[t] = lds8(scales + g);
             } else {
-                w[t][0] = lds32(codes + slot(row, g >> 2) + 4 * (g & 3));
-                byte[t] = lds8(scales + (g >> 1));
+                w[t][0] = lds32(from);
             }
-            if (row >= left) byte[t] = 0;
+            if (EDGE && 16 * kb + 2 * c + (t & 1) + 8 * (t >> 1) >= left) byte[t] = 0;
         }
         const uint32_t s01 = widen_scales(byte[0] | byte[1] << 8), s23 = widen_scales(byte[2] | byte[3] << 8);
 #pragma unroll
@@ -256,67 +278,78 @@ struct Codes {
     }
 };
 
-// 16-bit pages.  A turn is 16 keys; each lane copies just the 16-byte pieces
-// that it uses itself, into slots of its own.
-template <int DP, int NB>
+// 16-bit pages.  A turn is 16 keys.  Copies run through the rows as they lie
+// in memory; a row's 16-byte pieces are turned by the row's number, so that
+// the four lanes that read a key's pieces meet no bank twice (V's lanes
+// meet at most in pairs).
+template <int DP_, int NB>
 struct Halves {
     static constexpr bool kE2m1 = false;
-    static constexpr int kDim = DP;
-    static constexpr int kTurn = 16, kWarps = 4, kStages = 3;
-    static constexpr int kStage = 2 * kTurn * DP * 2;
-    static constexpr int kBlocks = 2;
+    static constexpr int kDim = DP_, DP = DP_;
+    static constexpr int kTurn = 16, kWarps = 4, kStages = 3, kBlocks = 2;
+    static constexpr int kPitch = DP * 2, kStage = 2 * kTurn * kPitch;
     static constexpr int kK = DP / 32, kV = DP / 64;  // pieces of a lane's K row and V row
+    static constexpr int kPieces = DP / 8, kRowsEach = 32 / kPieces;
 
+    int copy_to[DP == 128 ? 4 : 2];  // by the turn's rows modulo 8
+    int64_t from_k, from_v;
+    bool copies;
+
+    __device__ static int slot(int row, int piece) { return row * kPitch + ((piece ^ ((row & 1) * 4 + (row >> 1 & 3))) * 16); }
+
+    __device__ Halves(const Pool& c, int lane)
+    {
+        const int row = lane / kPieces, piece = lane % kPieces;
+        copies = 8 * piece < c.dim;
+        from_k = row * c.k_row + 16 * piece;
+        from_v = row * c.v_row + 16 * piece;
+#pragma unroll
+        for (int i = 0; i < (DP == 128 ? 4 : 2); ++i) copy_to[i] = slot(i * kRowsEach + row, piece);
+    }
     __device__ static int k_channel(int c, int i) { return 8 * (c + 4 * i); }
     __device__ static int v_channel(int g, int m) { return m / 4 * 64 + 8 * g + 2 * (m % 4); }
 
-    __device__ static void fetch(const Pool& c, const Source& s, uint32_t to, int j, const int (&page)[2], int lane)
+    __device__ void fetch(const Pool& c, const Source& s, uint32_t to, int j, const int (&page)[2], int lane) const
     {
-        const int g = lane >> 2, cc = lane & 3;
+        constexpr int kEight = 8 / kRowsEach;  // copies of 8 rows
+        const uint32_t pg = page[0] >= 0 ? page[0] : 0;
+        const bool there = page[0] >= 0 && copies;  // (channels past the last are zeros)
         const int64_t in_page = j & ((1 << c.page_shift) - 1);
-        const bool there = page[0] >= 0;
-        const uint8_t* k = s.k + page[0] * c.k_page + in_page * c.k_row;
-        const uint8_t* v = s.v + page[0] * c.v_page + in_page * c.v_row;
+        const uint8_t* k = reinterpret_cast<const uint8_t*>(s.k + static_cast<uint64_t>(pg) * c.k_page16) + in_page * c.k_row + from_k;
+        const uint8_t* v = reinterpret_cast<const uint8_t*>(s.v + static_cast<uint64_t>(pg) * c.v_page16) + in_page * c.v_row + from_v;
+        const int left = s.end - j - lane / kPieces;  // (rows that hold nothing may be NaN: zeros instead)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < kK; ++i) {
-                const int channel = k_channel(cc, i);
-                const bool ok = there && channel < c.dim && j + 8 * t + g < s.end;
-                copy16(to + ((t * kK + i) * 32 + lane) * 16, ok ? k + (8 * t + g) * c.k_row + 2 * channel : s.k, ok);
-            }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const int channel = 64 * i + 8 * g, row = 2 * cc + (t & 1) + 8 * (t >> 1);
-                const bool ok = there && channel < c.dim && j + row < s.end;
-                copy16(to + ((2 * kK + t * kV + i) * 32 + lane) * 16, ok ? v + row * c.v_row + 2 * channel : s.v, ok);
-            }
+        for (int i = 0; i < kTurn / kRowsEach; ++i) {
+            const uint32_t dst = to + copy_to[i % kEight] + i / kEight * 8 * kPitch;
+            const bool ok = there && i * kRowsEach < left;
+            copy16(dst, k + i * kRowsEach * c.k_row, ok);
+            copy16(dst + kTurn * kPitch, v + i * kRowsEach * c.v_row, ok);
+        }
     }
 
-    template <class F>
-    __device__ static void keys(const Pool&, uint32_t at, int, int g, int cc, int, F&& f)
+    template <bool EDGE, class F>
+    __device__ void keys(uint32_t at, int, int g, int, F&& f) const
     {
-        const uint32_t mine = at + (4 * g + cc) * 16;
+        const int c = threadIdx.x & 3;
 #pragma unroll
         for (int i = 0; i < kK; ++i) {
-            const uint4 x = lds128(mine + i * 512), y = lds128(mine + (kK + i) * 512);
+            const uint32_t from = at + slot(g, c + 4 * i);
+            const uint4 x = lds128(from), y = lds128(from + 8 * kPitch);
             const uint32_t a[4] = {x.x, y.x, x.y, y.y}, b[4] = {x.z, y.z, x.w, y.w};
             f(2 * i, a);
             f(2 * i + 1, b);
         }
     }
 
-    template <class F>
-    __device__ static void values(const Pool&, uint32_t at, int, int g, int cc, int, F&& f)
+    template <bool EDGE, class F>
+    __device__ void values(uint32_t at, int, int c, int, F&& f) const
     {
-        const uint32_t mine = at + (4 * g + cc) * 16;
+        const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             uint4 x[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) x[t] = lds128(mine + (2 * kK + t * kV + i) * 512);
+            for (int t = 0; t < 4; ++t) x[t] = lds128(at + kTurn * kPitch + slot(2 * c + (t & 1), g + 8 * i) + 8 * (t >> 1) * kPitch);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t a[4] = {__byte_perm(word(x[0], e), word(x[1], e), 0x5410),
@@ -396,13 +429,13 @@ __device__ __forceinline__ int64_t share_of(const Attn& p, int64_t total, int bl
 // begins in the middle of (or fills), and of the one that it breaks off.
 __host__ __device__ inline int64_t part_floats(int rows, int dim) { return static_cast<int64_t>(rows) * (dim + 2); }
 
-template <class T, bool BF16, int NB>
+// HALF: the products are binary16's.  BENT: scores are capped, or less a slope times the distance.
+template <class T, bool HALF, bool BENT, int NB>
 __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const __grid_constant__ Attn p)
 {
-    constexpr int ROWS = 8 * NB, DP = T::kDim;
+    constexpr int ROWS = 8 * NB, DP = T::DP;
     constexpr int kWarps = T::kWarps, KB = T::kTurn / 16, kSteps = DP / 16, kOut = DP / 16;
-    constexpr bool kHalf = T::kE2m1 || !BF16;  // the products are binary16's
-    constexpr float kShift = kHalf ? kRaise : 0.0f;
+    constexpr float kShift = HALF ? kRaise : 0.0f;
     static_assert(T::kWarps * T::kStages * T::kStage >= kWarps * ROWS * (DP + 4) * 4, "the warps' O fits the rings");
     extern __shared__ __align__(128) uint8_t dynamic[];
     __shared__ float sh_m[kWarps][ROWS], sh_l[kWarps][ROWS];
@@ -411,7 +444,7 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
     const int c = lane & 3, g = lane >> 2;
     const uint32_t ring = smem_addr(dynamic) + warp * T::kStages * T::kStage;
     float(*sh_o)[ROWS][DP + 4] = reinterpret_cast<float(*)[ROWS][DP + 4]>(dynamic);
-    const bool capped = p.cap > 0.0f;
+    const T format(p.c, lane);
 
     const int64_t total = all_units<ROWS>(p), share = share_of(p, total, gridDim.x);
     const int64_t begin = blockIdx.x * share, end = min(begin + share, total);
@@ -434,10 +467,11 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
 
         // This lane's packed row of each block of 8 for Q, and the two whose scores it holds.
         float o[kOut][NB][4], m[NB][2], l[NB][2];
-        float in[NB][2], plain[NB][2], slope[NB][2];
-        int lim[NB][2], at[NB][2];
+        float in[NB][2];
+        [[maybe_unused]] float plain[NB][2], slope[NB][2];
+        [[maybe_unused]] int at[NB][2];
+        int lim[NB][2], most = 0, least = 1 << 30;  // rows that are none see everything: nobody reads them
         uint32_t q[NB][2 * kSteps];
-        int most = 0;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int64_t r = static_cast<int64_t>(row_tile) * ROWS + 8 * b + g;
@@ -454,7 +488,7 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
             float raw = 1.0f;
             if constexpr (T::kE2m1) {
                 raw = p.c.k_scale;
-                if constexpr (BF16) {
+                if (p.bf16) {
                     uint32_t top = 0;
 #pragma unroll
                     for (int e = 0; e < 2 * kSteps; ++e) top = __vmaxu2(top, q[b][e] & 0x7fff7fffu);
@@ -482,40 +516,145 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 plain[b][h] = bend.plain;
                 slope[b][h] = bend.slope;
                 at[b][h] = s.start + i_of;
-                lim[b][h] = has_of ? limit_of(s, p.causal, i_of) : 0;
-                most = max(most, lim[b][h]);
+                lim[b][h] = 1 << 30;
+                if (has_of) {
+                    lim[b][h] = limit_of(s, p.causal, i_of);
+                    most = max(most, lim[b][h]);
+                    least = min(least, lim[b][h]);
+                }
                 m[b][h] = -INFINITY;
                 l[b][h] = 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < kOut; ++k) o[k][b][0] = o[k][b][1] = o[k][b][2] = o[k][b][3] = 0.0f;
         }
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        const float cap2 = p.cap * h3qk_core::kLog2e;
+#pragma unroll
+        for (int e = 1; e < 4; e <<= 1) {
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, e));
+            least = min(least, __shfl_xor_sync(0xffffffffu, least, e));
+        }
 
         Source src;
-        src.k = p.c.k + kv * p.c.k_head;
-        src.v = p.c.v + kv * p.c.v_head;
-        src.ks = p.c.k_scales + kv * p.c.ks_head;
-        src.vs = p.c.v_scales + kv * p.c.vs_head;
-        src.table = p.c.table + item * p.c.table_stride;
+        src.k = reinterpret_cast<const uint4*>(p.c.k + kv * p.c.k_head);
+        src.v = reinterpret_cast<const uint4*>(p.c.v + kv * p.c.v_head);
+        src.ks = reinterpret_cast<const uint4*>(p.c.k_scales + kv * p.c.ks_head);
+        src.vs = reinterpret_cast<const uint4*>(p.c.v_scales + kv * p.c.vs_head);
+        const int32_t* table = p.c.table + item * p.c.table_stride;
         const int k_first = unit * kUnit;
         src.end = min(k_first + units * kUnit, most);
         constexpr int kStep = T::kTurn * kWarps;
 
         // The pages of a turn's two halves (-1: nothing to read).
         auto pages = [&](int j, int (&pg)[2]) {
-            pg[0] = j < src.end ? page_of(p.c, src.table, j) : -1;
-            pg[1] = T::kTurn == 32 && j + 16 < src.end ? page_of(p.c, src.table, j + 16) : -1;
+            pg[0] = j < src.end ? page_of(p.c, table, j) : -1;
+            pg[1] = T::kTurn == 32 && j + 16 < src.end ? page_of(p.c, table, j + 16) : -1;
         };
+
+        // One turn's keys, which are in shared memory.  EDGE: some are hidden
+        // from some row, or hold nothing.
+        auto compute = [&](auto edge, uint32_t here, int j) {
+            constexpr bool EDGE = decltype(edge)::value;
+            const int left = src.end - j;
+            float sc[KB][NB][4];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) sc[kb][b][0] = sc[kb][b][1] = sc[kb][b][2] = sc[kb][b][3] = 0.0f;
+                format.template keys<EDGE>(here, kb, g, left, [&](int step, const uint32_t (&a)[4]) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) mma16<!HALF>(sc[kb][b], a, q[b][2 * step], q[b][2 * step + 1]);
+                });
+            }
+            float top[NB][2];  // in powers of two
+            bool grows = false;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float t = -INFINITY;
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = j + 16 * kb + 8 * e + g;
+                            float& v = sc[kb][b][2 * e + h];
+                            if constexpr (BENT) {
+                                const float raw = v;
+                                v = raw * in[b][h];
+                                if (p.cap > 0.0f) {
+                                    const float cap = p.cap * h3qk_core::kLog2e;
+                                    const float bent = fmaf(-2.0f * cap, rcp_fast(exp2_fast(v) + 1.0f), cap);
+                                    if (fabsf(v) < h3qk_core::kSmall) {
+                                        float flat, other;
+                                        const uint64_t z = pair(v, v);
+                                        unpair(flat, other, mul_pair(pair(raw * plain[b][h], 0.0f),
+                                                                     h3qk_core::tanh_series(mul_pair(z, z))));
+                                        v = flat;
+                                    } else {
+                                        v = bent;
+                                    }
+                                }
+                                if (p.slopes) v = fmaf(-slope[b][h], fabsf(static_cast<float>(at[b][h] - key)), v);
+                            }
+                            if (EDGE) v = key < lim[b][h] ? v : -INFINITY;
+                            t = fmaxf(t, v);
+                        }
+                    top[b][h] = BENT ? t : t * in[b][h];
+                    grows = grows || top[b][h] > m[b][h] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float t = top[b][h];
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                        t = fmaxf(t, m[b][h]);
+                        const float f = t == -INFINITY ? 1.0f : exp2_fast(m[b][h] - t);
+                        m[b][h] = t;
+                        l[b][h] *= f;
+#pragma unroll
+                        for (int k = 0; k < kOut; ++k) {
+                            o[k][b][h] *= f;
+                            o[k][b][2 + h] *= f;
+                        }
+                    }
+            }
+            uint32_t pt[KB][NB][2];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float off[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) off[h] = kShift - (m[b][h] == -INFINITY ? 0.0f : m[b][h]);
+                auto power = [&](float v, int h) { return exp2_fast(BENT ? v + off[h] : fmaf(v, in[b][h], off[h])); };
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float p0 = power(sc[kb][b][2 * e], 0), p1 = power(sc[kb][b][2 * e + 1], 1);
+                        l[b][0] += p0;
+                        l[b][1] += p1;
+                        pt[kb][b][e] = transpose8(round_pair<!HALF>(p0, p1));
+                    }
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                format.template values<EDGE>(here, kb, c, left, [&](int k, const uint32_t (&a)[4]) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) mma16<!HALF>(o[k][b], a, pt[kb][b][0], pt[kb][b][1]);
+                });
+        };
+
+        const int plain_end = min(src.end, least);
         int j = k_first + T::kTurn * warp;
         if (j < src.end) {
             int pg[2];
 #pragma unroll
             for (int i = 0; i < T::kStages - 1; ++i) {
                 pages(j + i * kStep, pg);
-                if (j + i * kStep < src.end) T::fetch(p.c, src, ring + i * T::kStage, j + i * kStep, pg, lane);
+                if (j + i * kStep < src.end) format.fetch(p.c, src, ring + i * T::kStage, j + i * kStep, pg, lane);
                 asm volatile("cp.async.commit_group;" ::: "memory");
             }
             pages(j + (T::kStages - 1) * kStep, pg);
@@ -523,96 +662,16 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
             for (; j < src.end; j += kStep) {
                 const int next = j + (T::kStages - 1) * kStep;
                 __syncwarp();  // the stage that is filled now has been read by all lanes
-                if (next < src.end) T::fetch(p.c, src, ring + (stage == 0 ? T::kStages - 1 : stage - 1) * T::kStage, next, pg, lane);
+                if (next < src.end)
+                    format.fetch(p.c, src, ring + (stage == 0 ? T::kStages - 1 : stage - 1) * T::kStage, next, pg, lane);
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 pages(next + kStep, pg);
                 asm volatile("cp.async.wait_group %0;" ::"n"(T::kStages - 1) : "memory");
                 __syncwarp();
                 const uint32_t here = ring + stage * T::kStage;
                 stage = stage + 1 == T::kStages ? 0 : stage + 1;
-                const int left = src.end - j;
-
-                float sc[KB][NB][4];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) sc[kb][b][0] = sc[kb][b][1] = sc[kb][b][2] = sc[kb][b][3] = 0.0f;
-                    T::keys(p.c, here, kb, g, c, left, [&](int step, const uint32_t (&a)[4]) {
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) mma16<!kHalf>(sc[kb][b], a, q[b][2 * step], q[b][2 * step + 1]);
-                    });
-                }
-                float top[NB][2];
-                bool grows = false;
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float t = -INFINITY;
-#pragma unroll
-                        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int key = j + 16 * kb + 8 * e + g;
-                                const float raw = sc[kb][b][2 * e + h];
-                                float v = raw * in[b][h];
-                                if (capped) {
-                                    float flat, other;
-                                    const uint64_t z = pair(v, v);
-                                    unpair(flat, other, mul_pair(pair(raw * plain[b][h], 0.0f), h3qk_core::tanh_series(mul_pair(z, z))));
-                                    const float bent = fmaf(-2.0f * cap2, rcp_fast(exp2_fast(v) + 1.0f), cap2);
-                                    v = fabsf(v) < h3qk_core::kSmall ? flat : bent;
-                                }
-                                if (p.slopes) v = fmaf(-slope[b][h], fabsf(static_cast<float>(at[b][h] - key)), v);
-                                v = key < lim[b][h] ? v : -INFINITY;
-                                sc[kb][b][2 * e + h] = v;
-                                t = fmaxf(t, v);
-                            }
-                        top[b][h] = t;
-                        grows = grows || t > m[b][h] + kSlack;
-                    }
-                if (__any_sync(0xffffffffu, grows)) {
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float t = top[b][h];
-                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                            t = fmaxf(t, m[b][h]);
-                            const float f = t == -INFINITY ? 1.0f : exp2_fast(m[b][h] - t);
-                            m[b][h] = t;
-                            l[b][h] *= f;
-#pragma unroll
-                            for (int k = 0; k < kOut; ++k) {
-                                o[k][b][h] *= f;
-                                o[k][b][2 + h] *= f;
-                            }
-                        }
-                }
-                uint32_t pt[KB][NB][2];
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float off[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) off[h] = (m[b][h] == -INFINITY ? 0.0f : m[b][h]) - kShift;
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float p0 = exp2_fast(sc[kb][b][2 * e] - off[0]), p1 = exp2_fast(sc[kb][b][2 * e + 1] - off[1]);
-                            l[b][0] += p0;
-                            l[b][1] += p1;
-                            pt[kb][b][e] = transpose8(round_pair<!kHalf>(p0, p1));
-                        }
-                }
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-                    T::values(p.c, here, kb, g, c, left, [&](int k, const uint32_t (&a)[4]) {
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) mma16<!kHalf>(o[k][b], a, pt[kb][b][0], pt[kb][b][1]);
-                    });
+                if (j + T::kTurn <= plain_end) compute(std::false_type{}, here, j);
+                else compute(std::true_type{}, here, j);
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -660,7 +719,7 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 v.w = fmaf(x.w, f, v.w);
             }
             if (whole) {
-                finish_row<BF16>(p, s, kv, r, d, v, top, sum, kShift, T::kE2m1 ? p.c.v_scale : 1.0f);
+                finish_row(p, s, kv, r, d, v, top, sum, kShift, T::kE2m1 ? p.c.v_scale : 1.0f);
             } else {
                 *reinterpret_cast<float4*>(to + row * p.c.dim + d) = v;
                 if (d == 0) *reinterpret_cast<float2*>(to + ROWS * p.c.dim + 2 * row) = make_float2(top, sum);
@@ -673,7 +732,7 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
 // One block a packed row of a run that was cut: its warps take the blocks'
 // parts in turn, in order, and are joined in order.
 constexpr int kJoinWarps = 4;
-template <bool BF16, int ROWS>
+template <int ROWS>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_few_kernel(const __grid_constant__ Attn p, int blocks,
                                                                    unsigned rows, float shift, float v_scale)
 {
@@ -748,14 +807,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_few_kernel(const __grid_
         v.w += x.w;
         sum += sh_sum[w];
     }
-    finish_row<BF16>(p, part.s, kv, r, d, v, top, sum, shift, v_scale);
+    finish_row(p, part.s, kv, r, d, v, top, sum, shift, v_scale);
 }
 
-template <class T, bool BF16, int NB>
+template <class T, bool HALF, bool BENT, int NB>
 cudaError_t launch(const Attn& p, int blocks, cudaStream_t st)
 {
     constexpr int smem = T::kWarps * T::kStages * T::kStage;
-    auto* kernel = few_kernel<T, BF16, NB>;
+    auto* kernel = few_kernel<T, HALF, BENT, NB>;
     static bool raised[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
@@ -768,19 +827,25 @@ cudaError_t launch(const Attn& p, int blocks, cudaStream_t st)
     h3qk_internal_count_launch();
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || blocks == 1) return e;
-    const int64_t rows = p.few < static_cast<int64_t>(p.max_rows) * p.group ? p.few : static_cast<int64_t>(p.max_rows) * p.group;
+    const int64_t all = static_cast<int64_t>(p.max_rows) * p.group, rows = p.few < all ? p.few : all;
     const dim3 grid(static_cast<unsigned>(rows * p.c.kv_heads * p.c.batch));
-    const float shift = T::kE2m1 || !BF16 ? kRaise : 0.0f;
-    return h3qk_ops::launch_chained(join_few_kernel<BF16, 8 * NB>, grid, dim3(32 * kJoinWarps), 0, st, p, blocks,
-                                    static_cast<unsigned>(rows), shift, T::kE2m1 ? p.c.v_scale : 1.0f);
+    return h3qk_ops::launch_chained(join_few_kernel<8 * NB>, grid, dim3(32 * kJoinWarps), 0, st, p, blocks,
+                                    static_cast<unsigned>(rows), HALF ? kRaise : 0.0f, T::kE2m1 ? p.c.v_scale : 1.0f);
 }
 
-template <template <int, int> class T, bool BF16>
-cudaError_t by_shape(int row_tile, int blocks, const Attn& p, cudaStream_t st)
+template <template <int, int> class T, int DIM, bool HALF>
+cudaError_t by_rows(int row_tile, int blocks, const Attn& p, cudaStream_t st)
 {
-    if (p.c.dim <= 64)
-        return row_tile == 8 ? launch<T<64, 1>, BF16, 1>(p, blocks, st) : launch<T<64, 2>, BF16, 2>(p, blocks, st);
-    return row_tile == 8 ? launch<T<128, 1>, BF16, 1>(p, blocks, st) : launch<T<128, 2>, BF16, 2>(p, blocks, st);
+    const bool bent = p.cap > 0.0f || p.slopes;
+    if (row_tile == 8)
+        return bent ? launch<T<DIM, 1>, HALF, true, 1>(p, blocks, st) : launch<T<DIM, 1>, HALF, false, 1>(p, blocks, st);
+    return bent ? launch<T<DIM, 2>, HALF, true, 2>(p, blocks, st) : launch<T<DIM, 2>, HALF, false, 2>(p, blocks, st);
+}
+
+template <bool HALF>
+cudaError_t halves(int row_tile, int blocks, const Attn& p, cudaStream_t st)
+{
+    return p.c.dim <= 64 ? by_rows<Halves, 64, HALF>(row_tile, blocks, p, st) : by_rows<Halves, 128, HALF>(row_tile, blocks, p, st);
 }
 
 }  // namespace
@@ -792,8 +857,13 @@ int h3qk_pages::few_blocks(bool e2m1, int row_tile)
     return an_sm * h3qk_internal_sm_count();
 }
 
-cudaError_t h3qk_pages::cache_few(bool bf16, bool e2m1, int row_tile, int blocks, const Attn& p, cudaStream_t st)
+cudaError_t h3qk_pages::cache_few(bool e2m1, int row_tile, int blocks, const Attn& p, cudaStream_t st)
 {
-    if (e2m1) return bf16 ? by_shape<Codes, true>(row_tile, blocks, p, st) : by_shape<Codes, false>(row_tile, blocks, p, st);
-    return bf16 ? by_shape<Halves, true>(row_tile, blocks, p, st) : by_shape<Halves, false>(row_tile, blocks, p, st);
+    if (!e2m1) return p.bf16 ? halves<false>(row_tile, blocks, p, st) : halves<true>(row_tile, blocks, p, st);
+    switch (p.c.dim) {
+    case 32: return by_rows<Codes, 32, true>(row_tile, blocks, p, st);
+    case 64: return by_rows<Codes, 64, true>(row_tile, blocks, p, st);
+    case 96: return by_rows<Codes, 96, true>(row_tile, blocks, p, st);
+    default: return by_rows<Codes, 128, true>(row_tile, blocks, p, st);
+    }
 }

@@ -642,7 +642,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // One warp a packed row: its parts' O, weighted to their common maximum, in order.
-template <bool BF16>
 __global__ void __launch_bounds__(256) join_tiles_kernel(const __grid_constant__ Attn p, float shift, float v_scale)
 {
     const int lane = threadIdx.x & 31, d = 4 * lane;
@@ -678,7 +677,7 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const __grid_constant__
             v.w = fmaf(x.w, fi, v.w);
         }
     }
-    finish_row<BF16>(p, at.s, at.kv, row, d, v, top, sum, shift, v_scale);
+    finish_row(p, at.s, at.kv, row, d, v, top, sum, shift, v_scale);
 }
 
 template <bool E2M1, bool BF16, int DP, int BENDS>
@@ -693,7 +692,7 @@ cudaError_t launch(const Attn& p, const Maps& m, const TileGrid& grid, cudaStrea
     h3qk_internal_count_launch();
     const cudaError_t launched = cudaGetLastError();
     if (launched != cudaSuccess || grid.join == 0) return launched;
-    return h3qk_ops::launch_chained(join_tiles_kernel<BF16>, dim3(static_cast<unsigned>(grid.join) * (2 * kTile / 8)), dim3(256),
+    return h3qk_ops::launch_chained(join_tiles_kernel, dim3(static_cast<unsigned>(grid.join) * (2 * kTile / 8)), dim3(256),
                                     0, st, p, E2M1 || !BF16 ? 7.0f : 0.0f, E2M1 ? p.c.v_scale : 1.0f);
 }
 
