@@ -12,10 +12,12 @@
 //    each thread copies its own row into the swizzled tile.
 //  - 16-bit pages: one warp loads tiles of 128 keys by TMA, a box for each
 //    page (or for 128 rows of a larger one), each lane its own page.
-//  - 4-bit pages: three warps read codes and scales one tile ahead into
-//    registers, convert them and store binary16 tiles, swizzled as TMA would:
-//    a warp-wide load is 512 contiguous bytes, and eight lanes that store
-//    together are eight rows of one 16-byte column, which meet no bank twice.
+//  - 4-bit pages: three warps copy codes and scales two tiles ahead into
+//    shared memory, convert them and store binary16 tiles, swizzled as TMA
+//    would: a warp-wide copy is 512 contiguous bytes, each lane converts the 16
+//    bytes that it copied, and eight lanes that store together are eight rows
+//    of one 16-byte column, which meet no bank twice.  (Ahead in registers,
+//    the loads were spilled and waited for one by one.)
 //    The products are binary16's whatever the type of q; bfloat16 rows are
 //    scaled by a power of two first, as in the kernel for few rows.
 //
@@ -39,14 +41,17 @@ constexpr int kThreads = 384;           // 2 x 4 softmax warps; products; three 
 constexpr float kSlack = 8.0f;          // log2: growth of the maximum that is tolerated
 constexpr int kBlockBytes = 128 * 128;  // 64 columns of a tile
 
-template <int DP>
+template <bool E2M1, int DP>
 struct Shape {
     static constexpr int kBlocks = DP / 64;
     static constexpr int kTileBytes = kBlocks * kBlockBytes;
-    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kStages = DP == 128 ? (E2M1 ? 4 : 5) : 8;
     static constexpr int kScores = DP == 128 ? 2 : 3;  // S buffers
     static constexpr uint32_t kOut = 128 * kScores;    // first column of O
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+    // 4 bits: tiles of codes and of scales on their way
+    static constexpr int kAhead = 3, kCodes = kTile * DP / 2, kScaleBytes = kTile * DP / 16;
+    static constexpr int kCodeStage = kCodes + kScaleBytes;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + (E2M1 ? kAhead * kCodeStage : 0);
 };
 
 struct Shared {
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cache_tiles_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const __grid_constant__ Attn p)
 {
-    using S = Shape<DP>;
+    using S = Shape<E2M1, DP>;
     constexpr int kStages = S::kStages;
     constexpr bool kHalf = E2M1 || !BF16;
     constexpr float kShift = kHalf ? 7.0f : 0.0f;
@@ -212,77 +217,99 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- 4-bit keys: three warps share a tile's rows ----------------------
         if constexpr (E2M1) {
             constexpr int kPieces = DP / 32;              // 16-byte pieces of codes a row
-            constexpr int kRowsEach = 32 / kPieces;       // rows of a warp-wide load
-            constexpr int kTurns = kTile / kRowsEach;     // loads a tile: 16 or 8
+            constexpr int kRowsEach = 32 / kPieces;       // rows of a warp-wide copy
+            constexpr int kTurns = kTile / kRowsEach;     // copies a tile: 16 or 8
             constexpr int kMine = (kTurns + 2) / 3;
             const int w = warp - 9, piece = lane / kRowsEach, sub = lane % kRowsEach;
-            const bool in = 32 * piece < p.c.dim;
-            const uint8_t* codes[2] = {p.c.k + at.kv * p.c.k_head + 16 * piece, p.c.v + at.kv * p.c.v_head + 16 * piece};
-            const uint8_t* scales[2] = {p.c.k_scales + at.kv * p.c.ks_head + 2 * piece,
-                                        p.c.v_scales + at.kv * p.c.vs_head + 2 * piece};
-            uint4 next[kMine];
-            uint32_t next_scale[kMine];
-            // Lane l holds the page of rows 16 (l mod 8) of a tile of keys.
-            auto page_for = [&](int j) {
-                const int key = key0 + j * kTile + 16 * (lane & 7);
-                return key < seen ? page_of(p.c, table, key) : -1;
+            const int dim = p.c.dim, row_bytes = dim / 2, groups = dim / 16;
+            const bool in = 32 * piece < dim;
+            const uint32_t staged = ring + kStages * S::kTileBytes;
+            // This lane's 16 bytes of each turn's codes; and of its scales, a few lanes'.
+            const int64_t code_at = sub * row_bytes + 16 * piece;
+            const bool has_scales = 16 * lane < kRowsEach * groups;
+            const uint8_t* codes[2] = {p.c.k + at.kv * p.c.k_head + code_at, p.c.v + at.kv * p.c.v_head + code_at};
+            const uint8_t* scales[2] = {p.c.k_scales + at.kv * p.c.ks_head + 16 * lane,
+                                        p.c.v_scales + at.kv * p.c.vs_head + 16 * lane};
+            auto copy16 = [](uint32_t dst, const uint8_t* src, bool there) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+                             : "memory");
             };
-            int pages = n_all > 0 ? page_for(0) : -1, pages_after = n_all > 1 ? page_for(1) : -1;
-            // Load u of tile i (K and V in turn) that falls to this warp.
-            auto row_of = [&](int i, int u) { return ((w + i) % 3 + 3 * u) * kRowsEach + sub; };
-            auto fetch = [&](int i, int u) {
-                const int row = row_of(i, u), key = key0 + (i >> 1) * kTile + row;
-                const int page = __shfl_sync(0xffffffffu, pages, (row >> 4) & 7);
-                next[u] = make_uint4(0, 0, 0, 0);
-                next_scale[u] = 0;
-                if (row < kTile && in && page >= 0 && key < seen) {
-                    const int64_t in_page = key & page_mask;
+            // Copies of tile i (K and V in turn) that fall to this warp.  Lane l
+            // holds the page of rows 16 (l mod 8) of the tile's keys.
+            int pages = -1;
+            auto fetch = [&](int i) {
+                if (i < 2 * n_all) {
                     const bool v = i & 1;
-                    next[u] = __ldg(reinterpret_cast<const uint4*>((v ? codes[1] : codes[0]) +
-                                                                   page * (v ? p.c.v_page : p.c.k_page) + in_page * (p.c.dim / 2)));
-                    next_scale[u] = __ldg(reinterpret_cast<const uint16_t*>((v ? scales[1] : scales[0]) +
-                                                                            page * (v ? p.c.vs_page : p.c.ks_page) +
-                                                                            in_page * (p.c.dim / 16)));
-                }
-            };
-            if (n_all > 0) {
+                    const int key_tile = key0 + (i >> 1) * kTile;
+                    if (!v) {
+                        const int key = key_tile + 16 * (lane & 7);
+                        pages = key < seen ? page_of(p.c, table, key) : -1;
+                    }
+                    const uint32_t to = staged + i % S::kAhead * S::kCodeStage;
+                    const uint8_t* from = v ? codes[1] : codes[0];
+                    const uint8_t* scale_from = v ? scales[1] : scales[0];
+                    const int64_t stride = v ? p.c.v_page : p.c.k_page, scale_stride = v ? p.c.vs_page : p.c.ks_page;
 #pragma unroll
-                for (int u = 0; u < kMine; ++u) fetch(0, u);
-            }
+                    for (int u = 0; u < kMine; ++u) {
+                        const int t = (w + i) % 3 + 3 * u;
+                        const int page = __shfl_sync(0xffffffffu, pages, t * kRowsEach / 16 & 7);
+                        if (t >= kTurns) continue;
+                        const int in_page = (key_tile + t * kRowsEach) & page_mask;
+                        const bool there = page >= 0;
+                        const int64_t pg = there ? page : 0;
+                        copy16(to + (t * 32 + lane) * 16, in ? from + pg * stride + in_page * row_bytes : p.c.k, there && in);
+                        if (has_scales)
+                            copy16(to + S::kCodes + t * kRowsEach * groups + 16 * lane,
+                                   scale_from + pg * scale_stride + in_page * groups, there);
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            for (int i = 0; i < S::kAhead - 1; ++i) fetch(i);
+            const uint32_t store_at = (piece >> 1) * kBlockBytes + sub * 128 + ((((piece & 1) * 4) ^ (sub & 7)) << 4);
             for (int i = 0; i < 2 * n_all; ++i) {
                 const int st = i % kStages;
+                __syncwarp();  // the codes that are overwritten now have been read
+                fetch(i + S::kAhead - 1);
+                asm volatile("cp.async.wait_group %0;" ::"n"(S::kAhead - 1) : "memory");
+                __syncwarp();
                 if (!wait(empty + 8 * st, ((i / kStages) & 1) ^ 1)) break;
-                if (i & 1) {  // the next tile has other keys
-                    pages = pages_after;
-                    pages_after = (i >> 1) + 2 < n_all ? page_for((i >> 1) + 2) : -1;
-                }
-                const uint32_t tile = ring + st * S::kTileBytes + (piece >> 1) * kBlockBytes;
+                const uint32_t tile = ring + st * S::kTileBytes + store_at, from = staged + i % S::kAhead * S::kCodeStage;
+                const int left = seen - (key0 + (i >> 1) * kTile) - sub;  // rows behind it hold nothing
 #pragma unroll
                 for (int u = 0; u < kMine; ++u) {
-                    const uint4 c = next[u];
-                    const uint32_t g = widen_scales(next_scale[u]);
-                    const int row = row_of(i, u);
-                    if (i + 1 < 2 * n_all) fetch(i + 1, u);
-                    if (row < kTile) {
-                        const uint32_t lo = __byte_perm(g, g, 0x1010), hi = __byte_perm(g, g, 0x3232);
-                        const uint32_t line = tile + row * 128;
+                    const int t = (w + i) % 3 + 3 * u;
+                    if (t >= kTurns) continue;
+                    uint32_t c[4], two = 0;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+                                 : "r"(from + (t * 32 + lane) * 16)
+                                 : "memory");
+                    if (in && t * kRowsEach < left) {
+                        uint16_t b;
+                        asm volatile("ld.shared.u16 %0, [%1];"
+                                     : "=h"(b)
+                                     : "r"(from + S::kCodes + (t * kRowsEach + sub) * groups + 2 * piece)
+                                     : "memory");
+                        two = b;
+                    }
+                    const uint32_t g = widen_scales(two), lo = __byte_perm(g, g, 0x1010), hi = __byte_perm(g, g, 0x3232);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t v[4];
-                            widen_codes(e == 0 ? c.x : e == 1 ? c.y : e == 2 ? c.z : c.w, v);
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t v[4];
+                        widen_codes(c[e], v);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = mul_half2(v[k], e < 2 ? lo : hi);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             line + ((((piece & 1) * 4 + e) ^ (row & 7)) << 4)),
-                                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                                         : "memory");
-                        }
+                        for (int k = 0; k < 4; ++k) v[k] = mul_half2(v[k], e < 2 ? lo : hi);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((tile ^ (e << 4)) + t * kRowsEach * 128),
+                                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                     : "memory");
                     }
                 }
                 fence_async();
                 __syncwarp();
                 if (lane == 0) bar_arrive(full + 8 * st);
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncwarp();
         }
     } else if (warp > 9) {
@@ -683,7 +710,7 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const __grid_constant__
 template <bool E2M1, bool BF16, int DP, int BENDS>
 cudaError_t launch(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st)
 {
-    constexpr int smem = Shape<DP>::kSmem;
+    constexpr int smem = Shape<E2M1, DP>::kSmem;
     auto* kernel = cache_tiles_kernel<E2M1, BF16, DP, BENDS>;
     static bool done[64] = {false};
     const cudaError_t e = h3qk_core::ready(kernel, smem, done);
