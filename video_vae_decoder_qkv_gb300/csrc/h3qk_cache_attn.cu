@@ -13,19 +13,22 @@ using h3qk_detail::overlap;
 using h3qk_detail::Range;
 using h3qk_detail::range_of;
 
-constexpr int kLeastUnits = 4;
+// What a block takes at least: for few rows units of 64 keys, two turns of its
+// warps; for many, tiles of 128 keys, to be worth its start and the join.
+constexpr int kLeastUnits = 4, kLeastTiles = 4;
 
-// Sequences of up to kFew packed rows go to the kernel for few rows, which
-// reads (and converts) their keys once for each 16 of them; longer ones to the
-// tiles of 256.
-constexpr int64_t kFew = 32;
+// Calls whose sequences have at most kFew packed rows go to the kernel for few
+// rows, which reads (and converts) their keys once for 8 or 16 of them; others
+// to the tiles of 256.  A call that mixes long chunks with single tokens stays
+// in one kernel: the tiles take the tokens' keys at nearly the same rate.
+constexpr int kFew = 16;
 
 // How a call is cut, from its sizes alone.
 struct Cut {
-    bool few, tiles;       // which kernels run: both where only the device knows the sequences' rows
+    bool tiles;            // the kernel for many rows
     int row_tile, blocks;  // few rows
     TileGrid grid;         // many rows
-    int64_t few_floats, tile_floats;  // of partial results
+    int64_t floats;        // of partial results
 };
 Cut cut_of(const h3qk_cache& c, const h3qk_cache_attn& a, int64_t max_rows)
 {
@@ -33,29 +36,25 @@ Cut cut_of(const h3qk_cache& c, const h3qk_cache_attn& a, int64_t max_rows)
     const int64_t group = a.heads / c.kv_heads, packed = max_rows * group;
     const int sms = h3qk_internal_sm_count();
     t.tiles = packed > kFew;
-    t.few = !t.tiles || a.q_offsets;
-    if (t.few) {
-        const int64_t rows = packed < kFew ? packed : kFew;
-        t.row_tile = rows <= 8 ? 8 : 16;
-        const int64_t tiles = (rows + t.row_tile - 1) / t.row_tile;
+    if (!t.tiles) {
+        t.row_tile = packed <= 8 ? 8 : 16;
+        const int64_t tiles = (packed + t.row_tile - 1) / t.row_tile;
         const int64_t per = (static_cast<int64_t>(c.max_pages) * c.page_size + kUnit - 1) / kUnit;
         const double units = static_cast<double>(c.batch) * c.kv_heads * tiles * (per > 0 ? per : 1);
         const int most = few_blocks(c.format == H3QK_E2M1, t.row_tile);
         const double want = std::ceil(units / kLeastUnits);
         t.blocks = want < most ? static_cast<int>(want) : most;
-        t.few_floats = (few_floats(t.blocks, t.row_tile, c.head_dim) + 3) / 4 * 4;
+        t.floats = few_floats(t.blocks, t.row_tile, c.head_dim);
     }
     if (t.tiles) {
         // Tiles of 256 at most: of all rows in full ones, and a partial one a sequence; or of sequences as long as may be.
-        const int64_t by_rows = a.tokens * group / h3qk_core::kRowTile + c.batch;
-        const int64_t by_batch = (packed + h3qk_core::kRowTile - 1) / h3qk_core::kRowTile * c.batch;
-        t.grid.blocks = (by_rows < by_batch ? by_rows : by_batch) * c.kv_heads;
-        if (a.q_offsets || 2 * t.grid.blocks <= sms) {
-            // (the device may find few enough to share out)
-            t.grid.join = t.grid.blocks < sms / 2 ? t.grid.blocks : sms / 2;
-            if (t.grid.blocks < sms) t.grid.blocks = sms;
-            t.tile_floats = sms * tile_floats(c.head_dim);
-        }
+        const double by_rows = std::floor(static_cast<double>(a.tokens) * group / h3qk_core::kRowTile) + c.batch;
+        const double by_batch = std::ceil(static_cast<double>(packed) / h3qk_core::kRowTile) * c.batch;
+        const double keys = std::ceil(static_cast<double>(c.max_pages) * c.page_size / 128);
+        const double units = (by_rows < by_batch ? by_rows : by_batch) * c.kv_heads * (keys > 1 ? keys : 1);
+        const double want = std::ceil(units / kLeastTiles);
+        t.grid.blocks = want < sms ? static_cast<int>(want) : sms;
+        t.floats = t.grid.blocks == 1 ? 0 : t.grid.blocks * (2 * tile_floats(c.head_dim) + kBrokenFloats);
     }
     return t;
 }
@@ -74,8 +73,8 @@ h3qk_status check_call(const h3qk_cache& c, const h3qk_cache_attn& a, int64_t* r
     if (!a.q_offsets && a.tokens % c.batch) return H3QK_ERR_INVALID_ARG;
     *rows = a.q_offsets ? a.tokens : a.tokens / c.batch;
     if (a.max_rows > 0 && a.max_rows < *rows) *rows = a.max_rows;
-    // the join's grid
-    if (static_cast<double>(*rows) * a.heads * c.batch > 2e9) return H3QK_ERR_INVALID_ARG;
+    // packed rows, and the join's grid, fit 31 bits
+    if (a.tokens * a.heads > INT32_MAX || static_cast<double>(a.heads) * c.batch * kFew > INT32_MAX) return H3QK_ERR_INVALID_ARG;
     return H3QK_OK;
 }
 
@@ -102,7 +101,7 @@ extern "C" size_t h3qk_cache_attention_workspace_bytes(const h3qk_cache* cache, 
     int64_t rows;
     if (!cache || !call || check_call(*cache, *call, &rows) != H3QK_OK || rows == 0) return 0;
     const Cut cut = cut_of(*cache, *call, rows);
-    return static_cast<size_t>(cut.few_floats + cut.tile_floats) * 4;
+    return static_cast<size_t>(cut.floats) * 4;
 }
 
 extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_cache_attn* call, h3qk_stream_t stream)
@@ -131,8 +130,7 @@ extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_
     if (!aligned(a.lse, 4) || !aligned(a.slopes, 4) || !aligned(a.prefix_lens, 4) || !aligned(a.q_offsets, 4))
         return H3QK_ERR_MISALIGNED;
     const Cut cut = cut_of(c, a, rows);
-    if (cut.grid.blocks > INT32_MAX) return H3QK_ERR_INVALID_ARG;
-    const size_t need = static_cast<size_t>(cut.few_floats + cut.tile_floats) * 4;
+    const size_t need = static_cast<size_t>(cut.floats) * 4;
     if (need && (!a.workspace || a.workspace_bytes < need)) return H3QK_ERR_INVALID_ARG;
     if (need && !aligned(a.workspace, 16)) return H3QK_ERR_MISALIGNED;
     const Range outs[3] = {out, range_of(a.lse, a.heads * a.tokens * 4), range_of(a.workspace, need)};
@@ -163,18 +161,15 @@ extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_
     p.q_token = a.q_token_stride, p.q_head = a.q_head_stride;
     p.out_token = a.out_token_stride, p.out_head = a.out_head_stride;
     p.lse = a.lse;
-    p.few = kFew;
-    p.least = kLeastUnits;
-    p.sms = h3qk_internal_sm_count();
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = p.bf16 != 0, e2m1 = c.format == H3QK_E2M1;
-    cudaError_t e = cudaSuccess;
-    if (cut.few) {
-        p.part = static_cast<float*>(a.workspace);
+    p.part = static_cast<float*>(a.workspace);
+    cudaError_t e;
+    if (!cut.tiles) {
+        p.least = kLeastUnits;
         e = cache_few(e2m1, cut.row_tile, cut.blocks, p, st);
-    }
-    if (e == cudaSuccess && cut.tiles) {
-        p.part = static_cast<float*>(a.workspace) + cut.few_floats;
+    } else {
+        p.least = kLeastTiles;
         p.stuck = h3qk_core::stuck_addr();
         Maps m = {};
         bool ok = p.stuck != nullptr;

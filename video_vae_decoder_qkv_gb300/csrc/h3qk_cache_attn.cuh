@@ -24,11 +24,12 @@ struct Attn {
     int64_t q_token, q_head, out_token, out_head;  // elements
     float* lse;                  // [heads][tokens]
     float* part;                 // partial results of the kernel that is launched
-    int64_t few;                 // sequences of at most so many packed rows go to the kernel for few rows
-    int32_t least;               // few rows: units that a block takes at least
-    int32_t sms;                 // many rows: the SMs, to share out few tiles' keys among
+    int32_t least;               // units that a block takes at least
     unsigned int* stuck;
 };
+
+// Packed rows fit 31 bits; their division is the unsigned one, which is short.
+__device__ __forceinline__ int divide(int a, int b) { return static_cast<int>(static_cast<unsigned>(a) / static_cast<unsigned>(b)); }
 
 // One sequence as the attention kernels see it.
 struct Sequence {
@@ -76,12 +77,12 @@ __device__ __forceinline__ float raise_of(uint32_t top, int& e)
 }
 
 // Writes 4 channels of one joined packed row (d = 0: its lse too).
-__device__ __forceinline__ void finish_row(const Attn& p, const Sequence& s, int kv, int64_t r, int d, float4 v, float top,
+__device__ __forceinline__ void finish_row(const Attn& p, const Sequence& s, int kv, int r, int d, float4 v, float top,
                                            float sum, float shift, float v_scale)
 {
     using h3qk_tc::round_pair;
-    const int head = kv * p.group + static_cast<int>(r % p.group);
-    const int64_t token = s.first + r / p.group;
+    const int i = divide(r, p.group), head = kv * p.group + r - i * p.group;
+    const int64_t token = s.first + i;
     const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
     if (d < p.c.dim) {
         uint2 w;
@@ -99,10 +100,12 @@ struct Maps {
     CUtensorMap k, v;  // 16-bit pages
 };
 struct TileGrid {
-    int64_t blocks, join;  // blocks of tiles or their parts; tiles that may have been shared (0: none)
+    int blocks;
 };
-// Floats that a block leaves which shares a tile: per packed row O[dim], then m and sum.
+// Floats of a partial tile (per packed row O[dim], then m and sum), of which a
+// block leaves two at most; and of the words that tell the join of them.
 inline int64_t tile_floats(int dim) { return h3qk_core::tile_part_floats(dim); }
+constexpr int kBrokenFloats = 5;
 constexpr int kUnit = 64;  // keys of a unit of work of the kernel for few rows
 H3QK_HIDDEN int few_blocks(bool e2m1, int row_tile);
 H3QK_HIDDEN int64_t few_floats(int blocks, int rows, int dim);

@@ -368,7 +368,7 @@ struct Halves {
 // A sequence's part of the line: `runs` (K/V heads x row tiles) of `per` units.
 struct Part {
     Sequence s;
-    int64_t packed;  // packed rows, 0: not in this kernel's line
+    int packed;  // packed rows
     int tiles, per;
     __device__ int64_t units(const Attn& p) const { return packed ? static_cast<int64_t>(p.c.kv_heads) * tiles * per : 0; }
 };
@@ -377,9 +377,8 @@ __device__ __forceinline__ Part part_of(const Attn& p, int item)
 {
     Part t;
     t.s = sequence_of(p, item);
-    t.packed = static_cast<int64_t>(t.s.n) * p.group;
-    if (t.packed > p.few) t.packed = 0;
-    t.tiles = static_cast<int>((t.packed + ROWS - 1) / ROWS);
+    t.packed = t.s.n * p.group;
+    t.tiles = (t.packed + ROWS - 1) / ROWS;
     t.per = max((t.s.keys + kUnit - 1) / kUnit, 1);  // a row without keys is a unit of its own
     return t;
 }
@@ -474,9 +473,9 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
         uint32_t q[NB][2 * kSteps];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const int64_t r = static_cast<int64_t>(row_tile) * ROWS + 8 * b + g;
+            const int r = row_tile * ROWS + 8 * b + g;
             const bool has = r < part.packed;
-            const int i = has ? static_cast<int>(r / p.group) : 0, head = kv * p.group + (has ? static_cast<int>(r % p.group) : 0);
+            const int i = has ? divide(r, p.group) : 0, head = kv * p.group + (has ? r - i * p.group : 0);
             const uint16_t* from = p.q + (s.first + i) * p.q_token + head * p.q_head;
 #pragma unroll
             for (int e = 0; e < kSteps / 2; ++e) {
@@ -700,7 +699,7 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
         const int per = p.c.dim / 4;
         for (int i = threadIdx.x; i < ROWS * per; i += 32 * kWarps) {
             const int row = i / per, d = 4 * (i - row * per);
-            const int64_t r = static_cast<int64_t>(row_tile) * ROWS + row;
+            const int r = row_tile * ROWS + row;
             if (r >= part.packed) break;
             float top = -INFINITY;
 #pragma unroll
@@ -739,7 +738,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_few_kernel(const __grid_
     __shared__ float4 sh_v[kJoinWarps][32];
     __shared__ float sh_sum[kJoinWarps], sh_top[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = 4 * lane;
-    const int64_t r = blockIdx.x % rows;  // packed row of the sequence
+    const int r = static_cast<int>(blockIdx.x % rows);  // packed row of the sequence
     const int kv = static_cast<int>(blockIdx.x / rows % p.c.kv_heads), item = static_cast<int>(blockIdx.x / rows / p.c.kv_heads);
     const Part part = part_of<ROWS>(p, item);
     h3qk_ops::wait_for_previous();
@@ -760,7 +759,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_few_kernel(const __grid_
     const int64_t u0 = before + (static_cast<int64_t>(kv) * part.tiles + r / ROWS) * part.per, u1 = u0 + part.per;
     const int first = static_cast<int>(u0 / share), last = static_cast<int>((u1 - 1) / share);
     if (first == last) return;  // finished in place
-    const int row = static_cast<int>(r % ROWS), n = last - first + 1;
+    const int row = r % ROWS, n = last - first + 1;
     const int64_t size = part_floats(ROWS, p.c.dim);
     // the first block's part is the one that it broke off, the others' the one that they began in
     auto slot = [&](int i) { return p.part + (2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0)) * size; };
@@ -827,8 +826,8 @@ cudaError_t launch(const Attn& p, int blocks, cudaStream_t st)
     h3qk_internal_count_launch();
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || blocks == 1) return e;
-    const int64_t all = static_cast<int64_t>(p.max_rows) * p.group, rows = p.few < all ? p.few : all;
-    const dim3 grid(static_cast<unsigned>(rows * p.c.kv_heads * p.c.batch));
+    const int rows = p.max_rows * p.group;
+    const dim3 grid(static_cast<unsigned>(rows) * p.c.kv_heads * p.c.batch);
     return h3qk_ops::launch_chained(join_few_kernel<8 * NB>, grid, dim3(32 * kJoinWarps), 0, st, p, blocks,
                                     static_cast<unsigned>(rows), HALF ? kRaise : 0.0f, T::kE2m1 ? p.c.v_scale : 1.0f);
 }
