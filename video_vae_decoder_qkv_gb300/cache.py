@@ -10,6 +10,7 @@ autograd graph.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import struct
 
@@ -139,6 +140,18 @@ def _offsets(q_offsets, batch, tokens, dev):
     return _need_lens(q_offsets, "q_offsets", batch + 1, dev)
 
 
+@functools.lru_cache(maxsize=256)
+def _opts(dtype, row_stride, n_axes, axis_dims, theta, eps):
+    """h3qk_opts of an append (the library reads it only; filling one takes longer than the call)."""
+    o = h3qk.default_opts()
+    o.in_dtype = _DTYPES[dtype]
+    o.n_axes = n_axes
+    if axis_dims is not None:
+        o.axis_dims = (ctypes.c_int32 * 3)(*axis_dims, *[0] * (3 - len(axis_dims)))
+    o.eps, o.theta, o.batch, o.qkv_row_stride = eps, theta, 1, row_stride
+    return ctypes.byref(o)
+
+
 @_on_stream
 def cache_append(qkv, norm_wq, norm_wk, cache, block_table, kv_lens, *, heads: int, rotary_dim: int, positions=None,
                  q_offsets=None, n_axes: int | None = None, axis_dims=None, theta: float = 10000.0, eps: float = 1e-6,
@@ -184,11 +197,9 @@ def cache_append(qkv, norm_wq, norm_wk, cache, block_table, kv_lens, *, heads: i
         out = torch.empty((tokens, heads, dim), dtype=qkv.dtype, device=dev)
     else:
         _need(out, "out", device=dev, dtypes=(qkv.dtype,), numel=tokens * heads * dim)
-    o = h3qk._opts_for(qkv, n_axes=n_axes, axis_dims=axis_dims, theta=theta, eps=eps, batch=1)
-    if tokens < 2:
-        o.qkv_row_stride = 0
+    o = _opts(qkv.dtype, qkv.stride(0) if tokens > 1 else 0, n_axes, None if axis_dims is None else tuple(axis_dims), theta, eps)
     block._call("h3qk_cache_append", dev, pool, qkv.data_ptr(), norm_wq.data_ptr(), norm_wk.data_ptr(), _ptr(positions),
-                tokens, heads, rotary_dim, offsets, out.data_ptr(), ctypes.byref(o), _stream(dev))
+                tokens, heads, rotary_dim, offsets, out.data_ptr(), o, _stream(dev))
     return out
 
 

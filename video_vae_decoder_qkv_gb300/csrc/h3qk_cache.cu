@@ -19,19 +19,21 @@ using h3qk_detail::range_of;
 // Q to packed rows and K, V to their places in the pages.
 //
 // Bound by HBM: each packed row is read once, and Q and the cache's bytes are
-// written.  The layout is the preparation's: a lane owns 8 channels, the LPR
-// lanes of a head row are a power of two, a warp holds 32 / LPR consecutive
-// packed rows, finds their sequences by a search in the offsets, and their
-// angles, once, and walks a slice of the heads; the next kAhead head rows are
-// on their way while kAhead are computed.
+// written.  The layout is the preparation's: a lane owns CH chunks of 8
+// channels, the LPR lanes of a head row are a power of two, a warp holds
+// 32 / LPR consecutive packed rows, finds their sequences by a search in the
+// offsets, and their angles, once, and walks a slice of the heads, kAhead head
+// rows of copies ahead of itself (in shared memory: loads ahead in
+// registers were waited for together).  13,000 rows of 40 + 2 x 8 heads of 128
+// in 16 bits: 68 us, 5.7 TB/s; 107 with the rows ahead in registers.
 //
 // 4 bits: a group of 16 channels is two neighbouring lanes.  The largest
 // magnitude of its 16-bit values is an integer maximum of their bits (exact,
 // and any infinity or NaN wins it), one exchange joins the lanes, and a lane's
 // 8 codes are one 4-byte store.
 // ---------------------------------------------------------------------------
-constexpr int kWarps = 8;
-constexpr int kAhead = 4;
+constexpr int kWarps = 8, kBlocks = 3;  // of a block; of an SM
+constexpr int kAhead = 3;
 
 struct AppendArgs {
     h3qk::Params p;  // the preparation's description of the rows; heads: Q, K and V together
@@ -75,17 +77,21 @@ __device__ __forceinline__ uint32_t encode_group(const uint32_t (&y)[4], float t
     return finite ? codes : 0u;
 }
 
-template <bool BF16, int LPR, bool E2M1>
-__global__ void __launch_bounds__(32 * kWarps, 2) append_kernel(const __grid_constant__ AppendArgs a)
+template <bool BF16, int LPR, int CH, bool E2M1>
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const __grid_constant__ AppendArgs a)
 {
     const h3qk::Params& p = a.p;
     const Pool& c = a.c;
     constexpr int TPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int chunk = lane % LPR, sub = lane / LPR;
-    const bool in = chunk < p.chunks;
+    const int chunk = lane % LPR, sub = lane / LPR;  // this lane's chunks: chunk + q LPR
     const int D = p.head_dim;
     const int kv_heads = c.kv_heads, q_heads = a.q_heads;
+    __shared__ uint4 slots[kWarps][kAhead][CH][32];
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(&slots[warp][0][0][lane]));
+    bool in[CH];
+#pragma unroll
+    for (int q = 0; q < CH; ++q) in[q] = chunk + q * LPR < p.chunks;
     const int64_t items = a.groups * a.slices;
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * kWarps + warp; it < items;
          it += static_cast<int64_t>(gridDim.x) * kWarps) {
@@ -113,16 +119,22 @@ __global__ void __launch_bounds__(32 * kWarps, 2) append_kernel(const __grid_con
             start = rows.first;
             n = rows.n;
         }
-        const bool row = in && item >= 0 && r >= start && r < start + n;
-        uint4 next[kAhead];
+        const bool row = item >= 0 && r >= start && r < start + n;
+        // (a lane reads back what it copied itself: there is nothing to synchronise)
         auto fetch = [&](int h) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                next[u] = make_uint4(0, 0, 0, 0);
-                if (row && h + u < h1) next[u] = __ldcs(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(h + u) * D));
+            for (int q = 0; q < CH; ++q) {
+                const bool there = row && in[q] && h < h1;
+                const uint16_t* from = there ? x + static_cast<int64_t>(h) * D + 8 * q * LPR : p.qkv;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 ring + ((h - h0) % kAhead * CH + q) * 512),
+                             "l"(from), "r"(there ? 16 : 0)
+                             : "memory");
             }
+            h3qk::cp_async_commit();
         };
-        fetch(h0);
+#pragma unroll
+        for (int u = 0; u < kAhead - 1; ++u) fetch(h0 + u);
         int at = 0, page = -1;
         if (row) {
             // (a length of any size: the difference is taken in 64 bits)
@@ -131,66 +143,94 @@ __global__ void __launch_bounds__(32 * kWarps, 2) append_kernel(const __grid_con
             if (at >= 0) page = page_of(c, c.table + item * c.table_stride, at);
         }
         const int in_page = at & ((1 << c.page_shift) - 1);
-        float cs[1][4], sn[1][4];
-        bool rot[1][4];
+        float cs[CH][4], sn[CH][4];
+        bool rot[CH][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            cs[0][i] = 1.0f;
-            sn[0][i] = 0.0f;
-            const int pair = 4 * chunk + i;
-            rot[0][i] = row && 2 * pair < p.rotary_dim;
-            if (rot[0][i]) {
-                const float pos = static_cast<float>(p.pos ? __ldg(p.pos + r * p.n_axes + p.axis[pair]) : at);
-                h3qk::sincos_h3(__fmul_rn(pos, p.inv_freq[pair]), sn[0][i], cs[0][i]);
+        for (int q = 0; q < CH; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cs[q][i] = 1.0f;
+                sn[q][i] = 0.0f;
+                const int pair = 4 * (chunk + q * LPR) + i;
+                rot[q][i] = row && 2 * pair < p.rotary_dim;
+                if (rot[q][i] && h0 < q_heads + kv_heads) {
+                    const float pos = static_cast<float>(p.pos ? __ldg(p.pos + r * p.n_axes + p.axis[pair]) : at);
+                    h3qk::sincos_h3(__fmul_rn(pos, p.inv_freq[pair]), sn[q][i], cs[q][i]);
+                }
             }
+        // Where this lane's first chunk of K and V head rows goes.
+        constexpr int kChunkBytes = E2M1 ? 4 : 16;
+        uint8_t* k_to = c.k + (page * c.k_page + in_page * c.k_row + chunk * kChunkBytes);
+        uint8_t* v_to = c.v + (page * c.v_page + in_page * c.v_row + chunk * kChunkBytes);
+        uint8_t *ks_to = nullptr, *vs_to = nullptr;
+        if constexpr (E2M1) {
+            ks_to = c.k_scales + (page * c.ks_page + static_cast<int64_t>(in_page) * (D / 16) + chunk / 2);
+            vs_to = c.v_scales + (page * c.vs_page + static_cast<int64_t>(in_page) * (D / 16) + chunk / 2);
         }
-        // Where this lane's channels of K and V head rows go.
-        const int64_t k_at = page * c.k_page + in_page * c.k_row + chunk * (E2M1 ? 4 : 16);
-        const int64_t v_at = page * c.v_page + in_page * c.v_row + chunk * (E2M1 ? 4 : 16);
-        const int64_t ks_at = E2M1 ? page * c.ks_page + static_cast<int64_t>(in_page) * (D / 16) + chunk / 2 : 0;
-        const int64_t vs_at = E2M1 ? page * c.vs_page + static_cast<int64_t>(in_page) * (D / 16) + chunk / 2 : 0;
         uint16_t* out = a.out_q + r * q_heads * D + 8 * chunk;
         const bool placed = row && page >= 0;
+        float4 w[2 * CH];
         for (int h = h0; h < h1; h += kAhead) {
-            uint4 raw[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) raw[u] = next[u];
-            if (h + kAhead < h1) fetch(h + kAhead);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int head = h + u;
                 if (head >= h1) break;
-                uint32_t y[1][4] = {{raw[u].x, raw[u].y, raw[u].z, raw[u].w}};
+                fetch(head + kAhead - 1);
+                h3qk::cp_async_wait<kAhead - 1>();
+                uint4 raw[CH];
+#pragma unroll
+                for (int q = 0; q < CH; ++q)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(raw[q].x), "=r"(raw[q].y), "=r"(raw[q].z), "=r"(raw[q].w)
+                                 : "r"(ring + (u * CH + q) * 512)
+                                 : "memory");
                 const bool is_v = head >= q_heads + kv_heads;
+                uint32_t y[CH][4];
                 if (!is_v) {
-                    float4 w[2];
-                    const float* from = (head < q_heads ? p.wq : p.wk) + 8 * chunk;
-                    w[0] = in ? __ldg(reinterpret_cast<const float4*>(from)) : make_float4(0, 0, 0, 0);
-                    w[1] = in ? __ldg(reinterpret_cast<const float4*>(from) + 1) : make_float4(0, 0, 0, 0);
-                    const uint4 one[1] = {raw[u]};
-                    h3qk::qk_row<BF16, LPR, 1>(one, w, cs, sn, rot, p.inv_d, p.eps, D, y);
+                    if (head == h0 || head == q_heads) {
+                        const float* from = (head < q_heads ? p.wq : p.wk) + 8 * chunk;
+#pragma unroll
+                        for (int q = 0; q < CH; ++q)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                w[2 * q + i] = in[q] ? __ldg(reinterpret_cast<const float4*>(from + 8 * q * LPR) + i)
+                                                     : make_float4(0, 0, 0, 0);
+                    }
+                    h3qk::qk_row<BF16, LPR, CH>(raw, w, cs, sn, rot, p.inv_d, p.eps, D, y);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < CH; ++q) y[q][0] = raw[q].x, y[q][1] = raw[q].y, y[q][2] = raw[q].z, y[q][3] = raw[q].w;
                 }
                 if (head < q_heads) {
-                    if (row) __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(head) * D),
-                                    make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]));
+#pragma unroll
+                    for (int q = 0; q < CH; ++q)
+                        if (row && in[q])
+                            __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(head) * D + 8 * q * LPR),
+                                   make_uint4(y[q][0], y[q][1], y[q][2], y[q][3]));
                     continue;
                 }
                 const int kv = is_v ? head - q_heads - kv_heads : head - q_heads;
-                uint8_t* to = is_v ? c.v + v_at + kv * c.v_head : c.k + k_at + kv * c.k_head;
-                if constexpr (E2M1) {
-                    uint32_t scale;
-                    const uint32_t codes =
-                        encode_group<BF16>(y[0], a.to_scale[is_v ? 1 : 0], is_v ? c.v_scale : c.k_scale, scale);
-                    if (placed) {
-                        *reinterpret_cast<uint32_t*>(to) = codes;
-                        if ((chunk & 1) == 0) *(is_v ? c.v_scales + vs_at + kv * c.vs_head : c.k_scales + ks_at + kv * c.ks_head) =
-                                                  static_cast<uint8_t>(scale);
+                uint8_t* to = is_v ? v_to + kv * c.v_head : k_to + kv * c.k_head;
+                [[maybe_unused]] uint8_t* scale_to = nullptr;
+                if constexpr (E2M1) scale_to = is_v ? vs_to + kv * c.vs_head : ks_to + kv * c.ks_head;
+#pragma unroll
+                for (int q = 0; q < CH; ++q) {
+                    if constexpr (E2M1) {
+                        uint32_t scale;
+                        const uint32_t codes =
+                            encode_group<BF16>(y[q], a.to_scale[is_v ? 1 : 0], is_v ? c.v_scale : c.k_scale, scale);
+                        if (placed && in[q]) {
+                            *reinterpret_cast<uint32_t*>(to + q * LPR * kChunkBytes) = codes;
+                            if ((chunk & 1) == 0) scale_to[q * LPR / 2] = static_cast<uint8_t>(scale);
+                        }
+                    } else {
+                        if (placed && in[q])
+                            *reinterpret_cast<uint4*>(to + q * LPR * kChunkBytes) = make_uint4(y[q][0], y[q][1], y[q][2], y[q][3]);
                     }
-                } else {
-                    if (placed) *reinterpret_cast<uint4*>(to) = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
                 }
             }
         }
+        h3qk::cp_async_wait<0>();
     }
 }
 
@@ -263,23 +303,24 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
     }
 }
 
+// P: chunks of a head row, to a power of two; two of them a lane.
 template <bool BF16>
 cudaError_t launch_append(int P, bool e2m1, const AppendArgs& a, int blocks, cudaStream_t st)
 {
     constexpr int kThreads = 32 * kWarps;
     if (e2m1) {
         switch (P) {
-        case 4: append_kernel<BF16, 4, true><<<blocks, kThreads, 0, st>>>(a); break;
-        case 8: append_kernel<BF16, 8, true><<<blocks, kThreads, 0, st>>>(a); break;
-        default: append_kernel<BF16, 16, true><<<blocks, kThreads, 0, st>>>(a); break;
+        case 4: append_kernel<BF16, 2, 2, true><<<blocks, kThreads, 0, st>>>(a); break;
+        case 8: append_kernel<BF16, 4, 2, true><<<blocks, kThreads, 0, st>>>(a); break;
+        default: append_kernel<BF16, 8, 2, true><<<blocks, kThreads, 0, st>>>(a); break;
         }
     } else {
         switch (P) {
-        case 1: append_kernel<BF16, 1, false><<<blocks, kThreads, 0, st>>>(a); break;
-        case 2: append_kernel<BF16, 2, false><<<blocks, kThreads, 0, st>>>(a); break;
-        case 4: append_kernel<BF16, 4, false><<<blocks, kThreads, 0, st>>>(a); break;
-        case 8: append_kernel<BF16, 8, false><<<blocks, kThreads, 0, st>>>(a); break;
-        default: append_kernel<BF16, 16, false><<<blocks, kThreads, 0, st>>>(a); break;
+        case 1: append_kernel<BF16, 1, 1, false><<<blocks, kThreads, 0, st>>>(a); break;
+        case 2: append_kernel<BF16, 1, 2, false><<<blocks, kThreads, 0, st>>>(a); break;
+        case 4: append_kernel<BF16, 2, 2, false><<<blocks, kThreads, 0, st>>>(a); break;
+        case 8: append_kernel<BF16, 4, 2, false><<<blocks, kThreads, 0, st>>>(a); break;
+        default: append_kernel<BF16, 8, 2, false><<<blocks, kThreads, 0, st>>>(a); break;
         }
     }
     h3qk_internal_count_launch();
@@ -475,12 +516,12 @@ extern "C" h3qk_status h3qk_cache_append(const h3qk_cache* cache, const void* qk
     a.out_q = static_cast<uint16_t*>(out_q);
     a.to_scale[0] = static_cast<float>(1.0 / (6.0 * a.c.k_scale));
     a.to_scale[1] = static_cast<float>(1.0 / (6.0 * a.c.v_scale));
-    const int tpw = 32 / pl.P;
+    const int tpw = pl.P == 1 ? 32 : 64 / pl.P;
     a.groups = (tokens + tpw - 1) / tpw;
     // Heads are cut into slices so that a warp's turns, at the cost of a
     // slice's heads and about eight heads' worth of search and angles each,
     // are fewest: one token's heads spread over the GPU, many rows' do not.
-    const int cap = 2 * h3qk_internal_sm_count();
+    const int cap = kBlocks * h3qk_internal_sm_count();
     const int64_t warps = static_cast<int64_t>(cap) * kWarps;
     int64_t least = INT64_MAX;
     for (int32_t slices = 1; slices <= (all + kAhead - 1) / kAhead; ++slices) {

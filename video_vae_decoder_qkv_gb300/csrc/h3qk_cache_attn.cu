@@ -21,7 +21,7 @@ constexpr int kLeastUnits = 4, kLeastTiles = 4;
 // rows, which reads (and converts) their keys once for 8 or 16 of them; others
 // to the tiles of 256.  A call that mixes long chunks with single tokens stays
 // in one kernel: the tiles take the tokens' keys at nearly the same rate.
-constexpr int kFew = 16;
+constexpr int kFew = 32;
 
 // How a call is cut, from its sizes alone.
 struct Cut {

@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kHalf = E2M1 || !BF16;
     constexpr float kShift = kHalf ? 7.0f : 0.0f;
     constexpr int kLoaders = E2M1 ? 3 : 1;
-    // (8 x 208 + 4 x 88 = 12 x 168: the converting warps need more than loading ones)
-    constexpr int kMathRegs = E2M1 ? 208 : h3qk_core::kMathRegs, kOtherRegs = E2M1 ? 88 : h3qk_core::kOtherRegs;
+    // (8 x 200 + 4 x 104 = 12 x 168: the converting warps need more than loading ones)
+    constexpr int kMathRegs = E2M1 ? 200 : h3qk_core::kMathRegs, kOtherRegs = E2M1 ? 104 : h3qk_core::kOtherRegs;
     static_assert(8 * kMathRegs + 4 * kOtherRegs == 12 * h3qk_core::kLaunchRegs, "the shares are what the launch gave");
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared sh;
@@ -419,28 +419,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const uint32_t tile = ring + st * S::kTileBytes + store_at, from = staged + ri % S::kAhead * S::kCodeStage;
                     const int left = pc.seen - (pc.key0 + (i >> 1) * kTile) - sub;  // rows behind it hold nothing
+                    // (all reads first: one by one, each turn would wait for its own)
+                    uint32_t c[kMine][4], two[kMine];
 #pragma unroll
                     for (int u = 0; u < kMine; ++u) {
                         const int t = (w + ri) % 3 + 3 * u;
                         if (t >= kTurns) continue;
-                        uint32_t c[4], two = 0;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+                                     : "=r"(c[u][0]), "=r"(c[u][1]), "=r"(c[u][2]), "=r"(c[u][3])
                                      : "r"(from + (t * 32 + lane) * 16)
                                      : "memory");
-                        if (in && t * kRowsEach < left) {
-                            uint16_t b;
-                            asm volatile("ld.shared.u16 %0, [%1];"
-                                         : "=h"(b)
-                                         : "r"(from + S::kCodes + (t * kRowsEach + sub) * groups + 2 * piece)
-                                         : "memory");
-                            two = b;
-                        }
-                        const uint32_t g = widen_scales(two), lo = __byte_perm(g, g, 0x1010), hi = __byte_perm(g, g, 0x3232);
+                        uint16_t b;
+                        asm volatile("ld.shared.u16 %0, [%1];"
+                                     : "=h"(b)
+                                     : "r"(from + S::kCodes + (t * kRowsEach + sub) * groups + 2 * piece)
+                                     : "memory");
+                        two[u] = in && t * kRowsEach < left ? b : 0;
+                    }
+#pragma unroll
+                    for (int u = 0; u < kMine; ++u) {
+                        const int t = (w + ri) % 3 + 3 * u;
+                        if (t >= kTurns) continue;
+                        const uint32_t g = widen_scales(two[u]), lo = __byte_perm(g, g, 0x1010), hi = __byte_perm(g, g, 0x3232);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t v[4];
-                            widen_codes(c[e], v);
+                            widen_codes(c[u][e], v);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) v[k] = mul_half2(v[k], e < 2 ? lo : hi);
                             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((tile ^ (e << 4)) + t * kRowsEach * 128),
