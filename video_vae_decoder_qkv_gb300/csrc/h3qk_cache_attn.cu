@@ -41,7 +41,7 @@ Cut cut_of(const h3qk_cache& c, const h3qk_cache_attn& a, int64_t max_rows)
         const int64_t tiles = (packed + t.row_tile - 1) / t.row_tile;
         const int64_t per = (static_cast<int64_t>(c.max_pages) * c.page_size + kUnit - 1) / kUnit;
         const double units = static_cast<double>(c.batch) * c.kv_heads * tiles * (per > 0 ? per : 1);
-        const int most = few_blocks(c.format == H3QK_E2M1, t.row_tile);
+        const int most = few_blocks(c.format == H3QK_E2M1);
         const double want = std::ceil(units / kLeastUnits);
         t.blocks = want < most ? static_cast<int>(want) : most;
         t.floats = few_floats(t.blocks, t.row_tile, c.head_dim);

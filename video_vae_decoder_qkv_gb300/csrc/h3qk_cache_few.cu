@@ -127,7 +127,7 @@ template <int DIM, int NB>
 struct Codes {
     static constexpr bool kE2m1 = true;
     static constexpr int kDim = DIM, DP = DIM <= 64 ? 64 : 128;
-    static constexpr int kTurn = 32, kWarps = NB == 1 ? 8 : 4, kStages = 3, kBlocks = NB == 1 ? 2 : 3;
+    static constexpr int kTurn = 32, kWarps = 3, kStages = 3, kBlocks = 4;
     static constexpr int kPitch = DP / 2;
     static constexpr int kGroups = DIM / 16;            // scale bytes a row
     static constexpr int kScales = 2 * kTurn * kPitch;  // where the scales begin; V's follow K's
@@ -438,9 +438,12 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
     static_assert(T::kWarps * T::kStages * T::kStage >= kWarps * ROWS * (DP + 4) * 4, "the warps' O fits the rings");
     extern __shared__ __align__(128) uint8_t dynamic[];
     __shared__ float sh_m[kWarps][ROWS], sh_l[kWarps][ROWS];
+    __shared__ uint2 sh_q[NB == 1 ? 1 : NB][NB == 1 ? 1 : kSteps][32];  // Q of several blocks, as the products take it
+    static_assert(NB <= kWarps, "a warp a block of rows of Q");
     h3qk_ops::allow_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = lane & 3, g = lane >> 2;
+    [[maybe_unused]] const uint32_t q_at = smem_addr(&sh_q[0][0][NB == 1 ? 0 : lane]);
     const uint32_t ring = smem_addr(dynamic) + warp * T::kStages * T::kStage;
     float(*sh_o)[ROWS][DP + 4] = reinterpret_cast<float(*)[ROWS][DP + 4]>(dynamic);
     const T format(p.c, lane);
@@ -467,12 +470,13 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
         // This lane's packed row of each block of 8 for Q, and the two whose scores it holds.
         float o[kOut][NB][4], m[NB][2], l[NB][2];
         float in[NB][2];
-        [[maybe_unused]] float plain[NB][2], slope[NB][2];
+        [[maybe_unused]] float slope[NB][2];
         [[maybe_unused]] int at[NB][2];
         int lim[NB][2], most = 0, least = 1 << 30;  // rows that are none see everything: nobody reads them
-        uint32_t q[NB][2 * kSteps];
+        [[maybe_unused]] uint32_t q1[2 * kSteps];  // Q of one block stays in registers
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
+            uint32_t q[2 * kSteps];
             const int r = row_tile * ROWS + 8 * b + g;
             const bool has = r < part.packed;
             const int i = has ? divide(r, p.group) : 0, head = kv * p.group + (has ? r - i * p.group : 0);
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 const int channel = T::k_channel(c, e);
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (has && channel < p.c.dim) v = __ldg(reinterpret_cast<const uint4*>(from + channel));
-                q[b][4 * e] = v.x, q[b][4 * e + 1] = v.y, q[b][4 * e + 2] = v.z, q[b][4 * e + 3] = v.w;
+                q[4 * e] = v.x, q[4 * e + 1] = v.y, q[4 * e + 2] = v.z, q[4 * e + 3] = v.w;
             }
             float raw = 1.0f;
             if constexpr (T::kE2m1) {
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 if (p.bf16) {
                     uint32_t top = 0;
 #pragma unroll
-                    for (int e = 0; e < 2 * kSteps; ++e) top = __vmaxu2(top, q[b][e] & 0x7fff7fffu);
+                    for (int e = 0; e < 2 * kSteps; ++e) top = __vmaxu2(top, q[e] & 0x7fff7fffu);
                     top = max(top & 0xffffu, top >> 16);
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -499,10 +503,17 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                     raw *= __int_as_float((127 + e - 141) << 23);
 #pragma unroll
                     for (int k = 0; k < 2 * kSteps; ++k) {
-                        const float2 f = widen_pair<true>(q[b][k]);
-                        q[b][k] = round_pair<false>(f.x * up, f.y * up);
+                        const float2 f = widen_pair<true>(q[k]);
+                        q[k] = round_pair<false>(f.x * up, f.y * up);
                     }
                 }
+            }
+            if constexpr (NB == 1) {
+#pragma unroll
+                for (int k = 0; k < 2 * kSteps; ++k) q1[k] = q[k];
+            } else if (warp == b) {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) sh_q[b][k][lane] = make_uint2(q[2 * k], q[2 * k + 1]);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -512,7 +523,6 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 const bool has_of = __shfl_sync(0xffffffffu, static_cast<int>(has), src) != 0;
                 const Bend bend = h3qk_pages::bend_of(p, head_of, raw_of);
                 in[b][h] = bend.in;
-                plain[b][h] = bend.plain;
                 slope[b][h] = bend.slope;
                 at[b][h] = s.start + i_of;
                 lim[b][h] = 1 << 30;
@@ -543,10 +553,17 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
         src.end = min(k_first + units * kUnit, most);
         constexpr int kStep = T::kTurn * kWarps;
 
-        // The pages of a turn's two halves (-1: nothing to read).
-        auto pages = [&](int j, int (&pg)[2]) {
-            pg[0] = j < src.end ? page_of(p.c, table, j) : -1;
-            pg[1] = T::kTurn == 32 && j + 16 < src.end ? page_of(p.c, table, j + 16) : -1;
+        // The pages of the warp's next turns, one a lane (-1: nothing to read): of
+        // 16 turns' two halves, or of 32 turns of 16 keys.
+        constexpr int kHalves = T::kTurn / 16, kHeld = 32 / kHalves;
+        int pages = -1;
+        auto hold = [&](int j) {
+            const int key = j + lane / kHalves * kStep + 16 * (lane % kHalves);
+            pages = key < src.end ? page_of(p.c, table, key) : -1;
+        };
+        auto pages_of = [&](int turn, int (&pg)[2]) {
+            pg[0] = __shfl_sync(0xffffffffu, pages, turn % kHeld * kHalves);
+            pg[1] = kHalves == 2 ? __shfl_sync(0xffffffffu, pages, turn % kHeld * kHalves + 1) : -1;
         };
 
         // One turn's keys, which are in shared memory.  EDGE: some are hidden
@@ -561,8 +578,58 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 for (int b = 0; b < NB; ++b) sc[kb][b][0] = sc[kb][b][1] = sc[kb][b][2] = sc[kb][b][3] = 0.0f;
                 format.template keys<EDGE>(here, kb, g, left, [&](int step, const uint32_t (&a)[4]) {
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) mma16<!HALF>(sc[kb][b], a, q[b][2 * step], q[b][2 * step + 1]);
+                    for (int b = 0; b < NB; ++b) {
+                        if constexpr (NB == 1) {
+                            mma16<!HALF>(sc[kb][b], a, q1[2 * step], q1[2 * step + 1]);
+                        } else {
+                            const uint2 w = lds64(q_at + (b * kSteps + step) * 256);
+                            mma16<!HALF>(sc[kb][b], a, w.x, w.y);
+                        }
+                    }
                 });
+            }
+            // BENT: the scores' exponents.  The cap works on four scores at once, which
+            // come multiplied with `in`, so that one bend serves all rows.
+            if constexpr (BENT) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float* v[4 * KB / 2][4];  // fours: of one row over two blocks of keys, or of both rows
+#pragma unroll
+                    for (int f = 0; f < KB; ++f)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[f][i] = KB == 2 ? &sc[i / 2][b][2 * (i & 1) + f] : &sc[0][b][2 * (i & 1) + i / 2];
+#pragma unroll
+                    for (int f = 0; f < KB; ++f) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int h = KB == 2 ? f : i / 2, key = j + (KB == 2 ? 16 * (i / 2) : 0) + 8 * (i & 1) + g;
+                            // (hidden scores may be NaN, and four share a reciprocal)
+                            if (EDGE && key >= lim[b][h]) *v[f][i] = 0.0f;
+                            *v[f][i] *= in[b][h];
+                        }
+                        if (p.cap > 0.0f) {
+                            Bend bend;
+                            bend.in = 1.0f;
+                            bend.plain = 0.5f * p.cap;
+                            bend.cap = p.cap * h3qk_core::kLog2e;
+                            bend.slope = 0.0f;
+                            uint64_t z[2] = {pair(*v[f][0], *v[f][1]), pair(*v[f][2], *v[f][3])}, keep[2];
+                            if (p.cap > h3qk_core::kWideCap)
+                                h3qk_core::bend_four<h3qk_core::kCapped | h3qk_core::kWide, false>(z, bend, 0.0f, 0.0f, keep);
+                            else
+                                h3qk_core::bend_four<h3qk_core::kCapped, false>(z, bend, 0.0f, 0.0f, keep);
+                            unpair(*v[f][0], *v[f][1], z[0]);
+                            unpair(*v[f][2], *v[f][3], z[1]);
+                        }
+                        if (p.slopes)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int h = KB == 2 ? f : i / 2, key = j + (KB == 2 ? 16 * (i / 2) : 0) + 8 * (i & 1) + g;
+                                *v[f][i] = fmaf(-slope[b][h], fabsf(static_cast<float>(at[b][h] - key)), *v[f][i]);
+                            }
+                    }
+                }
             }
             float top[NB][2];  // in powers of two
             bool grows = false;
@@ -575,27 +642,8 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int key = j + 16 * kb + 8 * e + g;
                             float& v = sc[kb][b][2 * e + h];
-                            if constexpr (BENT) {
-                                const float raw = v;
-                                v = raw * in[b][h];
-                                if (p.cap > 0.0f) {
-                                    const float cap = p.cap * h3qk_core::kLog2e;
-                                    const float bent = fmaf(-2.0f * cap, rcp_fast(exp2_fast(v) + 1.0f), cap);
-                                    if (fabsf(v) < h3qk_core::kSmall) {
-                                        float flat, other;
-                                        const uint64_t z = pair(v, v);
-                                        unpair(flat, other, mul_pair(pair(raw * plain[b][h], 0.0f),
-                                                                     h3qk_core::tanh_series(mul_pair(z, z))));
-                                        v = flat;
-                                    } else {
-                                        v = bent;
-                                    }
-                                }
-                                if (p.slopes) v = fmaf(-slope[b][h], fabsf(static_cast<float>(at[b][h] - key)), v);
-                            }
-                            if (EDGE) v = key < lim[b][h] ? v : -INFINITY;
+                            if (EDGE) v = j + 16 * kb + 8 * e + g < lim[b][h] ? v : -INFINITY;
                             t = fmaxf(t, v);
                         }
                     top[b][h] = BENT ? t : t * in[b][h];
@@ -646,25 +694,27 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 });
         };
 
+        if constexpr (NB > 1) __syncthreads();
         const int plain_end = min(src.end, least);
         int j = k_first + T::kTurn * warp;
         if (j < src.end) {
-            int pg[2];
+            int pg[2], ahead = 0;  // turns fetched
+            hold(j);
 #pragma unroll
-            for (int i = 0; i < T::kStages - 1; ++i) {
-                pages(j + i * kStep, pg);
-                if (j + i * kStep < src.end) format.fetch(p.c, src, ring + i * T::kStage, j + i * kStep, pg, lane);
+            for (; ahead < T::kStages - 1; ++ahead) {
+                pages_of(ahead, pg);
+                if (j + ahead * kStep < src.end) format.fetch(p.c, src, ring + ahead * T::kStage, j + ahead * kStep, pg, lane);
                 asm volatile("cp.async.commit_group;" ::: "memory");
             }
-            pages(j + (T::kStages - 1) * kStep, pg);
             int stage = 0;
-            for (; j < src.end; j += kStep) {
+            for (; j < src.end; j += kStep, ++ahead) {
                 const int next = j + (T::kStages - 1) * kStep;
+                if (ahead % kHeld == 0) hold(next);
+                pages_of(ahead, pg);
                 __syncwarp();  // the stage that is filled now has been read by all lanes
                 if (next < src.end)
                     format.fetch(p.c, src, ring + (stage == 0 ? T::kStages - 1 : stage - 1) * T::kStage, next, pg, lane);
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                pages(next + kStep, pg);
                 asm volatile("cp.async.wait_group %0;" ::"n"(T::kStages - 1) : "memory");
                 __syncwarp();
                 const uint32_t here = ring + stage * T::kStage;
@@ -850,9 +900,9 @@ cudaError_t halves(int row_tile, int blocks, const Attn& p, cudaStream_t st)
 }  // namespace
 
 int64_t h3qk_pages::few_floats(int blocks, int rows, int dim) { return blocks == 1 ? 0 : 2 * blocks * part_floats(rows, dim); }
-int h3qk_pages::few_blocks(bool e2m1, int row_tile)
+int h3qk_pages::few_blocks(bool e2m1)
 {
-    const int an_sm = e2m1 ? (row_tile == 8 ? Codes<128, 1>::kBlocks : Codes<128, 2>::kBlocks) : Halves<128, 1>::kBlocks;
+    const int an_sm = e2m1 ? Codes<128, 1>::kBlocks : Halves<128, 1>::kBlocks;
     return an_sm * h3qk_internal_sm_count();
 }
 
