@@ -114,10 +114,19 @@ class Cache:
         return cls(*codes, *(s.view(torch.float8_e4m3fn) for s in scales), k_scale=k_scale, v_scale=v_scale)
 
 
+def _list(t, name, n, dev):
+    """The address of an int32 list of n (0 for none)."""
+    if t is None:
+        return 0
+    if t.dtype is torch.int32 and t.shape == (n,) and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _need_lens(t, name, n, dev)  # says what is wrong
+
+
 def _pool(cache, block_table, kv_lens):
     """h3qk_cache as bytes, after checking the table and the lengths: (packed, batch)."""
     dev = cache.device
-    if block_table.dtype != torch.int32:
+    if block_table.dtype is not torch.int32:
         raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
     if block_table.dim() != 2 or block_table.device != dev:
         raise ValueError(f"block_table must be [batch, max_pages] on {dev}")
@@ -127,17 +136,16 @@ def _pool(cache, block_table, kv_lens):
         raise ValueError("block_table must have unit stride along a sequence's pages, and no overlapping rows")
     if batch < 1 or max_pages * cache.page_size >= 1 << 30:
         raise ValueError("block_table must hold at least one sequence, and fewer than 2^30 rows of each")
-    lens = _need_lens(kv_lens, "kv_lens", batch, dev)
-    if not lens:
+    if kv_lens is None:
         raise ValueError("kv_lens is required")
-    return cache._packed + _TABLE.pack(batch, max_pages, block_table.data_ptr(), max(across, max_pages) if batch > 1 else 0,
-                                       lens), batch
+    return cache._packed + _TABLE.pack(batch, max_pages, block_table.data_ptr(), across if batch > 1 else 0,
+                                       _list(kv_lens, "kv_lens", batch, dev)), batch
 
 
 def _offsets(q_offsets, batch, tokens, dev):
     if q_offsets is None and tokens % batch:
         raise ValueError(f"{tokens} rows cannot be shared evenly by {batch} sequences: q_offsets is required")
-    return _need_lens(q_offsets, "q_offsets", batch + 1, dev)
+    return _list(q_offsets, "q_offsets", batch + 1, dev)
 
 
 @functools.lru_cache(maxsize=256)
@@ -204,7 +212,7 @@ def cache_append(qkv, norm_wq, norm_wk, cache, block_table, kv_lens, *, heads: i
 
 
 def _head_rows(t, name, shape, dtype, dev):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -253,12 +261,14 @@ def cache_attention(q, cache, block_table, kv_lens, *, q_offsets=None, max_rows:
     tokens, heads, dim = shape
     if dim != cache.head_dim or heads < 1 or heads % cache.kv_heads:
         raise ValueError(f"q's {heads} heads of {dim} cannot share the cache's {cache.kv_heads} of {cache.head_dim}")
-    q_strides = _head_rows(q, "q", shape, dtype, dev)
+    q_token, q_head = _head_rows(q, "q", shape, dtype, dev)
     pool, batch = _pool(cache, block_table, kv_lens)
     offsets = _offsets(q_offsets, batch, tokens, dev)
     if out is None:
         out = torch.empty_like(q)
-    out_strides = _head_rows(out, "out", shape, dtype, dev)
+        out_token, out_head, _ = out.stride()
+    else:
+        out_token, out_head = _head_rows(out, "out", shape, dtype, dev)
     if lse is None:
         lse = torch.empty((heads, tokens), dtype=torch.float32, device=dev)
     else:
@@ -267,24 +277,20 @@ def cache_attention(q, cache, block_table, kv_lens, *, q_offsets=None, max_rows:
     if slopes is not None:
         _need(slopes, "slopes", device=dev, dtypes=(torch.float32,), numel=heads)
         slope_ptr = slopes.data_ptr()
-    prefix = _need_lens(prefix_lens, "prefix_lens", batch, dev)
-
-    def args(ws, ws_bytes):
-        return _ATTN.pack(_DTYPES[dtype], heads, 1 if causal else 0, min(max_rows or 0, 1 << 30), scale or 0.0, softcap,
-                          tokens, q.data_ptr(), out.data_ptr(), *q_strides, *out_strides, lse.data_ptr(), slope_ptr, prefix,
-                          offsets, ws, ws_bytes)
+    prefix = _list(prefix_lens, "prefix_lens", batch, dev)
 
     # The size depends on sizes and on which lists there are, not on any value.
-    key = (cache.dtype, cache.kv_heads, cache.page_size, tuple(shape), batch, block_table.shape[1], max_rows, bool(causal),
-           offsets != 0, prefix != 0)
+    key = (cache.dtype, cache.kv_heads, cache.page_size, shape, batch, block_table.shape[1], max_rows, offsets == 0)
     need = block._sizes.get(("h3qk_cache_attention_workspace_bytes", dev.index, key))
+    call = [_DTYPES[dtype], heads, 1 if causal else 0, min(max_rows or 0, 1 << 30), scale or 0.0, softcap, tokens,
+            q.data_ptr(), out.data_ptr(), q_token, q_head, out_token, out_head, lse.data_ptr(), slope_ptr, prefix, offsets]
     if need is None:
-        need = block._size("h3qk_cache_attention_workspace_bytes", dev, pool, args(0, 0), key=key)
+        need = block._size("h3qk_cache_attention_workspace_bytes", dev, pool, _ATTN.pack(*call, 0, 0), key=key)
     ws = ws_bytes = 0
     if need:
         workspace, ws_bytes = _workspace(workspace, need, dev)
         ws = workspace.data_ptr()
-    block._call("h3qk_cache_attention", dev, pool, args(ws, ws_bytes), _stream(dev))
+    block._call("h3qk_cache_attention", dev, pool, _ATTN.pack(*call, ws, ws_bytes), _stream(dev))
     return out, lse
 
 
@@ -306,14 +312,15 @@ def cache_read(cache, block_table, kv_lens, *, starts=None, rows: int | None = N
         rows = block_table.shape[1] * cache.page_size
     if rows < 0 or rows >= 1 << 30:
         raise ValueError(f"rows must be from 0 to 2^30, got {rows}")
-    first = _need_lens(starts, "starts", batch, dev)
+    first = _list(starts, "starts", batch, dev)
     shape = (batch, cache.kv_heads, rows, cache.head_dim)
-    out = []
-    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _need(t, name, device=dev, dtypes=(dtype,), numel=batch * cache.kv_heads * rows * cache.head_dim)
-        out.append(t)
-    block._call("h3qk_cache_read", dev, pool, first, rows, _DTYPES[dtype], out[0].data_ptr(), out[1].data_ptr(), _stream(dev))
-    return out[0], out[1]
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out_k, "out_k", device=dev, dtypes=(dtype,), numel=batch * cache.kv_heads * rows * cache.head_dim)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out_v, "out_v", device=dev, dtypes=(dtype,), numel=batch * cache.kv_heads * rows * cache.head_dim)
+    block._call("h3qk_cache_read", dev, pool, first, rows, _DTYPES[dtype], out_k.data_ptr(), out_v.data_ptr(), _stream(dev))
+    return out_k, out_v

@@ -16,6 +16,8 @@ using h3qk_detail::range_of;
 // What a block takes at least: for few rows units of 64 keys, two turns of its
 // warps; for many, tiles of 128 keys, to be worth its start and the join.
 constexpr int kLeastUnits = 4, kLeastTiles = 4;
+// What a block of a cluster takes at most: beyond, the line's shares are shorter.
+constexpr int kMostUnits = 16;
 
 // Calls whose sequences have at most kFew packed rows go to the kernel for few
 // rows, which reads (and converts) their keys once for 8 or 16 of them; others
@@ -27,6 +29,7 @@ constexpr int kFew = 32;
 struct Cut {
     bool tiles;            // the kernel for many rows
     int row_tile, blocks;  // few rows
+    int cluster;           // their row tiles, where clusters take them
     TileGrid grid;         // many rows
     int64_t floats;        // of partial results
 };
@@ -42,6 +45,14 @@ Cut cut_of(const h3qk_cache& c, const h3qk_cache_attn& a, int64_t max_rows)
         const int64_t per = (static_cast<int64_t>(c.max_pages) * c.page_size + kUnit - 1) / kUnit;
         const double units = static_cast<double>(c.batch) * c.kv_heads * tiles * (per > 0 ? per : 1);
         const int most = few_blocks(c.format == H3QK_E2M1);
+        // A cluster a run, while all of them fit the GPU at once and a block's
+        // share of the longest cache stays short.
+        const double clustered = static_cast<double>(c.batch) * c.kv_heads * tiles * kCluster;
+        if (clustered <= most && per <= kCluster * kMostUnits) {
+            t.cluster = static_cast<int>(tiles);
+            t.blocks = static_cast<int>(clustered);
+            return t;
+        }
         const double want = std::ceil(units / kLeastUnits);
         t.blocks = want < most ? static_cast<int>(want) : most;
         t.floats = few_floats(t.blocks, t.row_tile, c.head_dim);
@@ -167,6 +178,7 @@ extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_
     cudaError_t e;
     if (!cut.tiles) {
         p.least = kLeastUnits;
+        p.cluster = cut.cluster;
         e = cache_few(e2m1, cut.row_tile, cut.blocks, p, st);
     } else {
         p.least = kLeastTiles;

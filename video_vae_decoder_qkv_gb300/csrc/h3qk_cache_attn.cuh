@@ -25,6 +25,7 @@ struct Attn {
     float* lse;                  // [heads][tokens]
     float* part;                 // partial results of the kernel that is launched
     int32_t least;               // units that a block takes at least
+    int32_t cluster;             // few rows: 0, or row tiles of the longest sequence, a cluster a run
     unsigned int* stuck;
 };
 
@@ -106,7 +107,8 @@ struct TileGrid {
 // block leaves two at most; and of the words that tell the join of them.
 inline int64_t tile_floats(int dim) { return h3qk_core::tile_part_floats(dim); }
 constexpr int kBrokenFloats = 5;
-constexpr int kUnit = 64;  // keys of a unit of work of the kernel for few rows
+constexpr int kUnit = 64;    // keys of a unit of work of the kernel for few rows
+constexpr int kCluster = 8;  // blocks that share a run without a second launch
 H3QK_HIDDEN int few_blocks(bool e2m1);
 H3QK_HIDDEN int64_t few_floats(int blocks, int rows, int dim);
 H3QK_HIDDEN cudaError_t cache_few(bool e2m1, int row_tile, int blocks, const Attn& p, cudaStream_t st);

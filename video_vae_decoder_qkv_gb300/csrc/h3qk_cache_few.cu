@@ -12,6 +12,11 @@
 // another; whole runs are finished in place, and cut ones leave a partial
 // result (O, maximum, sum) that a second, chained kernel joins in order.
 //
+// Short caches of few sequences (a token's latency) take one launch: a cluster
+// of kCluster blocks shares a run, and joins its parts through the blocks'
+// shared memory.  One token over 4,896 keys, 4 K/V heads of 64: @@ us, with the
+// line and its join 10.6.
+//
 // Inside a share the block's warps take turns of keys in round robin, each
 // with its own copies in flight (cp.async into a ring of its own: no barrier
 // between warps), its own running maximum, sum and O, and meet in shared
@@ -428,6 +433,18 @@ __device__ __forceinline__ int64_t share_of(const Attn& p, int64_t total, int bl
 // begins in the middle of (or fills), and of the one that it breaks off.
 __host__ __device__ inline int64_t part_floats(int rows, int dim) { return static_cast<int64_t>(rows) * (dim + 2); }
 
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this block's shared memory in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t of_block(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
 // HALF: the products are binary16's.  BENT: scores are capped, or less a slope times the distance.
 template <class T, bool HALF, bool BENT, int NB>
 __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const __grid_constant__ Attn p)
@@ -448,24 +465,44 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
     float(*sh_o)[ROWS][DP + 4] = reinterpret_cast<float(*)[ROWS][DP + 4]>(dynamic);
     const T format(p.c, lane);
 
-    const int64_t total = all_units<ROWS>(p), share = share_of(p, total, gridDim.x);
-    const int64_t begin = blockIdx.x * share, end = min(begin + share, total);
-    if (begin >= end) return;
-    int64_t before;
-    int item = find_unit<ROWS>(p, begin, before);
-    Part part = part_of<ROWS>(p, item);
+    int64_t begin = 0, end = 1, before = 0;
+    int item;
+    Part part;
+    if (p.cluster) {
+        item = blockIdx.x / (kCluster * p.c.kv_heads * p.cluster);
+        part = part_of<ROWS>(p, item);
+        if (static_cast<int>(blockIdx.x / kCluster % p.cluster) >= part.tiles) return;  // the whole cluster
+    } else {
+        const int64_t total = all_units<ROWS>(p), share = share_of(p, total, gridDim.x);
+        begin = blockIdx.x * share;
+        end = min(begin + share, total);
+        if (begin >= end) return;
+        item = find_unit<ROWS>(p, begin, before);
+        part = part_of<ROWS>(p, item);
+    }
 
     for (int64_t pos = begin; pos < end;) {
-        while (pos >= before + part.units(p)) {  // (every unit up to `end` has a sequence)
-            before += part.units(p);
-            part = part_of<ROWS>(p, ++item);
+        int unit, units, kv, row_tile;
+        if (p.cluster) {
+            const int run = blockIdx.x / kCluster, each = (part.per + kCluster - 1) / kCluster;
+            row_tile = run % p.cluster;
+            kv = run / p.cluster % p.c.kv_heads;
+            unit = min(static_cast<int>(blockIdx.x % kCluster) * each, part.per);
+            units = min(part.per - unit, each);
+            pos = end;
+        } else {
+            while (pos >= before + part.units(p)) {  // (every unit up to `end` has a sequence)
+                before += part.units(p);
+                part = part_of<ROWS>(p, ++item);
+            }
+            const int64_t run = (pos - before) / part.per;
+            unit = static_cast<int>((pos - before) - run * part.per);
+            units = static_cast<int>(min(static_cast<int64_t>(part.per - unit), end - pos));
+            kv = static_cast<int>(run / part.tiles);
+            row_tile = static_cast<int>(run % part.tiles);
+            pos += units;
         }
         const Sequence& s = part.s;
-        const int64_t run = (pos - before) / part.per;
-        const int unit = static_cast<int>((pos - before) - run * part.per);
-        const int units = static_cast<int>(min(static_cast<int64_t>(part.per - unit), end - pos));
-        const int kv = static_cast<int>(run / part.tiles), row_tile = static_cast<int>(run % part.tiles);
-        pos += units;
 
         // This lane's packed row of each block of 8 for Q, and the two whose scores it holds.
         float o[kOut][NB][4], m[NB][2], l[NB][2];
@@ -744,8 +781,11 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                     *reinterpret_cast<float2*>(&sh_o[warp][row][T::v_channel(g, k)]) = make_float2(o[k][b][h], o[k][b][2 + h]);
             }
         __syncthreads();
-        const bool whole = units == part.per;
-        float* to = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (unit == 0 ? 1 : 0)) * part_floats(ROWS, p.c.dim);
+        const bool whole = units == part.per && !p.cluster;
+        // (of a cluster: this block's part, behind the warps' O)
+        float* shared_part = reinterpret_cast<float*>(dynamic) + kWarps * ROWS * (DP + 4);
+        static_assert(T::kWarps * T::kStages * T::kStage >= (kWarps * ROWS * (DP + 4) + ROWS * (DP + 2)) * 4, "a part fits behind");
+        float* to = p.cluster ? shared_part : p.part + (2 * static_cast<int64_t>(blockIdx.x) + (unit == 0 ? 1 : 0)) * part_floats(ROWS, p.c.dim);
         const int per = p.c.dim / 4;
         for (int i = threadIdx.x; i < ROWS * per; i += 32 * kWarps) {
             const int row = i / per, d = 4 * (i - row * per);
@@ -774,7 +814,44 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 if (d == 0) *reinterpret_cast<float2*>(to + ROWS * p.c.dim + 2 * row) = make_float2(top, sum);
             }
         }
-        __syncthreads();
+        if (!p.cluster) {
+            __syncthreads();
+            continue;
+        }
+        // Each block joins a share of the values, part by part in order.
+        cluster_sync();
+        const uint32_t mine = smem_addr(shared_part);
+        for (int i = threadIdx.x + 32 * kWarps * static_cast<int>(blockIdx.x % kCluster); i < ROWS * per;
+             i += 32 * kWarps * kCluster) {
+            const int row = i / per, d = 4 * (i - row * per), r = row_tile * ROWS + row;
+            if (r >= part.packed) break;
+            float tops[kCluster], sums[kCluster], top = -INFINITY, sum = 0.0f;
+            float4 x[kCluster], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kCluster; ++w) {
+                const uint32_t there = of_block(mine, w);
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(tops[w]), "=f"(sums[w])
+                             : "r"(there + (ROWS * p.c.dim + 2 * row) * 4)
+                             : "memory");
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(x[w].x), "=f"(x[w].y), "=f"(x[w].z), "=f"(x[w].w)
+                             : "r"(there + (row * p.c.dim + d) * 4)
+                             : "memory");
+                top = fmaxf(top, tops[w]);
+            }
+#pragma unroll
+            for (int w = 0; w < kCluster; ++w) {
+                const float f = tops[w] == -INFINITY ? (sums[w] == 0.0f ? 0.0f : 1.0f) : exp2_fast(tops[w] - top);
+                sum = fmaf(sums[w], f, sum);
+                v.x = fmaf(x[w].x, f, v.x);
+                v.y = fmaf(x[w].y, f, v.y);
+                v.z = fmaf(x[w].z, f, v.z);
+                v.w = fmaf(x[w].w, f, v.w);
+            }
+            finish_row(p, s, kv, r, d, v, top, sum, kShift, T::kE2m1 ? p.c.v_scale : 1.0f);
+        }
+        cluster_sync();  // no block leaves while another reads its part
     }
 }
 
@@ -871,6 +948,22 @@ cudaError_t launch(const Attn& p, int blocks, cudaStream_t st)
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         raised[dev] = true;
+    }
+    if (p.cluster) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+        cfg.blockDim = dim3(32 * T::kWarps);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kCluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+        h3qk_internal_count_launch();
+        return e != cudaSuccess ? e : cudaGetLastError();
     }
     kernel<<<blocks, 32 * T::kWarps, smem, st>>>(p);
     h3qk_internal_count_launch();
