@@ -33,7 +33,10 @@ using h3qk_detail::range_of;
 // 8 codes are one 4-byte store.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8, kBlocks = 3;  // of a block; of an SM
-constexpr int kAhead = 3;
+// Head rows of copies ahead: the 4-bit form's longer arithmetic hides them
+// behind less (32,640 rows of 40 + 2 x 8 heads of 128, read back: 212 us with 2,
+// 224 with 3; in 16 bits 13,000 rows 70 us with 2, 67 with 3).
+constexpr int kAhead4 = 2, kAhead16 = 3;
 
 struct AppendArgs {
     h3qk::Params p;  // the preparation's description of the rows; heads: Q, K and V together
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const __gr
 {
     const h3qk::Params& p = a.p;
     const Pool& c = a.c;
-    constexpr int TPW = 32 / LPR;
+    constexpr int TPW = 32 / LPR, kAhead = E2M1 ? kAhead4 : kAhead16;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunk = lane % LPR, sub = lane / LPR;  // this lane's chunks: chunk + q LPR
     const int D = p.head_dim;
@@ -235,16 +238,20 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const __gr
 }
 
 // ---------------------------------------------------------------------------
-// Reading back: a thread takes 8 channels of kReadRows rows of a page pool's
-// head, K in one half of the grid and V in the other.  Bound by HBM: mostly
+// Reading back: a thread takes 8 channels of kReadRows rows of a head at a
+// time, `turns` times, the next turn's rows on their way; K in one half of the
+// grid and V in the other.  Small calls spread over the GPU in one turn.  Four
+// caches of up to 32,768 keys, 8 K/V heads of 128, 4 bits to bf16: 106 us, 6.0
+// TB/s; 116 in one turn a thread.  Bound by HBM: mostly
 // the dense rows' 2 bytes a value on their way out.
 // ---------------------------------------------------------------------------
-constexpr int kReadRows = 4;
+constexpr int kReadRows = 3, kReadTurns = 8;
 
 struct ReadArgs {
     Pool c;
     const int32_t* starts;
     int64_t rows;
+    int32_t turns;
     uint16_t* out[2];
 };
 
@@ -262,44 +269,58 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
     const int64_t page_bytes = is_v ? c.v_page : c.k_page, row_bytes = is_v ? c.v_row : c.k_row;
     const int64_t scale_page = is_v ? c.vs_page : c.ks_page;
     const float tensor_scale = is_v ? c.v_scale : c.k_scale;
+    const int64_t step = static_cast<int64_t>(blockDim.y) * kReadRows;
+    const int64_t end = min(a.rows, (blockIdx.x + int64_t{1}) * step * a.turns);
     uint4 got[kReadRows];
     uint32_t scale[kReadRows];
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y * kReadRows + threadIdx.y;
+    auto fetch = [&](int64_t first) {
 #pragma unroll
-    for (int u = 0; u < kReadRows; ++u) {
-        const int64_t r = first + static_cast<int64_t>(u) * blockDim.y, at = start + r;
-        got[u] = make_uint4(0, 0, 0, 0);
-        scale[u] = 0;
-        if (r >= a.rows || at >= keys) continue;
-        const int page = page_of(c, table, static_cast<int>(at));
-        if (page < 0) continue;
-        const int in_page = static_cast<int>(at) & ((1 << c.page_shift) - 1);
-        const uint8_t* from = data + page * page_bytes + in_page * row_bytes;
-        if constexpr (E2M1) {
-            got[u].x = __ldcs(reinterpret_cast<const uint32_t*>(from) + chunk);
-            scale[u] = __ldg(scales + page * scale_page + static_cast<int64_t>(in_page) * (c.dim / 16) + chunk / 2);
-        } else {
-            got[u] = __ldcs(reinterpret_cast<const uint4*>(from) + chunk);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < kReadRows; ++u) {
-        const int64_t r = first + static_cast<int64_t>(u) * blockDim.y;
-        if (r >= a.rows) continue;
-        if constexpr (E2M1) {
-            uint32_t v[4], w[4];
-            widen_codes(got[u].x, v);
-            const uint32_t g = widen_scales(scale[u] * 0x101u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // the product of code and scale is exact
-                const float2 f = h3qk::widen2<false>(mul_half2(v[i], g));
-                w[i] = h3qk::round2<BF16>(__fmul_rn(f.x, tensor_scale), __fmul_rn(f.y, tensor_scale));
+        for (int u = 0; u < kReadRows; ++u) {
+            const int64_t r = first + u * blockDim.y, at = start + r;
+            got[u] = make_uint4(0, 0, 0, 0);
+            scale[u] = 0;
+            if (r >= end || at >= keys) continue;
+            const int page = page_of(c, table, static_cast<int>(at));
+            if (page < 0) continue;
+            const int in_page = static_cast<int>(at) & ((1 << c.page_shift) - 1);
+            const uint8_t* from = data + page * page_bytes + in_page * row_bytes;
+            if constexpr (E2M1) {
+                got[u].x = __ldcs(reinterpret_cast<const uint32_t*>(from) + chunk);
+                scale[u] = __ldg(scales + page * scale_page + static_cast<int64_t>(in_page) * (c.dim / 16) + chunk / 2);
+            } else {
+                got[u] = __ldcs(reinterpret_cast<const uint4*>(from) + chunk);
             }
-            got[u] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        __stcs(reinterpret_cast<uint4*>(a.out[is_v ? 1 : 0] + (static_cast<int64_t>(blockIdx.y) * a.rows + r) * c.dim) + chunk,
-               got[u]);
+    };
+    int64_t first = blockIdx.x * step * a.turns + threadIdx.y;
+    fetch(first);
+    for (; first < end; first += step) {
+        uint4 now[kReadRows];
+#pragma unroll
+        for (int u = 0; u < kReadRows; ++u) {
+            now[u] = got[u];
+            if constexpr (E2M1) now[u].y = scale[u];
+        }
+        if (first + step < end) fetch(first + step);  // the next turn's rows are on their way
+#pragma unroll
+        for (int u = 0; u < kReadRows; ++u) {
+            const int64_t r = first + u * blockDim.y;
+            if (r >= end) continue;
+            if constexpr (E2M1) {
+                uint32_t v[4], w[4];
+                widen_codes(now[u].x, v);
+                const uint32_t g = widen_scales(now[u].y * 0x101u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // the product of code and scale is exact
+                    const float2 f = h3qk::widen2<false>(mul_half2(v[i], g));
+                    w[i] = h3qk::round2<BF16>(__fmul_rn(f.x, tensor_scale), __fmul_rn(f.y, tensor_scale));
+                }
+                now[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __stcs(reinterpret_cast<uint4*>(a.out[is_v ? 1 : 0] + (static_cast<int64_t>(blockIdx.y) * a.rows + r) * c.dim) + chunk,
+                   now[u]);
+        }
     }
 }
 
@@ -524,8 +545,8 @@ extern "C" h3qk_status h3qk_cache_append(const h3qk_cache* cache, const void* qk
     const int cap = kBlocks * h3qk_internal_sm_count();
     const int64_t warps = static_cast<int64_t>(cap) * kWarps;
     int64_t least = INT64_MAX;
-    for (int32_t slices = 1; slices <= (all + kAhead - 1) / kAhead; ++slices) {
-        const int32_t h = ((all + slices - 1) / slices + kAhead - 1) / kAhead * kAhead;
+    for (int32_t slices = 1; slices <= (all + 3) / 4; ++slices) {
+        const int32_t h = ((all + slices - 1) / slices + 3) / 4 * 4;
         const int64_t n = (all + h - 1) / h;
         const int64_t cost = (a.groups * n + warps - 1) / warps * (h + 8);
         if (cost < least) {
@@ -572,7 +593,11 @@ extern "C" h3qk_status h3qk_cache_read(const h3qk_cache* cache, const int32_t* s
     a.out[1] = static_cast<uint16_t*>(out_v);
     const int chunks = a.c.dim / 8, per = 256 / chunks;
     const dim3 block(chunks, per);
-    const dim3 grid(static_cast<unsigned>((rows + per * kReadRows - 1) / (per * kReadRows)), static_cast<unsigned>(slots), 2);
+    const int64_t one_turn = (rows + per * kReadRows - 1) / (per * kReadRows);
+    const int64_t turns = one_turn * slots * 2 / (8 * h3qk_internal_sm_count());
+    a.turns = static_cast<int32_t>(turns < 1 ? 1 : turns > kReadTurns ? kReadTurns : turns);
+    const int64_t a_block = static_cast<int64_t>(per) * kReadRows * a.turns;
+    const dim3 grid(static_cast<unsigned>((rows + a_block - 1) / a_block), static_cast<unsigned>(slots), 2);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == H3QK_BF16;
     if (e2m1) {
