@@ -14,8 +14,8 @@
 //
 // Short caches of few sequences (a token's latency) take one launch: a cluster
 // of kCluster blocks shares a run, and joins its parts through the blocks'
-// shared memory.  One token over 4,896 keys, 4 K/V heads of 64: @@ us, with the
-// line and its join 10.6.
+// shared memory.  One token over 4,896 keys, 4 K/V heads of 64: 7.6 us, with the
+// line and its join 10.7.
 //
 // Inside a share the block's warps take turns of keys in round robin, each
 // with its own copies in flight (cp.async into a ring of its own: no barrier
@@ -131,7 +131,7 @@ struct Source {
 template <int DIM, int NB>
 struct Codes {
     static constexpr bool kE2m1 = true;
-    static constexpr int kDim = DIM, DP = DIM <= 64 ? 64 : 128;
+    static constexpr int DP = DIM <= 64 ? 64 : 128;
     static constexpr int kTurn = 32, kWarps = 3, kStages = 3, kBlocks = 4;
     static constexpr int kPitch = DP / 2;
     static constexpr int kGroups = DIM / 16;            // scale bytes a row
@@ -290,7 +290,7 @@ struct Codes {
 template <int DP_, int NB>
 struct Halves {
     static constexpr bool kE2m1 = false;
-    static constexpr int kDim = DP_, DP = DP_;
+    static constexpr int DP = DP_;
     static constexpr int kTurn = 16, kWarps = 4, kStages = 3, kBlocks = 2;
     static constexpr int kPitch = DP * 2, kStage = 2 * kTurn * kPitch;
     static constexpr int kK = DP / 32, kV = DP / 64;  // pieces of a lane's K row and V row

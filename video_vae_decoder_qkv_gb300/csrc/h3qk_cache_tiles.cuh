@@ -83,11 +83,16 @@ __device__ __forceinline__ Run run_of(const Attn& p, int item)
     r.tiles = (r.packed + 2 * kTile - 1) / (2 * kTile);
     return r;
 }
-// Tiles of keys that a tile's rows see; a tile without keys is a unit all the same.
+// A tile's units: the tiles of keys that its rows see, behind kTileCost units
+// for its rows of Q, the pipeline's start and its result.  (2,048 rows of a
+// fresh prompt, where the first tiles see few keys, 40 heads on 8 of 128: 125 us
+// with none, 107 with 1, 88 with 3, 83 with 6, 86 with 10; chunks behind long
+// caches 746, 750, 734, 723 and 728.)
+constexpr int kTileCost = 5;
 __device__ __forceinline__ int units_of(const Attn& p, const Run& r, int tile)
 {
     const int last = min((tile + 1) * 2 * kTile, r.packed) - 1;
-    return max((limit_of(r.s, p.causal, divide(last, p.group)) + kTile - 1) / kTile, 1);
+    return (limit_of(r.s, p.causal, divide(last, p.group)) + kTile - 1) / kTile + kTileCost;
 }
 // Warp-wide: the units of one K/V head of each lane's run.  Runs of many
 // tiles are counted by all lanes together.
@@ -206,6 +211,7 @@ struct Line {
 // What a block does of one tile: `n_all` tiles of keys from the j0-th on.
 struct Piece {
     int row0;               // the tile's first packed row
+    int unit0;              // the first of its units
     int j0, n_all, key0;
     int n[2];               // tiles of keys of each group
     int seen;               // keys that any row sees
@@ -213,9 +219,11 @@ struct Piece {
     __device__ __forceinline__ Piece(const Attn& p, const Line& at, int64_t pos, int64_t end, bool codes)
     {
         row0 = at.tile * 2 * kTile;
-        j0 = static_cast<int>(pos - at.before);
-        n_all = static_cast<int>(min(static_cast<int64_t>(at.units - j0), end - pos));
-        whole = n_all == at.units;
+        unit0 = static_cast<int>(pos - at.before);
+        const int past_unit = static_cast<int>(min(static_cast<int64_t>(at.units), end - at.before));
+        whole = past_unit - unit0 == at.units;
+        j0 = max(unit0 - kTileCost, 0);
+        n_all = max(past_unit - kTileCost, 0) - j0;
         int full[2];
         seen = 0;
 #pragma unroll
@@ -853,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The share ends in this tile.  Its parts: this block's and, the shares being
                 // equal, as many as the rest takes; a tile that an earlier block broke off is that one's.
                 const int64_t rest = at.before + at.units - end;
-                broken->parts = rest > 0 && pc.j0 == 0 ? 1 + static_cast<int>((rest + at.share - 1) / at.share) : 0;
+                broken->parts = rest > 0 && pc.unit0 == 0 ? 1 + static_cast<int>((rest + at.share - 1) / at.share) : 0;
                 broken->first = at.run.s.first;
                 broken->packed_left = at.run.packed - pc.row0;
                 broken->kv = at.kv;
@@ -861,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool writes = row.has && !(pc.halved && g == 1);
             const bool nan_row = sum != sum, some = n > 0;
-            float* to = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (pc.j0 == 0 ? 1 : 0)) * part_floats(p.c.dim);
+            float* to = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (pc.unit0 == 0 ? 1 : 0)) * part_floats(p.c.dim);
             const int tr = (pc.halved ? 0 : g * kTile) + r;
             if (writes) {
                 if (!pc.whole) *reinterpret_cast<float2*>(to + 2 * kTile * p.c.dim + 2 * tr) = make_float2(top, sum);
@@ -920,54 +928,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// For each block whose share broke a tile off: one warp a packed row, its
-// parts' O, weighted to their common maximum, in order.
-constexpr int kJoinRows = 8;  // and warps of a block
-__global__ void __launch_bounds__(32 * kJoinRows) join_tiles_kernel(const __grid_constant__ Attn p, int blocks, float shift,
-                                                                    float v_scale)
+// For each block whose share broke a tile off: a warp takes four packed rows
+// at once, their parts' O, weighted to their common maximum, in order.
+constexpr int kJoinWarps = 8, kJoinAtOnce = 4, kJoinRows = kJoinWarps * kJoinAtOnce;  // of a block
+__global__ void __launch_bounds__(32 * kJoinWarps) join_tiles_kernel(const __grid_constant__ Attn p, int blocks, float shift,
+                                                                     float v_scale)
 {
     const int lane = threadIdx.x & 31, d = 4 * lane;
     const int first = blockIdx.x / (2 * kTile / kJoinRows);
-    const int tr = blockIdx.x % (2 * kTile / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
+    const int tr = blockIdx.x % (2 * kTile / kJoinRows) * kJoinRows + (threadIdx.x >> 5) * kJoinAtOnce;
     const int64_t size = part_floats(p.c.dim);
     // (every block waits: what follows this kernel must find the tiles done)
     h3qk_ops::wait_for_previous();
     const int* words = reinterpret_cast<const int*>(reinterpret_cast<const Broken*>(p.part + 2 * blocks * size) + first);
     int word = 0;
     if (lane < 5) word = __ldcg(words + lane);
-    const int n = __shfl_sync(0xffffffffu, word, 0);
-    if (tr >= __shfl_sync(0xffffffffu, word, 2) || n == 0) return;
+    const int n = __shfl_sync(0xffffffffu, word, 0), rows = min(__shfl_sync(0xffffffffu, word, 2) - tr, kJoinAtOnce);
+    if (rows <= 0 || n == 0) return;
     Sequence s = {};
     s.first = __shfl_sync(0xffffffffu, word, 1);
     const int kv = __shfl_sync(0xffffffffu, word, 3), row = __shfl_sync(0xffffffffu, word, 4) + tr;
     // the first block's part is the one that it broke off, the others' the one that they began in
     auto slot = [&](int i) { return p.part + (2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0)) * size; };
-    auto stat = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(slot(i) + 2 * kTile * p.c.dim + 2 * tr)); };
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, stat(i).x);
+    auto stat = [&](int i, int q) {
+        return __ldcg(reinterpret_cast<const float2*>(slot(i) + 2 * kTile * p.c.dim + 2 * (tr + q)));
+    };
+    float top[kJoinAtOnce], sum[kJoinAtOnce];
+    float4 v[kJoinAtOnce];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float sum = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        float2 mine = make_float2(-INFINITY, 0.0f);
-        if (i0 + lane < n) mine = stat(i0 + lane);
-        const float f = mine.x == -INFINITY ? (mine.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(mine.x - top);
-        const int count = min(32, n - i0);
-#pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, mine.y, i);
-            sum = fmaf(li, fi, sum);
-            if (d < p.c.dim) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(slot(i0 + i) + static_cast<int64_t>(tr) * p.c.dim + d));
-                v.x = fmaf(x.x, fi, v.x);
-                v.y = fmaf(x.y, fi, v.y);
-                v.z = fmaf(x.z, fi, v.z);
-                v.w = fmaf(x.w, fi, v.w);
-            }
-        }
+    for (int q = 0; q < kJoinAtOnce; ++q) {
+        top[q] = -INFINITY;
+        sum[q] = 0.0f;
+        v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    finish_row(p, s, kv, row, d, v, top, sum, shift, v_scale);
+    for (int i = lane; i < n; i += 32)
+#pragma unroll
+        for (int q = 0; q < kJoinAtOnce; ++q)
+            if (q < rows) top[q] = fmaxf(top[q], stat(i, q).x);
+#pragma unroll
+    for (int q = 0; q < kJoinAtOnce; ++q)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], o));
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float f[kJoinAtOnce], l[kJoinAtOnce];
+#pragma unroll
+        for (int q = 0; q < kJoinAtOnce; ++q) {
+            float2 mine = make_float2(-INFINITY, 0.0f);
+            if (i0 + lane < n && q < rows) mine = stat(i0 + lane, q);
+            f[q] = mine.x == -INFINITY ? (mine.y == 0.0f ? 0.0f : 1.0f) : exp2_fast(mine.x - top[q]);
+            l[q] = mine.y;
+        }
+        const int count = min(32, n - i0);
+#pragma unroll 2
+        for (int i = 0; i < count; ++i)
+#pragma unroll
+            for (int q = 0; q < kJoinAtOnce; ++q) {
+                const float fi = __shfl_sync(0xffffffffu, f[q], i), li = __shfl_sync(0xffffffffu, l[q], i);
+                sum[q] = fmaf(li, fi, sum[q]);
+                if (d < p.c.dim && q < rows) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(slot(i0 + i) + (tr + q) * p.c.dim + d));
+                    v[q].x = fmaf(x.x, fi, v[q].x);
+                    v[q].y = fmaf(x.y, fi, v[q].y);
+                    v[q].z = fmaf(x.z, fi, v[q].z);
+                    v[q].w = fmaf(x.w, fi, v[q].w);
+                }
+            }
+    }
+#pragma unroll
+    for (int q = 0; q < kJoinAtOnce; ++q)
+        if (q < rows) finish_row(p, s, kv, row + q, d, v[q], top[q], sum[q], shift, v_scale);
 }
 
 template <bool E2M1, bool BF16, int DP, int BENDS>
@@ -983,7 +1012,7 @@ cudaError_t launch(const Attn& p, const Maps& m, const TileGrid& grid, cudaStrea
     const cudaError_t launched = cudaGetLastError();
     if (launched != cudaSuccess || grid.blocks == 1) return launched;
     return h3qk_ops::launch_chained(join_tiles_kernel, dim3(static_cast<unsigned>(grid.blocks - 1) * (2 * kTile / kJoinRows)),
-                                    dim3(32 * kJoinRows), 0, st, p, grid.blocks, E2M1 || !BF16 ? 7.0f : 0.0f, E2M1 ? p.c.v_scale : 1.0f);
+                                    dim3(32 * kJoinWarps), 0, st, p, grid.blocks, E2M1 || !BF16 ? 7.0f : 0.0f, E2M1 ? p.c.v_scale : 1.0f);
 }
 
 // (slopes of 0 where there are none: caps are an instance less that way)
