@@ -633,9 +633,10 @@ h3qk_status h3qk_cache_append(const h3qk_cache* cache, const void* qkv, const fl
  * sees its kv_lens[b] keys; with causal, of those the ones up to its own
  * position and the first prefix_lens[b].  Rows that see no key get out = 0 and
  * lse = -infinity; rows of no sequence, and rows past max_rows of one, are left
- * as they were.  Scores, sums and outputs are binary32.  p is rounded for its
- * product with v: to the type of q, over 4-bit caches of few rows always to
- * binary16.  The same call gives the same bits every time.
+ * as they were.  A non-finite key reaches the rows that see it, a non-finite
+ * value may reach all rows of a sequence that sees it, and rows of the cache
+ * that no row sees reach none.  Scores, sums and outputs are binary32.  p is rounded for its
+ * product with v: to the type of q, over 4-bit caches always to binary16.  The same call gives the same bits every time.
  * Fill the struct from zeros.
  */
 typedef struct h3qk_cache_attn {
@@ -665,6 +666,7 @@ h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_cache_attn*
  * head_dim] (contiguous, 16-byte aligned, of dtype: a 16-bit cache's own; what
  * 4 bits stand for, rounded once), with zeros after them.  starts NULL: from
  * row 0.  The result serves h3qk_attention and its gradient, or another cache.
+ * batch * kv_heads is at most 65535.
  */
 h3qk_status h3qk_cache_read(const h3qk_cache* cache, const int32_t* starts, int64_t rows, h3qk_dtype dtype,
                             void* out_k, void* out_v, h3qk_stream_t stream);

@@ -146,8 +146,54 @@ def test_rows_without_offsets(fmt, rows):
     cache, table, lens = cu.build([100, 61, 400], 2, 64, 32, fmt)
     q = torch.randn(3 * rows, 4, 64, device="cuda").to(BF16)
     off = torch.arange(0, 3 * rows + 1, rows, dtype=torch.int32, device="cuda")
-    a, b = cache_attention(q, cache, table, lens), cache_attention(q, cache, table, lens, q_offsets=off)
+    a, b = cache_attention(q, cache, table, lens), cache_attention(q, cache, table, lens, q_offsets=off, max_rows=rows)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # without max_rows the host does not know the sequences' rows, and may cut the call otherwise
+    c = cache_attention(q, cache, table, lens, q_offsets=off)
+    want, _ = cu.attention(q, cache, table, lens.tolist(), off.tolist())
+    for got in (a, c):
+        bu.assert_within(got[0], want["out"], want["out_bound"], "out")
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", BF16])
+@pytest.mark.parametrize("rows,most", [(5, 2), (90, 60)])
+def test_rows_past_max_rows_are_left(fmt, rows, most):
+    """A sequence's first rows keep their places; the later ones are not touched."""
+    cache, table, lens = cu.build([rows, 300], 2, 64, 32, fmt)
+    q = torch.randn(2 * rows, 4, 64, device="cuda").to(BF16)
+    out = torch.full_like(q, 9.0)
+    cache_attention(q, cache, table, lens, max_rows=most, out=out)
+    want, _ = cu.attention(q, cache, table, lens.tolist(), [0, rows, 2 * rows])
+    kept = (torch.arange(2 * rows) % rows) < most
+    bu.assert_within(out[kept], want["out"][kept], want["out_bound"][kept], "out")
+    assert bool((out[~kept] == 9.0).all())
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", BF16])
+def test_call_on_a_device_that_is_not_current(fmt):
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one device")
+    cache, table, lens = cu.build([200], 2, 64, 32, fmt)
+    q = torch.randn(1, 4, 64, device="cuda:0").to(BF16)
+    want = cache_attention(q, cache, table, lens)
+    with torch.cuda.device(1):
+        got = cache_attention(q, cache, table, lens)
+    assert torch.equal(got[0], want[0])
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", BF16])
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_empty_pool_and_empty_table(fmt, rows):
+    """No pages at all: every row sees zeros where it has keys, and nothing where the table has no room."""
+    cache = Cache.empty(0, 2, 64, dtype=fmt)
+    q = torch.randn(2 * rows, 4, 64, device="cuda").to(BF16)
+    lens = torch.tensor([rows, 0], dtype=torch.int32, device="cuda")
+    out, lse = cache_attention(q, cache, torch.zeros(2, 8, dtype=torch.int32, device="cuda"), lens)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse[:, rows:]).all())
+    n = torch.arange(1, rows + 1, device="cuda").clamp(max=512)
+    assert torch.allclose(lse[0, :rows], n.float().log(), atol=1e-5)
+    out, lse = cache_attention(q, cache, torch.zeros(2, 0, dtype=torch.int32, device="cuda"), lens)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
 
 
 @pytest.mark.parametrize("fmt", ["e2m1", BF16])
@@ -228,3 +274,10 @@ def test_offsets_of_a_large_pool_pass_32_bits():
     want = cache_attention(q, small, table, lens)
     got = cache_attention(q, Cache(pool[0], pool[1]), far[table.long()].int(), lens)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_no_block_gave_up():
+    """After everything above: the kernels' bounded waits never ran out."""
+    from video_vae_decoder_qkv_gb300 import block
+
+    assert block._fn("h3qk_attention_stuck")() == 0

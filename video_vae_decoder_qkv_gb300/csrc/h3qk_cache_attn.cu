@@ -196,7 +196,7 @@ extern "C" h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_
             for (int i = 0; i < 2; ++i)
                 ok = ok && h3qk_core::encode_map(maps[i], data[i], bf16, c.head_dim, rows_a_page, none ? 1 : c.kv_heads,
                                                  none ? 1 : c.pages, none ? row : strides[i][0], none ? 16 * row : strides[i][1],
-                                                 none ? 16 * row : strides[i][2], none ? 16 : box);
+                                                 none ? 16 * row : strides[i][2], box);
         }
         if (!ok) return h3qk_core::no_maps();
         if (e2m1) e = bf16 ? cache_tiles_e2m1_bf16(p, m, cut.grid, st) : cache_tiles_e2m1_fp16(p, m, cut.grid, st);
