@@ -22,12 +22,12 @@
 //    scaled by a power of two first, as in the kernel for few rows.
 //
 // The tiles of the call, sequence after sequence, K/V head after head, each as
-// many units as it has tiles of 128 keys, are one line, cut into equal shares,
-// one a block: however few tiles there are, and however uneven, the SMs finish
-// together.  A tile that is cut leaves a partial result (O, maximum, sum) in
-// each of its blocks, and a chained kernel joins them in order.  Only the
-// device knows the sequences' rows and keys: every warp finds its block's
-// place in the line by itself.
+// many units as it has tiles of 128 keys and kTileCost more, are one line, cut
+// into equal shares, one a block: however few tiles there are, and however
+// uneven, the SMs finish together.  A tile that is cut leaves a partial result
+// (O, maximum, sum) in each of its blocks, and a chained kernel joins them in
+// order.  Only the device knows the sequences' rows and keys: a warp of each
+// block finds the block's place in the line.
 //
 // A tile of at most 128 rows is held by both groups, which take its keys in
 // turn and join their results from TMEM.
