@@ -71,6 +71,19 @@ __device__ __forceinline__ uint32_t widen_scales(uint32_t w)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
     return r;
 }
+// One half of a pair twice (as moves, which the products take as operand forms).
+__device__ __forceinline__ uint32_t both_low(uint32_t a)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t both_high(uint32_t a)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(a));
+    return r;
+}
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b)
 {
     uint32_t r;

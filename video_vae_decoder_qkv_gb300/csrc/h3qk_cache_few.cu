@@ -228,8 +228,8 @@ struct Codes {
             if (DIM < DP && !k_in) two = 0;
             if (EDGE && 16 * kb + 8 * t + g >= left) two = 0;
             const uint32_t wide = widen_scales(two);
-            sc[t][0] = __byte_perm(wide, wide, 0x1010);
-            if constexpr (DP == 128) sc[t][1] = __byte_perm(wide, wide, 0x3232);
+            sc[t][0] = both_low(wide);
+            if constexpr (DP == 128) sc[t][1] = both_high(wide);
         }
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {

@@ -370,15 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (E2M1) {
             constexpr int kPieces = DP / 32;              // 16-byte pieces of codes a row
             constexpr int kRowsEach = 32 / kPieces;       // rows of a warp-wide copy
-            constexpr int kTurns = kTile / kRowsEach;     // copies a tile: 16 or 8
-            constexpr int kMine = (kTurns + 2) / 3;
+            // A tile is eight blocks of 16 rows (which lie on one page), kPer copies each;
+            // the warps take three, three and two of them, in turn.
+            constexpr int kPer = 16 / kRowsEach, kMine = 3;
             const int w = warp - 9, piece = lane / kRowsEach, sub = lane % kRowsEach;
             const int dim = p.c.dim, row_bytes = dim / 2, groups = dim / 16;
             const bool in = 32 * piece < dim;
             const uint32_t staged = ring + kStages * S::kTileBytes;
-            // This lane's 16 bytes of each turn's codes; and of its scales, a few lanes'.
+            // This lane's 16 bytes of each copy of codes; and of a block's scales, a few lanes'.
             const int64_t code_at = sub * row_bytes + 16 * piece;
-            const bool has_scales = 16 * lane < kRowsEach * groups;
+            const bool has_scales = 16 * lane < dim;
             auto copy16 = [](uint32_t dst, const uint8_t* src, bool there) {
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
                              : "memory");
@@ -407,17 +408,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint8_t* from = v ? codes[1] : codes[0];
                         const uint8_t* scale_from = v ? scales[1] : scales[0];
                         const int64_t stride = v ? p.c.v_page : p.c.k_page, scale_stride = v ? p.c.vs_page : p.c.ks_page;
+                        const int block0 = (w + ri) % 3 * 3;
 #pragma unroll
                         for (int u = 0; u < kMine; ++u) {
-                            const int t = (w + ri) % 3 + 3 * u;
-                            const int page = __shfl_sync(0xffffffffu, pages, t * kRowsEach / 16 & 7);
-                            if (t >= kTurns) continue;
-                            const int in_page = (key_tile + t * kRowsEach) & page_mask;
+                            const int block = block0 + u;
+                            const int page = __shfl_sync(0xffffffffu, pages, block & 7);
+                            if (block >= 8) continue;
+                            const int in_page = (key_tile + 16 * block) & page_mask;
                             const bool there = page >= 0;
                             const int64_t pg = there ? page : 0;
-                            copy16(to + (t * 32 + lane) * 16, in ? from + pg * stride + in_page * row_bytes : p.c.k, there && in);
+                            const uint8_t* rows = in ? from + pg * stride + in_page * row_bytes : p.c.k;
+#pragma unroll
+                            for (int q = 0; q < kPer; ++q)
+                                copy16(to + ((block * kPer + q) * 32 + lane) * 16, in ? rows + q * kRowsEach * row_bytes : p.c.k,
+                                       there && in);
                             if (has_scales)
-                                copy16(to + S::kCodes + t * kRowsEach * groups + 16 * lane,
+                                copy16(to + S::kCodes + block * dim + 16 * lane,
                                        scale_from + pg * scale_stride + in_page * groups, there);
                         }
                     }
@@ -434,12 +440,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const uint32_t tile = ring + st * S::kTileBytes + store_at, from = staged + ri % S::kAhead * S::kCodeStage;
                     const int left = pc.seen - (pc.key0 + (i >> 1) * kTile) - sub;  // rows behind it hold nothing
-                    // (all reads first: one by one, each turn would wait for its own)
-                    uint32_t c[kMine][4], two[kMine];
+                    const int block0 = (w + ri) % 3 * 3;
+                    // (all reads first: one by one, each would be waited for by itself)
+                    uint32_t c[kMine * kPer][4], two[kMine * kPer];
 #pragma unroll
-                    for (int u = 0; u < kMine; ++u) {
-                        const int t = (w + ri) % 3 + 3 * u;
-                        if (t >= kTurns) continue;
+                    for (int u = 0; u < kMine * kPer; ++u) {
+                        const int t = block0 * kPer + u;
+                        if (t >= 8 * kPer) continue;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(c[u][0]), "=r"(c[u][1]), "=r"(c[u][2]), "=r"(c[u][3])
                                      : "r"(from + (t * 32 + lane) * 16)
@@ -452,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         two[u] = in && t * kRowsEach < left ? b : 0;
                     }
 #pragma unroll
-                    for (int u = 0; u < kMine; ++u) {
-                        const int t = (w + ri) % 3 + 3 * u;
-                        if (t >= kTurns) continue;
-                        const uint32_t g = widen_scales(two[u]), lo = __byte_perm(g, g, 0x1010), hi = __byte_perm(g, g, 0x3232);
+                    for (int u = 0; u < kMine * kPer; ++u) {
+                        const int t = block0 * kPer + u;
+                        if (t >= 8 * kPer) continue;
+                        const uint32_t g = widen_scales(two[u]), lo = both_low(g), hi = both_high(g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t v[4];
