@@ -46,7 +46,7 @@ Cut cut_of(const h3qk_cache& c, const h3qk_cache_attn& a, int64_t max_rows)
         const int64_t tiles = (packed + t.row_tile - 1) / t.row_tile;
         const int64_t per = (static_cast<int64_t>(c.max_pages) * c.page_size + kUnit - 1) / kUnit;
         const double units = static_cast<double>(c.batch) * c.kv_heads * tiles * (per > 0 ? per : 1);
-        const int most = few_blocks(c.format == H3QK_E2M1);
+        const int most = few_blocks(c.format == H3QK_E2M1, t.row_tile);
         // A cluster a run, while all of them fit the GPU at once and a block's
         // share of the longest cache stays short.
         const double clustered = static_cast<double>(c.batch) * c.kv_heads * tiles * kCluster;

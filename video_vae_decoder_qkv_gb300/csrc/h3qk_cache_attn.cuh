@@ -109,7 +109,7 @@ inline int64_t tile_floats(int dim) { return h3qk_core::tile_part_floats(dim); }
 constexpr int kBrokenFloats = 5;
 constexpr int kUnit = 64;    // keys of a unit of work of the kernel for few rows
 constexpr int kCluster = 8;  // blocks that share a run without a second launch
-H3QK_HIDDEN int few_blocks(bool e2m1);
+H3QK_HIDDEN int few_blocks(bool e2m1, int row_tile);
 H3QK_HIDDEN int64_t few_floats(int blocks, int rows, int dim);
 H3QK_HIDDEN cudaError_t cache_few(bool e2m1, int row_tile, int blocks, const Attn& p, cudaStream_t st);
 H3QK_HIDDEN cudaError_t cache_tiles_e2m1_fp16(const Attn& p, const Maps& m, const TileGrid& grid, cudaStream_t st);

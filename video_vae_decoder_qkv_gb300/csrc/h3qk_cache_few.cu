@@ -6,7 +6,7 @@
 // take 210 us, 6.5 TB/s.  4 bits leave a multiprocessor 6.5 cycles a key and
 // head, in which its four schedulers issue some 18 instructions (four
 // conversions, five products with scales and P, and what they need): 32 such
-// caches take 130 us, 5.5 TB/s, one of 524,288 keys 113 us.  Twelve warps with
+// caches take 130 us, 5.5 TB/s, one of 524,288 keys 112 us.  Twelve warps with
 // 168 registers each measured better than sixteen with 128 (148 us) or eight
 // with 255 (152).  The packed rows of a sequence (its query rows times the
 // heads that share a K/V head) form tiles of 8 or 16.
@@ -20,8 +20,8 @@
 //
 // Short caches of few sequences (a token's latency) take one launch: a cluster
 // of kCluster blocks shares a run, and joins its parts through the blocks'
-// shared memory.  One token over 4,896 keys, 4 K/V heads of 64: 7.6 us, with the
-// line and its join 10.7.
+// shared memory.  One token over 4,896 keys, 4 K/V heads of 64: 6.8 us (with
+// blocks of three warps 7.6, and then with the line and its join 10.7).
 //
 // Inside a share the block's warps take turns of keys in round robin, each
 // with its own copies in flight (cp.async into a ring of its own: no barrier
@@ -138,7 +138,10 @@ template <int DIM, int NB>
 struct Codes {
     static constexpr bool kE2m1 = true;
     static constexpr int DP = DIM <= 64 ? 64 : 128;
-    static constexpr int kTurn = 32, kWarps = 3, kStages = 3, kBlocks = 4;
+    // Twelve warps an SM either way.  One row block: blocks of four, as a cluster's
+    // eight blocks are then the more warps (one token over 4,896 keys: 6.8 us, of
+    // three 7.6).  Two row blocks: of three (drafts, 24 caches: 69 us, of four 75).
+    static constexpr int kTurn = 32, kWarps = NB == 1 ? 4 : 3, kStages = 3, kBlocks = NB == 1 ? 3 : 4;
     static constexpr int kPitch = DP / 2;
     static constexpr int kGroups = DIM / 16;            // scale bytes a row
     static constexpr int kScales = 2 * kTurn * kPitch;  // where the scales begin; V's follow K's
@@ -999,9 +1002,9 @@ cudaError_t halves(int row_tile, int blocks, const Attn& p, cudaStream_t st)
 }  // namespace
 
 int64_t h3qk_pages::few_floats(int blocks, int rows, int dim) { return blocks == 1 ? 0 : 2 * blocks * part_floats(rows, dim); }
-int h3qk_pages::few_blocks(bool e2m1)
+int h3qk_pages::few_blocks(bool e2m1, int row_tile)
 {
-    const int an_sm = e2m1 ? Codes<128, 1>::kBlocks : Halves<128, 1>::kBlocks;
+    const int an_sm = !e2m1 ? Halves<128, 1>::kBlocks : row_tile == 8 ? Codes<128, 1>::kBlocks : Codes<128, 2>::kBlocks;
     return an_sm * h3qk_internal_sm_count();
 }
 
