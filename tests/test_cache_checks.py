@@ -269,3 +269,12 @@ def test_null_calls(no_gpu):
 
 def test_structs_are_packed_as_the_header_lays_them_out():
     assert len(pool()) == 192 and cache_module._ATTN.size == 128
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scales", "k_scale", "v_scale", "pages", "dtype"])
+def test_a_cache_stays_what_it_was_made_of(name):
+    c = Cache(*codes())
+    was = getattr(c, name)
+    with pytest.raises(AttributeError):
+        setattr(c, name, was)
+    assert getattr(c, name) is was

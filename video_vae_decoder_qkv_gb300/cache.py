@@ -47,10 +47,11 @@ class Cache:
     [pages, kv_heads, page_size, head_dim / 16], head_dim a multiple of 32 up
     to 128; a value is its e2m1 code (channel 2i in the low half of byte i)
     times its group's scale times ``k_scale`` (``v_scale``).  page_size is a
-    power of two from 16 on.  ``Cache.empty`` allocates one."""
+    power of two from 16 on.  ``Cache.empty`` allocates one.  What a cache is made
+    of stays: other tensors or scales are another Cache."""
 
     __slots__ = ("k", "v", "k_scales", "v_scales", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim",
-                 "dtype", "device", "_packed")
+                 "dtype", "device", "_head", "_tail")
 
     def __init__(self, k, v, k_scales=None, v_scales=None, *, k_scale: float = 1.0, v_scale: float = 1.0):
         if k.dim() != 4:
@@ -86,8 +87,14 @@ class Cache:
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.dtype, self.device = ("e2m1" if codes else k.dtype), k.device
-        self._packed = _POOL.pack(E2M1 if codes else _DTYPES[k.dtype], heads, dim, page, pages, k.data_ptr(), v.data_ptr(),
-                                  _ptr(k_scales) or 0, _ptr(v_scales) or 0, *strides, self.k_scale, self.v_scale)
+        # h3qk_cache but for the addresses, which each call takes anew
+        self._head = (E2M1 if codes else _DTYPES[k.dtype], heads, dim, page, pages)
+        self._tail = (*strides, self.k_scale, self.v_scale)
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "_tail"):
+            raise AttributeError(f"{name} of a Cache is fixed: make another Cache")
+        object.__setattr__(self, name, value)
 
     @staticmethod
     def _need(t, name, shape, dtype, dev):
@@ -138,8 +145,11 @@ def _pool(cache, block_table, kv_lens):
         raise ValueError("block_table must hold at least one sequence, and fewer than 2^30 rows of each")
     if kv_lens is None:
         raise ValueError("kv_lens is required")
-    return cache._packed + _TABLE.pack(batch, max_pages, block_table.data_ptr(), across if batch > 1 else 0,
-                                       _list(kv_lens, "kv_lens", batch, dev)), batch
+    ks, vs = cache.k_scales, cache.v_scales
+    packed = _POOL.pack(*cache._head, cache.k.data_ptr(), cache.v.data_ptr(), 0 if ks is None else ks.data_ptr(),
+                        0 if vs is None else vs.data_ptr(), *cache._tail)
+    return packed + _TABLE.pack(batch, max_pages, block_table.data_ptr(), across if batch > 1 else 0,
+                                _list(kv_lens, "kv_lens", batch, dev)), batch
 
 
 def _offsets(q_offsets, batch, tokens, dev):
