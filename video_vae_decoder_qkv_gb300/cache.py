@@ -31,6 +31,7 @@ block._SIGNATURES.update({
 
 # h3qk_cache and h3qk_cache_attn (include/h3qk.h), each packed in one step
 _POOL = struct.Struct("@4iq4P12q2f")
+_POINTERS = struct.Struct("@4P")  # _POOL's, which begin at byte 24
 _TABLE = struct.Struct("@2iPqP")
 _ATTN = struct.Struct("@4i2fq2P4q5PN")
 
@@ -88,8 +89,9 @@ class Cache:
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.dtype, self.device = ("e2m1" if codes else k.dtype), k.device
         # h3qk_cache but for the addresses, which each call takes anew
-        self._head = (E2M1 if codes else _DTYPES[k.dtype], heads, dim, page, pages)
-        self._tail = (*strides, self.k_scale, self.v_scale)
+        packed = _POOL.pack(E2M1 if codes else _DTYPES[k.dtype], heads, dim, page, pages, 0, 0, 0, 0, *strides, self.k_scale,
+                            self.v_scale)
+        self._head, self._tail = packed[:24], packed[24 + _POINTERS.size:]
 
     def __setattr__(self, name, value):
         if hasattr(self, "_tail"):
@@ -146,10 +148,11 @@ def _pool(cache, block_table, kv_lens):
     if kv_lens is None:
         raise ValueError("kv_lens is required")
     ks, vs = cache.k_scales, cache.v_scales
-    packed = _POOL.pack(*cache._head, cache.k.data_ptr(), cache.v.data_ptr(), 0 if ks is None else ks.data_ptr(),
-                        0 if vs is None else vs.data_ptr(), *cache._tail)
-    return packed + _TABLE.pack(batch, max_pages, block_table.data_ptr(), across if batch > 1 else 0,
-                                _list(kv_lens, "kv_lens", batch, dev)), batch
+    pointers = _POINTERS.pack(cache.k.data_ptr(), cache.v.data_ptr(), 0 if ks is None else ks.data_ptr(),
+                              0 if vs is None else vs.data_ptr())
+    table = _TABLE.pack(batch, max_pages, block_table.data_ptr(), across if batch > 1 else 0,
+                        _list(kv_lens, "kv_lens", batch, dev))
+    return cache._head + pointers + cache._tail + table, batch
 
 
 def _offsets(q_offsets, batch, tokens, dev):
