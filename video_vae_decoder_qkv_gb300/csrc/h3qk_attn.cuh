@@ -132,7 +132,9 @@ inline int64_t tiles_of(const Params& p, int64_t rows, int size)
 // hardware reciprocal, of the product of their y (1/x has half the rate of
 // 2^x, 16 a cycle and SM, and would bound the capped kernels; a reciprocal
 // from multiply-adds measured slower).
-// Which bends a call has is fixed at compile time.
+// Which bends a call has is fixed at compile time.  A NaN score makes all four
+// NaN, so they have to be of one row; APART: the scores at even places belong to
+// one row and those at odd places to another, and two share a reciprocal.
 //
 // The error is absolute in tanh, so a cap far above the scores costs them
 // digits: cap 2^-21.  Beyond kWideCap, where that passes 2^-11 (fp16 rounds p
@@ -179,7 +181,7 @@ __device__ __forceinline__ uint64_t tanh_series(uint64_t w)
 
 // The exponents of four raw scores (two pairs) at distances far, far + dir,
 // ...; with KEEP, also 1 - tanh^2 of a cap.
-template <int BENDS, bool KEEP>
+template <int BENDS, bool KEEP, bool APART = false>
 __device__ __forceinline__ void bend_four(uint64_t (&z)[2], const Bend& b, float far, float dir, uint64_t (&keep)[2])
 {
     using namespace h3qk_tc;
@@ -202,8 +204,13 @@ __device__ __forceinline__ void bend_four(uint64_t (&z)[2], const Bend& b, float
         }
         float p_lo, p_hi;
         unpair(p_lo, p_hi, mul_pair(y[0], y[1]));
-        const float all = rcp_fast(p_lo * p_hi);
-        const uint64_t both = pair(all * p_hi, all * p_lo);  // 1 / (y[0] y[1])
+        uint64_t both;  // 1 / (y[0] y[1])
+        if constexpr (APART) {
+            both = pair(rcp_fast(p_lo), rcp_fast(p_hi));
+        } else {
+            const float all = rcp_fast(p_lo * p_hi);
+            both = pair(all * p_hi, all * p_lo);
+        }
         r[0] = mul_pair(both, y[1]);
         r[1] = mul_pair(both, y[0]);
 #pragma unroll

@@ -635,23 +635,27 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                 });
             }
             // BENT: the scores' exponents.  The cap works on four scores at once, which
-            // come multiplied with `in`, so that one bend serves all rows.
+            // come multiplied with `in`, so that one bend serves them.
             if constexpr (BENT) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    float* v[4 * KB / 2][4];  // fours: of one row over two blocks of keys, or of both rows
+                    // Fours: of one row over two blocks of keys; or of both rows, whose reciprocals
+                    // then lie apart (a row's NaN, from its Q or a key that it sees, is not the other's).
+                    constexpr bool kApart = KB == 1;
+                    float* v[KB][4];
 #pragma unroll
                     for (int f = 0; f < KB; ++f)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[f][i] = KB == 2 ? &sc[i / 2][b][2 * (i & 1) + f] : &sc[0][b][2 * (i & 1) + i / 2];
+                        for (int i = 0; i < 4; ++i) v[f][i] = kApart ? &sc[0][b][i] : &sc[i / 2][b][2 * (i & 1) + f];
+                    auto row_of = [](int f, int i) { return kApart ? i & 1 : f; };
+                    auto key_of = [&](int i) { return j + (kApart ? 8 * (i / 2) : 16 * (i / 2) + 8 * (i & 1)) + g; };
 #pragma unroll
                     for (int f = 0; f < KB; ++f) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int h = KB == 2 ? f : i / 2, key = j + (KB == 2 ? 16 * (i / 2) : 0) + 8 * (i & 1) + g;
-                            // (hidden scores may be NaN, and four share a reciprocal)
-                            if (EDGE && key >= lim[b][h]) *v[f][i] = 0.0f;
+                            const int h = row_of(f, i);
+                            // (hidden scores may be NaN, and a row's share a reciprocal)
+                            if (EDGE && key_of(i) >= lim[b][h]) *v[f][i] = 0.0f;
                             *v[f][i] *= in[b][h];
                         }
                         if (p.cap > 0.0f) {
@@ -662,17 +666,17 @@ __global__ void __launch_bounds__(32 * T::kWarps, T::kBlocks) few_kernel(const _
                             bend.slope = 0.0f;
                             uint64_t z[2] = {pair(*v[f][0], *v[f][1]), pair(*v[f][2], *v[f][3])}, keep[2];
                             if (p.cap > h3qk_core::kWideCap)
-                                h3qk_core::bend_four<h3qk_core::kCapped | h3qk_core::kWide, false>(z, bend, 0.0f, 0.0f, keep);
+                                h3qk_core::bend_four<h3qk_core::kCapped | h3qk_core::kWide, false, kApart>(z, bend, 0.0f, 0.0f, keep);
                             else
-                                h3qk_core::bend_four<h3qk_core::kCapped, false>(z, bend, 0.0f, 0.0f, keep);
+                                h3qk_core::bend_four<h3qk_core::kCapped, false, kApart>(z, bend, 0.0f, 0.0f, keep);
                             unpair(*v[f][0], *v[f][1], z[0]);
                             unpair(*v[f][2], *v[f][3], z[1]);
                         }
                         if (p.slopes)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const int h = KB == 2 ? f : i / 2, key = j + (KB == 2 ? 16 * (i / 2) : 0) + 8 * (i & 1) + g;
-                                *v[f][i] = fmaf(-slope[b][h], fabsf(static_cast<float>(at[b][h] - key)), *v[f][i]);
+                                const int h = row_of(f, i);
+                                *v[f][i] = fmaf(-slope[b][h], fabsf(static_cast<float>(at[b][h] - key_of(i))), *v[f][i]);
                             }
                     }
                 }
