@@ -1,0 +1,56 @@
+"""The paged cache's operators, without a GPU, where one call could spoil the
+next or a value or layout lies at the edge of what is allowed."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from video_vae_decoder_qkv_gb300 import Cache, attention, block, cache as cache_module, cache_attention  # noqa: E402
+
+F16, I32 = torch.float16, torch.int32
+
+
+@pytest.fixture
+def packed_calls(monkeypatch):
+    """Calls of the binding go into a list, and no further."""
+    passed = []
+    monkeypatch.setattr(block, "_sizes", {})
+    monkeypatch.setattr(block, "_call", lambda name, dev, *args: passed.append(args))
+    monkeypatch.setattr(block, "_stream", lambda dev: None)
+    monkeypatch.setattr(cache_module, "_stream", lambda dev: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    return passed
+
+
+BAD_BENDS = [dict(softcap=-1.0), dict(softcap=math.nan), dict(softcap=math.inf), dict(softcap=1e-50), dict(softcap=1e39),
+             dict(scale=math.inf), dict(scale=math.nan), dict(scale=-1.0), dict(scale=0.0), dict(scale=1e-50),
+             dict(scale=1e39)]
+
+
+@pytest.mark.parametrize("bad", BAD_BENDS, ids=str)
+def test_a_refused_call_leaves_the_next_ones_workspace(packed_calls, bad):
+    """Refused before a size is kept for it: calls of the same sizes get the workspace that the library asks for."""
+    cache = Cache.empty(64, 8, 128, device="cpu", dtype=F16)
+    table, lens = torch.zeros(4, 256, dtype=I32), torch.ones(4, dtype=I32)
+    for rows in (4, 400):
+        q = torch.empty(rows, 40, 128, dtype=F16)
+        with pytest.raises(ValueError):
+            cache_attention(q, cache, table, lens, **bad)
+        assert not packed_calls
+        for good in (dict(), dict(softcap=3.0), dict(scale=0.5)):
+            cache_attention(q, cache, table, lens, **good)
+            pool, call, _ = packed_calls.pop()
+            want = block._fn("h3qk_cache_attention_workspace_bytes")(pool, call)
+            assert want > 0 and cache_module._ATTN.unpack(call)[-1] == want
+
+
+@pytest.mark.parametrize("bad", BAD_BENDS, ids=str)
+def test_a_refused_call_leaves_the_next_ones_workspace_dense(packed_calls, bad):
+    q, k = torch.empty(1, 16, 1, 64, dtype=F16), torch.empty(1, 16, 4896, 64, dtype=F16)
+    with pytest.raises(ValueError):
+        attention(q, k, k, **bad)
+    attention(q, k, k)
+    packed, _ = packed_calls.pop()
+    want = block._fn("h3qk_attention_workspace_bytes")(packed)
+    assert want > 0 and block._ATTN.unpack(packed)[28] == want

@@ -314,14 +314,26 @@ def _need_lens(t, name, n, dev):
     return t.data_ptr()
 
 
-def _attn_common(q, k, v, scale, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts):
+# What binary32 does not round to zero or infinity lies between these.
+_F32_LOW, _F32_HIGH = 2.0 ** -150, 2.0 ** 128 - 2.0 ** 103
+
+
+def _need_bend(scale, softcap):
+    """Refuses what the library would refuse, or what binary32 makes a zero, which it reads as a default.  The size
+    of a workspace is kept for calls that differ in these only, so none is asked with a value that is refused."""
+    if scale is not None and not _F32_LOW < scale < _F32_HIGH:
+        raise ValueError(f"scale must be positive and finite (in binary32), got {scale}")
+    if softcap != 0.0 and not _F32_LOW < softcap < _F32_HIGH:
+        raise ValueError(f"softcap must be 0, or positive and finite (in binary32), got {softcap}")
+
+
+def _attn_common(q, k, v, scale, softcap, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts):
     """Checks shared by both directions: (batch, heads, kv_heads, q_rows, kv_rows, dim, docs, strides, pointers)."""
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("q must be float16 or bfloat16")
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must be [batch, heads, rows, head_dim]")
-    if scale is not None and not scale > 0:
-        raise ValueError(f"scale must be positive, got {scale}")
+    _need_bend(scale, softcap)
     dev = q.device
     batch, heads, sq, dim = q.shape
     _, kv_heads, sk, _ = k.shape
@@ -377,7 +389,7 @@ def attention(q, k, v, *, scale: float | None = None, softcap: float = 0.0, slop
     (tokens produced one by one) splits the keys over the GPU and joins the
     parts (h3qk_attention)."""
     batch, heads, kv_heads, sq, sk, dim, docs, strides, lists = _attn_common(
-        q, k, v, scale, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
+        q, k, v, scale, softcap, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
     dev = q.device
     if out is None:
         out = torch.empty_like(q)
@@ -418,7 +430,7 @@ def attention_backward(grad_out, q, k, v, out, lse, *, scale: float | None = Non
     gives the same bits every time.  The slopes get no gradient
     (h3qk_attention_backward)."""
     batch, heads, kv_heads, sq, sk, dim, docs, strides, lists = _attn_common(
-        q, k, v, scale, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
+        q, k, v, scale, softcap, slopes, prefix_lens, doc_offsets, q_lens, kv_lens, q_starts)
     grad_out = _spread(grad_out)
     dev = q.device
     row, key = (batch, heads, sq, dim), (batch, kv_heads, sk, dim)

@@ -17,7 +17,7 @@ import struct
 import torch
 
 from . import block, h3qk
-from .block import _DTYPES, _need_lens, _on_stream, _stream, _workspace
+from .block import _DTYPES, _need_bend, _need_lens, _on_stream, _stream, _workspace
 from .h3qk import _need, _ptr
 
 E2M1 = 5
@@ -264,8 +264,7 @@ def cache_attention(q, cache, block_table, kv_lens, *, q_offsets=None, max_rows:
         raise TypeError(f"q must be {cache.dtype} as the cache, got {dtype}")
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
-    if scale is not None and not scale > 0:
-        raise ValueError(f"scale must be positive, got {scale}")
+    _need_bend(scale, softcap)
     if max_rows is not None and max_rows < 1:
         raise ValueError(f"max_rows must be positive, got {max_rows}")
     if prefix_lens is not None and not causal:
