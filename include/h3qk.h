@@ -630,7 +630,8 @@ h3qk_status h3qk_cache_append(const h3qk_cache* cache, const void* qkv, const fl
 /*
  * h3qk_cache_attention: h3qk_attention's formula with the keys and values of
  * a cache.  Row i of sequence b stands at position kv_lens[b] - n_b + i and
- * sees its kv_lens[b] keys; with causal, of those the ones up to its own
+ * sees its kv_lens[b] keys, of a longer sequence those that its table has room
+ * for (a negative length is 0); with causal, of those the ones up to its own
  * position and the first prefix_lens[b].  Rows that see no key get out = 0 and
  * lse = -infinity; rows of no sequence, and rows past max_rows of one, are left
  * as they were.  A non-finite key reaches the rows that see it, a non-finite

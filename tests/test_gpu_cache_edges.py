@@ -1,5 +1,6 @@
 """The paged cache's operators where their documentation allows more than
-ordinary calls make: rows that are not finite beside rows that are."""
+ordinary calls make: rows that are not finite beside rows that are, and
+sequences that are longer than their table."""
 import math
 
 import block_util as bu
@@ -58,3 +59,29 @@ def test_nan_row_reaches_no_other(fmt, dtype, rows, group, softcap):
     assert bool(torch.isnan(out[spoilt]).all()) and bool(torch.isnan(lse.t()[spoilt]).all())
     for got, name in ((out, "out"), (lse.t(), "lse")):
         bu.assert_within(got[~spoilt], want[name][~spoilt], want[name + "_bound"][~spoilt], name)
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("rows,past", [(2, 1), (4, 2), (3, 900), (40, 2), (300, 37), (40, 2 ** 31 - 1 - 320)])
+@pytest.mark.parametrize("fmt", ["e2m1", BF16])
+def test_rows_of_sequences_past_their_table_keep_their_positions(fmt, rows, past, slopes):
+    """Row i stands at kv_lens - n + i, as the append places it, whatever the table has room for."""
+    if slopes and past > 1000:
+        pytest.skip("scores less a slope times 2^31 have no digits left")
+    room, heads = 320, 4
+    cache, table, kv_lens = cu.build([room, 100], 2, 64, 64, fmt)
+    kv_lens[0] = room + past
+    q = torch.randn(2 * rows, heads, 64, device="cuda").to(BF16)
+    sl = torch.rand(heads, device="cuda") * 0.2 if slopes else None
+    out, lse = cache_attention(q, cache, table, kv_lens, slopes=sl)
+    k_all, v_all = cu.values(cache)
+    for b, keys, start in ((0, room, room + past - rows), (1, 100, 100 - rows)):
+        at = slice(b * rows, (b + 1) * rows)
+        # (where a row stands past the keys, what it sees is all of them)
+        vis, dist = bu.visible(rows, keys, 1, True, q_starts=[start])
+        want = bu.attention(q[at].transpose(0, 1)[None], cu.rows_of(k_all, table[b], keys)[None],
+                            cu.rows_of(v_all, table[b], keys)[None], vis, dist, slopes=sl)
+        bu.assert_within(out[at].transpose(0, 1), want["out"][0], want["out_bound"][0], "out")
+        seen = ~torch.isneginf(want["lse"][0])
+        assert torch.equal(~torch.isneginf(lse[:, at]), seen)
+        bu.assert_within(lse[:, at][seen], want["lse"][0][seen], want["lse_bound"][0][seen], "lse")

@@ -43,8 +43,9 @@ __device__ __forceinline__ Sequence sequence_of(const Attn& p, int item)
     s.first = r.first;
     s.n = min(r.n, p.max_rows);
     s.keys = keys_of(p.c, item);
-    // (rows that max_rows hides are still the last ones of the cache)
-    s.start = s.keys - r.n;
+    // The length as it is given, beyond the table too, says where the rows stand
+    // (those that max_rows hides among them).  start + i stays below it.
+    s.start = max(__ldg(p.c.kv_lens + item), 0) - r.n;
     s.prefix = p.prefix_lens ? max(__ldg(p.prefix_lens + item), 0) : 0;
     return s;
 }
