@@ -10,7 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from video_vae_decoder_qkv_gb300 import cache_attention  # noqa: E402
+from video_vae_decoder_qkv_gb300 import cache_append, cache_attention, prepare  # noqa: E402
 
 F16, BF16 = torch.float16, torch.bfloat16
 
@@ -85,3 +85,18 @@ def test_rows_of_sequences_past_their_table_keep_their_positions(fmt, rows, past
         seen = ~torch.isneginf(want["lse"][0])
         assert torch.equal(~torch.isneginf(lse[:, at]), seen)
         bu.assert_within(lse[:, at][seen], want["lse"][0][seen], want["lse_bound"][0][seen], "lse")
+
+
+@pytest.mark.parametrize("length", [2 ** 30 + 5, 2 ** 31 - 1])
+def test_places_past_2_30_turn_q_by_their_own_angle(length):
+    cache, table, kv_lens = cu.build([64], 2, 64, 64, BF16)
+    kv_lens[0] = length
+    qkv = torch.randn(3, 6 * 64, device="cuda").to(BF16)
+    w = torch.rand(64, device="cuda") + 0.5
+    was = cache.k.clone(), cache.v.clone()
+    got = cache_append(qkv, w, w, cache, table, kv_lens, heads=2, rotary_dim=64)
+    pos = torch.arange(length - 3, length, device="cuda").int()[:, None]
+    want = prepare(qkv, w, w, pos, heads=2, head_dim=64, rotary_dim=64, n_axes=1, out_layout="token_major")[0]
+    assert torch.equal(got.flatten(), want.flatten())
+    for now, then in zip((cache.k, cache.v), was):
+        assert torch.equal(now.view(torch.int16), then.view(torch.int16))

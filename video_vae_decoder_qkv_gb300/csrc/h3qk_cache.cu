@@ -140,9 +140,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const __gr
         for (int u = 0; u < kAhead - 1; ++u) fetch(h0 + u);
         int at = 0, page = -1;
         if (row) {
-            // (a length of any size: the difference is taken in 64 bits)
+            // (places stay below the length; a negative one's difference is taken in 64 bits)
             const int64_t place = static_cast<int64_t>(__ldg(c.kv_lens + item)) - n + (r - start);
-            at = static_cast<int>(min(max(place, -(int64_t{1} << 30)), int64_t{1} << 30));
+            at = static_cast<int>(max(place, static_cast<int64_t>(INT32_MIN)));
             if (at >= 0) page = page_of(c, c.table + item * c.table_stride, at);
         }
         const int in_page = at & ((1 << c.page_shift) - 1);
