@@ -594,7 +594,7 @@ typedef struct h3qk_cache {
     void *k, *v;             /* [pages, kv_heads, page_size, head_dim], or codes [..., head_dim / 2]; 16-byte aligned */
     void *k_scales, *v_scales;  /* E2M1 only: e4m3 [pages, kv_heads, page_size, head_dim / 16]; 16-byte aligned */
     h3qk_strides k_strides, v_strides, k_scale_strides, v_scale_strides;  /* item: from page to page; below 2^36 bytes */
-    float k_scale, v_scale;  /* E2M1 only: finite, > 0; 0 means 1 */
+    float k_scale, v_scale;  /* E2M1 only: 2^-117 to 2^117; 0 means 1 */
     int32_t batch;           /* sequences, 1 to 65535 */
     int32_t max_pages;       /* entries of a sequence in the table; max_pages * page_size < 2^30 */
     const int32_t* block_table;  /* [batch, max_pages], sequences table_stride entries apart */

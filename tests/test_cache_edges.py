@@ -6,7 +6,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from video_vae_decoder_qkv_gb300 import Cache, attention, block, cache as cache_module, cache_attention  # noqa: E402
+import test_cache_checks as checks  # noqa: E402
+from test_cache_checks import no_gpu  # noqa: E402, F401
+from video_vae_decoder_qkv_gb300 import Cache, attention, block, cache as cache_module, cache_attention, h3qk  # noqa: E402
 
 F16, I32 = torch.float16, torch.int32
 
@@ -54,3 +56,21 @@ def test_a_refused_call_leaves_the_next_ones_workspace_dense(packed_calls, bad):
     packed, _ = packed_calls.pop()
     want = block._fn("h3qk_attention_workspace_bytes")(packed)
     assert want > 0 and block._ATTN.unpack(packed)[28] == want
+
+
+@pytest.mark.parametrize("scale", [1e-50, 2.0 ** -118, 2.0 ** 118, 1e39, -1.0])
+def test_tensor_scales_that_the_rounding_cannot_take_are_refused(scale):
+    for name in ("k_scale", "v_scale"):
+        with pytest.raises(ValueError, match=name):
+            Cache(*checks.codes(), **{name: scale})
+        with pytest.raises(ValueError, match=name):
+            Cache.empty(4, 2, 64, dtype="e2m1", device="cpu", **{name: scale})
+
+
+@pytest.mark.parametrize("scale,want", [(2.0 ** -149, h3qk.ERR_INVALID_ARG), (2.0 ** -118, h3qk.ERR_INVALID_ARG),
+                                        (2.0 ** 118, h3qk.ERR_INVALID_ARG), (2.0 ** -117, h3qk.ERR_CUDA),
+                                        (2.0 ** 117, h3qk.ERR_CUDA), (0.0, h3qk.ERR_CUDA)])
+def test_tensor_scales_of_the_library(no_gpu, scale, want):  # noqa: F811
+    for name in ("k_scale", "v_scale"):
+        kw = {**checks.E2M1, name: scale}
+        assert checks.c_append(**kw) == want and checks.c_attend(**kw) == want and checks.c_read(**kw) == want

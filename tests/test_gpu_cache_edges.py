@@ -1,16 +1,17 @@
 """The paged cache's operators where their documentation allows more than
-ordinary calls make: rows that are not finite beside rows that are, and
-sequences that are longer than their table."""
+ordinary calls make: rows that are not finite beside rows that are,
+sequences that are longer than their table, and the largest and smallest scales."""
 import math
 
 import block_util as bu
 import cache_util as cu
 import pytest
+from test_gpu_cache_append import check
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from video_vae_decoder_qkv_gb300 import cache_append, cache_attention, prepare  # noqa: E402
+from video_vae_decoder_qkv_gb300 import cache_append, cache_attention, cache_read, prepare  # noqa: E402
 
 F16, BF16 = torch.float16, torch.bfloat16
 
@@ -100,3 +101,15 @@ def test_places_past_2_30_turn_q_by_their_own_angle(length):
     assert torch.equal(got.flatten(), want.flatten())
     for now, then in zip((cache.k, cache.v), was):
         assert torch.equal(now.view(torch.int16), then.view(torch.int16))
+
+
+@pytest.mark.parametrize("log2", [-117, 117])
+def test_append_with_the_largest_and_smallest_tensor_scales(log2):
+    """Values of the scale's size get their codes, and zeros stay zeros."""
+    def edit(qkv):
+        qkv[:, 6 * 64:] *= 2.0 ** log2  # V of two heads, after 4 + 2 of Q and K
+        qkv[3, 6 * 64:] = 0
+
+    cache, table, lens = check([(9, 20), (40, 41)], BF16, "e2m1", 4, 2, 64, 64, k_scale=1.0, v_scale=2.0 ** log2, edit=edit)
+    _, v = cache_read(cache, table, lens, rows=20)
+    assert bool((v[0, :, 14] == 0).all()) and bool(v[0, :, 15].any())

@@ -11,7 +11,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 import struct
 
 import torch
@@ -47,7 +46,7 @@ class Cache:
     page_size, head_dim / 2] and ``k_scales``, ``v_scales`` float8_e4m3fn
     [pages, kv_heads, page_size, head_dim / 16], head_dim a multiple of 32 up
     to 128; a value is its e2m1 code (channel 2i in the low half of byte i)
-    times its group's scale times ``k_scale`` (``v_scale``).  page_size is a
+    times its group's scale times ``k_scale`` (``v_scale``; 2^-117 to 2^117).  page_size is a
     power of two from 16 on.  ``Cache.empty`` allocates one.  What a cache is made
     of stays: other tensors or scales are another Cache."""
 
@@ -70,8 +69,8 @@ class Cache:
         if codes != (k_scales is not None) or codes != (v_scales is not None):
             raise ValueError("k_scales and v_scales belong to codes, and only to them")
         for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if not (s > 0 and math.isfinite(s)):
-                raise ValueError(f"{name} must be positive and finite, got {s}")
+            if not 2.0 ** -117 <= s <= 2.0 ** 117:
+                raise ValueError(f"{name} must be from 2^-117 to 2^117, got {s}")
             if not codes and s != 1.0:
                 raise ValueError(f"{name} belongs to codes")
         strides = []

@@ -1,6 +1,6 @@
 // The paged cache: the checks of a pool, appending prepared rows, and reading
 // rows back.  Layout and 4-bit format are described at h3qk_cache in h3qk.h.
-#include <cmath>
+#include <utility>
 
 #include "h3qk_cache_host.h"
 #include "h3qk_kernels.cuh"
@@ -429,8 +429,10 @@ h3qk_status h3qk_pages::check_pool(const h3qk_cache* cache, bool written, Pool* 
     if (stride < c.max_pages || stride > (INT64_C(1) << 40)) return H3QK_ERR_INVALID_ARG;
     if (!c.kv_lens || (!c.block_table && c.max_pages > 0)) return H3QK_ERR_INVALID_ARG;
     if (!aligned(c.kv_lens, 4) || !aligned(c.block_table, 4)) return H3QK_ERR_MISALIGNED;
-    if (!(c.k_scale >= 0.0f) || !std::isfinite(c.k_scale) || !(c.v_scale >= 0.0f) || !std::isfinite(c.v_scale))
-        return H3QK_ERR_INVALID_ARG;
+    // Between these every step of the rounding is a normal binary32 number: the smallest
+    // group scale times k_scale is 2^-126, and 1 / (6 k_scale) well above that.
+    for (const float ts : {c.k_scale, c.v_scale})
+        if (ts != 0.0f && !(ts >= 0x1p-117f && ts <= 0x1p117f)) return H3QK_ERR_INVALID_ARG;
     if (!e2m1 && ((c.k_scale != 0.0f && c.k_scale != 1.0f) || (c.v_scale != 0.0f && c.v_scale != 1.0f) || c.k_scales ||
                   c.v_scales))
         return H3QK_ERR_INVALID_ARG;
