@@ -113,3 +113,17 @@ def test_append_with_the_largest_and_smallest_tensor_scales(log2):
     cache, table, lens = check([(9, 20), (40, 41)], BF16, "e2m1", 4, 2, 64, 64, k_scale=1.0, v_scale=2.0 ** log2, edit=edit)
     _, v = cache_read(cache, table, lens, rows=20)
     assert bool((v[0, :, 14] == 0).all()) and bool(v[0, :, 15].any())
+
+
+@pytest.mark.parametrize("rows", [3, 70])
+@pytest.mark.parametrize("exponent,softcap", [(120, 1e-8), (100, 1e-20), (0, 1e-40)])
+@pytest.mark.parametrize("fmt", ["e2m1", BF16])
+def test_caps_far_below_the_scores(fmt, exponent, softcap, rows):
+    """All that a row sees lies within +-softcap of 0, so that it weighs the same (to 2e-8, well below the bound's 2^-18)."""
+    lens = [100, 70]
+    cache, table, kv_lens = cu.build(lens, 1, 64, 64, fmt)
+    q = (torch.randn(2 * rows, 2, 64, device="cuda") * 2.0 ** exponent).to(BF16)
+    out, lse = cache_attention(q, cache, table, kv_lens, softcap=softcap)
+    want, _ = cu.attention(torch.zeros_like(q), cache, table, lens, [0, rows, 2 * rows])
+    bu.assert_within(out, want["out"], want["out_bound"], "out")
+    bu.assert_within(lse.t(), want["lse"], want["lse_bound"], "lse")

@@ -61,7 +61,8 @@ __device__ __forceinline__ h3qk_core::Bend bend_of(const Attn& p, int head, floa
     Bend b;
     // (positive and finite, so that it keeps a hidden score's -infinity)
     b.plain = fminf(fmaxf(p.scale * kLog2e * raw, 0x1p-126f), 3.0e38f);
-    b.in = p.cap > 0.0f ? fminf(p.scale * 2.0f * kLog2e / p.cap, 3.0e38f) * raw : b.plain;
+    // (finite before and after: an infinite factor would make a score of 0 NaN)
+    b.in = p.cap > 0.0f ? fminf(fminf(p.scale * 2.0f * kLog2e / p.cap, 3.0e38f) * raw, 3.0e38f) : b.plain;
     b.cap = p.cap * kLog2e;
     b.slope = p.slopes ? __ldg(p.slopes + head) * kLog2e : 0.0f;
     return b;
