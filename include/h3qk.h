@@ -620,8 +620,9 @@ typedef struct h3qk_cache {
  * bit.  A place belongs to one row: which of two rows that name the same place
  * is kept is not defined, and with E2M1 neither may be.  opts' batch,
  * out_layout, valid_lens, static_scales, workspace and sat_counts are ignored.
- * No output may overlap an input or another output (K and V may share pages of
- * a pool).  Errors and asynchrony as for h3qk_prepare.
+ * No output may overlap an input or another output, whole spans counted; but K,
+ * V and their scales may lie between one another's pages, heads or rows, where
+ * they step alike.  Errors and asynchrony as for h3qk_prepare.
  */
 h3qk_status h3qk_cache_append(const h3qk_cache* cache, const void* qkv, const float* norm_wq, const float* norm_wk,
                               const int32_t* positions, int64_t tokens, int32_t heads, int32_t rotary_dim,

@@ -1,6 +1,7 @@
 """The paged cache's operators, without a GPU, where one call could spoil the
 next or a value or layout lies at the edge of what is allowed."""
 import math
+import random
 
 import pytest
 
@@ -74,3 +75,57 @@ def test_tensor_scales_of_the_library(no_gpu, scale, want):  # noqa: F811
     for name in ("k_scale", "v_scale"):
         kw = {**checks.E2M1, name: scale}
         assert checks.c_append(**kw) == want and checks.c_attend(**kw) == want and checks.c_read(**kw) == want
+
+
+A = checks.A
+BOTH_IN_A_ROW = dict(v=A + 256, k_st=(8192, 64, 256), v_st=(8192, 64, 256))  # [pages, page_size, 2, kv_heads, head_dim]
+CODES_IN_A_PAGE = dict(checks.E2M1, v=A + 1024, k_st=(4096, 2048, 32), v_st=(4096, 2048, 32))  # [pages, kv_heads, 2, ...]
+ALL_OF_A_HEAD = dict(checks.E2M1, v=A + 1024, ks=A + 2048, vs=A + 2176, k_st=(4608, 2304, 32), v_st=(4608, 2304, 32),
+                     ks_st=(4608, 2304, 4), vs_st=(4608, 2304, 4))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (BOTH_IN_A_ROW, h3qk.ERR_CUDA), ({**BOTH_IN_A_ROW, "v": A + 128}, h3qk.ERR_ALIAS),
+    ({**BOTH_IN_A_ROW, "v": A + 384}, h3qk.ERR_ALIAS), ({**BOTH_IN_A_ROW, "pages": 1}, h3qk.ERR_CUDA),
+    ({**BOTH_IN_A_ROW, "v": A - 256}, h3qk.ERR_CUDA), ({**BOTH_IN_A_ROW, "v": A + 512 + 256}, h3qk.ERR_CUDA),
+    ({**BOTH_IN_A_ROW, "v": A + 512}, h3qk.ERR_ALIAS), ({**BOTH_IN_A_ROW, "v_st": (8192, 64, 128)}, h3qk.ERR_ALIAS),
+    (CODES_IN_A_PAGE, h3qk.ERR_CUDA), ({**CODES_IN_A_PAGE, "v": A + 512}, h3qk.ERR_ALIAS),
+    (ALL_OF_A_HEAD, h3qk.ERR_CUDA), ({**ALL_OF_A_HEAD, "ks": A + 2048 - 16}, h3qk.ERR_ALIAS),
+    ({**ALL_OF_A_HEAD, "vs": A + 2176 + 16}, h3qk.ERR_ALIAS),
+])
+def test_pools_whose_parts_lie_between_one_another(no_gpu, kw, want):  # noqa: F811
+    assert checks.c_append(**kw) == want
+    assert checks.c_attend(**kw) == h3qk.ERR_CUDA  # (reading may overlap as it likes)
+
+
+def test_no_overlap_of_a_written_pool_is_missed(no_gpu):  # noqa: F811
+    """Small pools of random strides, against the bytes that their rows have, counted one by one."""
+    rng = random.Random(1)
+    taken = 0
+    for _ in range(3000):
+        kv, pages, page = rng.choice((1, 2, 3)), rng.choice((1, 2, 3)), 16
+        def strides():
+            order, step, got = [("head", kv), ("row", page), ("item", pages)], 8, {}
+            rng.shuffle(order)
+            for name, n in order:
+                got[name] = step * rng.choice((1, 1, 2, 3))
+                step = got[name] * n
+            return got["item"], got["head"], got["row"]
+
+        k_st = strides()
+        v_st = k_st if rng.random() < 0.7 else strides()
+        apart = 16 * rng.randrange(-60, 60)
+        every = []
+        for st in (k_st, v_st):
+            every.append([2 * (p * st[0] + h * st[1] + r * st[2]) for p in range(pages) for h in range(kv) for r in range(page)])
+        k, v = ({at // 16 + off for at in rows} for rows, off in zip(every, (0, apart // 16)))
+        apart_rows = len(k) == len(every[0]) and len(v) == len(every[1]) and not k & v
+        got = checks.c_append(dict(heads=kv, rotary=0), kv_heads=kv, pages=pages, page_size=page, head_dim=8, k_st=k_st,
+                              v_st=v_st, v=A + apart)
+        assert got in (h3qk.ERR_ALIAS, h3qk.ERR_CUDA)
+        if got == h3qk.ERR_CUDA:
+            assert apart_rows, (kv, pages, k_st, v_st, apart)
+            taken += 1
+        elif k_st == v_st:
+            assert not apart_rows, (kv, pages, k_st, v_st, apart)
+    assert taken > 300

@@ -11,7 +11,7 @@ from test_gpu_cache_append import check
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from video_vae_decoder_qkv_gb300 import cache_append, cache_attention, cache_read, prepare  # noqa: E402
+from video_vae_decoder_qkv_gb300 import Cache, cache_append, cache_attention, cache_read, prepare  # noqa: E402
 
 F16, BF16 = torch.float16, torch.bfloat16
 
@@ -127,3 +127,22 @@ def test_caps_far_below_the_scores(fmt, exponent, softcap, rows):
     want, _ = cu.attention(torch.zeros_like(q), cache, table, lens, [0, rows, 2 * rows])
     bu.assert_within(out, want["out"], want["out_bound"], "out")
     bu.assert_within(lse.t(), want["lse"], want["lse_bound"], "lse")
+
+
+@pytest.mark.parametrize("seqs", [[(9, 20), (40, 41)], [(1, 64)]])
+def test_append_to_a_pool_with_k_and_v_beside_each_other_in_a_row(monkeypatch, seqs):
+    """[pages, page_size, 2, kv_heads, head_dim]"""
+    plain = cu.build
+
+    def build(*args, **kw):
+        cache, table, lens = plain(*args, **kw)
+        both = torch.stack([cache.k, cache.v]).permute(1, 3, 0, 2, 4).contiguous()
+        return Cache(*(both[:, :, i].transpose(1, 2) for i in (0, 1))), table, lens
+
+    monkeypatch.setattr(cu, "build", build)
+    cache, table, lens = check(seqs, BF16, BF16, 4, 2, 72, 32)
+    assert cache.k.stride() == (32 * 2 * 2 * 72, 72, 2 * 2 * 72, 1)
+    q = torch.randn(len(seqs), 4, 72, device="cuda").to(BF16)
+    out, _ = cache_attention(q, cache, table, lens)
+    want, _ = cu.attention(q, cache, table, [s[1] for s in seqs], list(range(len(seqs) + 1)))
+    bu.assert_within(out, want["out"], want["out_bound"], "out")

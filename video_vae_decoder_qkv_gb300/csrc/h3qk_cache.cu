@@ -1,7 +1,5 @@
 // The paged cache: the checks of a pool, appending prepared rows, and reading
 // rows back.  Layout and 4-bit format are described at h3qk_cache in h3qk.h.
-#include <utility>
-
 #include "h3qk_cache_host.h"
 #include "h3qk_kernels.cuh"
 
@@ -348,14 +346,29 @@ cudaError_t launch_append(int P, bool e2m1, const AppendArgs& a, int blocks, cud
     return cudaGetLastError();
 }
 
-// The bytes of one pool tensor, from its first to its last.
+// The bytes of one pool tensor: rows of row_bytes, their steps in bytes.
+struct Step {
+    int64_t step, n;
+};
 struct Span {
     int64_t page, head, row, row_bytes;
-    int64_t in_page(const h3qk_cache& c) const
+    int64_t all(const h3qk_cache& c) const  // from its first byte to its last
     {
-        return (c.kv_heads - 1) * head + (c.page_size - 1) * row + row_bytes;
+        return c.pages ? (c.pages - 1) * page + (c.kv_heads - 1) * head + (c.page_size - 1) * row + row_bytes : 0;
     }
-    int64_t all(const h3qk_cache& c) const { return c.pages ? (c.pages - 1) * page + in_page(c) : 0; }
+    // Its dimensions of more than one entry, the widest step first.
+    int steps(const h3qk_cache& c, Step (&d)[3]) const
+    {
+        const Step from[3] = {{page, c.pages}, {head, c.kv_heads}, {row, c.page_size}};
+        int n = 0;
+        for (const Step& s : from) {
+            if (s.n == 1) continue;
+            int at = n++;
+            for (; at > 0 && d[at - 1].step < s.step; --at) d[at] = d[at - 1];
+            d[at] = s;
+        }
+        return n;
+    }
 };
 
 // Strides of one tensor in bytes; those of single-entry dimensions are replaced by ones that fit.
@@ -379,36 +392,50 @@ h3qk_status check_strides(const h3qk_cache& c, const void* data, h3qk_strides s,
     return span > 1e15 ? H3QK_ERR_INVALID_ARG : H3QK_OK;
 }
 
-// Rows of a tensor that is written may not run into one another: ordered by
-// stride, each dimension steps over the one before it.
+// Rows of a tensor that is written may not run into one another: each
+// dimension steps over the ones inside it.
 bool disjoint_rows(const Span& s, const h3qk_cache& c)
 {
-    int64_t step[3] = {s.row, s.head, s.page}, n[3] = {c.page_size, c.kv_heads, c.pages};
-    for (int i = 0; i < 2; ++i)
-        for (int k = 0; k < 2 - i; ++k)
-            if (step[k] > step[k + 1]) {
-                std::swap(step[k], step[k + 1]);
-                std::swap(n[k], n[k + 1]);
-            }
+    Step d[3];
     int64_t reach = s.row_bytes;
-    for (int i = 0; i < 3; ++i) {
-        if (n[i] == 1) continue;
-        if (step[i] < reach) return false;
-        reach += step[i] * (n[i] - 1);
+    for (int i = s.steps(c, d) - 1; i >= 0; --i) {
+        if (d[i].step < reach) return false;
+        reach += d[i].step * (d[i].n - 1);
     }
     return true;
 }
 
-// Whether two tensors of a pool share bytes.  Those of one page may lie
-// between the pages of the other: the same stride, and a page's part of each
-// inside the other's gap.
-bool collide(const uint8_t* a, const Span& x, const uint8_t* b, const Span& y, const h3qk_cache& c)
+int64_t reach_of(const Step* d, int n, int64_t row_bytes)
 {
-    if (!overlap(range_of(a, x.all(c)), range_of(b, y.all(c)))) return false;
-    if (x.page != y.page) return true;
-    if (a > b) return collide(b, y, a, x, c);
-    const int64_t apart = (b - a) % x.page;
-    return apart < x.in_page(c) || apart + y.in_page(c) > x.page;
+    for (int i = 0; i < n; ++i) row_bytes += d[i].step * (d[i].n - 1);
+    return row_bytes;
+}
+
+// Whether two tensors of a pool, the second `apart` bytes behind the first, share
+// bytes; each is disjoint in itself.  Where their widest steps are the same,
+// what lies inside one may lie between the steps of the other (K and V of a
+// page, of a head or of a row beside each other): the few pairs of their blocks
+// that could meet are looked at.  Else their whole extents count.
+bool collide(const Step* x, int nx, int64_t x_row, const Step* y, int ny, int64_t y_row, int64_t apart)
+{
+    if (apart >= reach_of(x, nx, x_row) || -apart >= reach_of(y, ny, y_row)) return false;
+    if (nx == 0 || ny == 0 || x->step != y->step || x->n != y->n) return true;
+    const int64_t step = x->step, in_x = reach_of(x + 1, nx - 1, x_row), in_y = reach_of(y + 1, ny - 1, y_row);
+    // block i + t of the second starts apart + t step behind block i of the first
+    int64_t first = (-in_y - apart) / step - 1, last = (in_x - apart) / step + 1;
+    if (first < 1 - x->n) first = 1 - x->n;
+    if (last > x->n - 1) last = x->n - 1;
+    for (int64_t t = first; t <= last; ++t)
+        if (collide(x + 1, nx - 1, x_row, y + 1, ny - 1, y_row, apart + t * step)) return true;
+    return false;
+}
+bool collide(const void* a, const Span& x, const void* b, const Span& y, const h3qk_cache& c)
+{
+    if (c.pages == 0) return false;
+    Step dx[3], dy[3];
+    const int nx = x.steps(c, dx), ny = y.steps(c, dy);
+    return collide(dx, nx, x.row_bytes, dy, ny, y.row_bytes,
+                   static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)));
 }
 
 }  // namespace
@@ -447,13 +474,13 @@ h3qk_status h3qk_pages::check_pool(const h3qk_cache* cache, bool written, Pool* 
         if ((st = check_strides(c, c.k_scales, c.k_scale_strides, c.head_dim / 16, 1, false, &s[2])) != H3QK_OK) return st;
         if ((st = check_strides(c, c.v_scales, c.v_scale_strides, c.head_dim / 16, 1, false, &s[3])) != H3QK_OK) return st;
     }
-    if (written)
-        for (int i = 0; i < parts; ++i) {
+    if (written) {
+        for (int i = 0; i < parts; ++i)
             if (!disjoint_rows(s[i], c)) return H3QK_ERR_ALIAS;
+        for (int i = 0; i < parts; ++i)
             for (int k = i + 1; k < parts; ++k)
-                if (collide(static_cast<uint8_t*>(data[i]), s[i], static_cast<uint8_t*>(data[k]), s[k], c))
-                    return H3QK_ERR_ALIAS;
-        }
+                if (collide(data[i], s[i], data[k], s[k], c)) return H3QK_ERR_ALIAS;
+    }
     for (int i = 0; i < 4; ++i) ranges->data[i] = range_of(data[i], i < parts ? s[i].all(c) : 0);
     ranges->lists[0] = range_of(c.block_table, c.max_pages ? ((c.batch - 1) * stride + c.max_pages) * 4 : 0);
     ranges->lists[1] = range_of(c.kv_lens, c.batch * 4);
