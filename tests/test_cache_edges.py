@@ -129,3 +129,38 @@ def test_no_overlap_of_a_written_pool_is_missed(no_gpu):  # noqa: F811
         elif k_st == v_st:
             assert not apart_rows, (kv, pages, k_st, v_st, apart)
     assert taken > 300
+
+
+def called(packed_calls, cache):
+    """h3qk_cache of a call, unpacked."""
+    cache_attention(torch.empty(2, 4, 64, dtype=F16), cache, torch.zeros(2, 4, dtype=I32), torch.ones(2, dtype=I32))
+    pool = packed_calls.pop()[0]
+    return cache_module._POOL.unpack(pool[:cache_module._POOL.size])
+
+
+CHANGES = {
+    "shape": lambda t: t.resize_(2, 2, 64, 64), "fewer": lambda t: t.resize_(1, 2, 64, 64), "more": lambda t: t.resize_(300, 2, 64, 64),
+    "turned": lambda t: t.transpose_(1, 2), "set": lambda t: t.set_(torch.empty(1, 2, 64, 64, dtype=t.dtype)),
+    "data": lambda t: setattr(t, "data", torch.empty(1, 2, 64, 64, dtype=t.dtype)),
+    "part": lambda t: t.set_(t.untyped_storage(), 8, (1, 2, 64, 56)),
+}
+
+
+@pytest.mark.parametrize("change", list(CHANGES))
+@pytest.mark.parametrize("fmt", ["e2m1", F16])
+def test_tensors_that_are_changed_in_place(packed_calls, fmt, change):
+    """Other memory is refused; other shapes of the same memory leave the cache as it was made, within that memory."""
+    for name in ("k", "v") if fmt == F16 else ("k", "v", "k_scales", "v_scales"):
+        cache = Cache.empty(9, 2, 64, device="cpu", dtype=fmt)
+        was = called(packed_calls, cache)
+        t = getattr(cache, name)
+        CHANGES[change](t)
+        if change in ("set", "data", "part"):
+            with pytest.raises(ValueError, match="other memory"):
+                called(packed_calls, cache)
+            assert not packed_calls
+            continue
+        now = called(packed_calls, cache)
+        assert now[:5] == was[:5] and now[9:] == was[9:]  # all but the addresses
+        at = 5 + ("k", "v", "k_scales", "v_scales").index(name)
+        assert now[at] == t.data_ptr() and t.untyped_storage().nbytes() >= 9 * 2 * 64 * (4 if "scales" in name else 32)

@@ -48,10 +48,12 @@ class Cache:
     to 128; a value is its e2m1 code (channel 2i in the low half of byte i)
     times its group's scale times ``k_scale`` (``v_scale``; 2^-117 to 2^117).  page_size is a
     power of two from 16 on.  ``Cache.empty`` allocates one.  What a cache is made
-    of stays: other tensors or scales are another Cache."""
+    of stays: other tensors or scales are another Cache.  A tensor that is given
+    other memory in place (``set_``, ``data``) is refused at the next call; one
+    that is only given another shape leaves the cache as it was made."""
 
     __slots__ = ("k", "v", "k_scales", "v_scales", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim",
-                 "dtype", "device", "_head", "_tail")
+                 "dtype", "device", "_held", "_head", "_tail")
 
     def __init__(self, k, v, k_scales=None, v_scales=None, *, k_scale: float = 1.0, v_scale: float = 1.0):
         if k.dim() != 4:
@@ -87,6 +89,8 @@ class Cache:
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.dtype, self.device = ("e2m1" if codes else k.dtype), k.device
+        # Views of our own, whose shapes and strides nobody else can change in place.
+        self._held = tuple(t if t is None else t.detach() for t in (k, v, k_scales, v_scales))
         # h3qk_cache but for the addresses, which each call takes anew
         packed = _POOL.pack(E2M1 if codes else _DTYPES[k.dtype], heads, dim, page, pages, 0, 0, 0, 0, *strides, self.k_scale,
                             self.v_scale)
@@ -131,6 +135,10 @@ def _list(t, name, n, dev):
     return _need_lens(t, name, n, dev)  # says what is wrong
 
 
+def _addresses(k, v, ks, vs):
+    return k.data_ptr(), v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr()
+
+
 def _pool(cache, block_table, kv_lens):
     """h3qk_cache as bytes, after checking the table and the lengths: (packed, batch)."""
     dev = cache.device
@@ -146,12 +154,12 @@ def _pool(cache, block_table, kv_lens):
         raise ValueError("block_table must hold at least one sequence, and fewer than 2^30 rows of each")
     if kv_lens is None:
         raise ValueError("kv_lens is required")
-    ks, vs = cache.k_scales, cache.v_scales
-    pointers = _POINTERS.pack(cache.k.data_ptr(), cache.v.data_ptr(), 0 if ks is None else ks.data_ptr(),
-                              0 if vs is None else vs.data_ptr())
+    at = _addresses(*cache._held)
+    if at != _addresses(cache.k, cache.v, cache.k_scales, cache.v_scales):
+        raise ValueError("a tensor of the Cache has other memory than when it was made: make another Cache")
     table = _TABLE.pack(batch, max_pages, block_table.data_ptr(), across if batch > 1 else 0,
                         _list(kv_lens, "kv_lens", batch, dev))
-    return cache._head + pointers + cache._tail + table, batch
+    return cache._head + _POINTERS.pack(*at) + cache._tail + table, batch
 
 
 def _offsets(q_offsets, batch, tokens, dev):
