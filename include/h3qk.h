@@ -647,7 +647,8 @@ typedef struct h3qk_cache_attn {
     int32_t causal;          /* 0 or 1 */
     int32_t max_rows;        /* no sequence has more rows; 0: tokens (without q_offsets: tokens / batch) */
     float scale, softcap;    /* as for h3qk_attention */
-    int64_t tokens;          /* rows of q, below 2^30 */
+    int64_t tokens;          /* rows of q, below 2^30; tokens * heads below 2^31, and the rows of a sequence times
+                                heads / kv_heads at most 2^31 - 256 */
     const void* q;           /* [tokens, heads, head_dim] */
     void* out;               /* as q */
     int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;  /* elements, multiples of 8 */

@@ -164,3 +164,14 @@ def test_tensors_that_are_changed_in_place(packed_calls, fmt, change):
         assert now[:5] == was[:5] and now[9:] == was[9:]  # all but the addresses
         at = 5 + ("k", "v", "k_scales", "v_scales").index(name)
         assert now[at] == t.data_ptr() and t.untyped_storage().nbytes() >= 9 * 2 * 64 * (4 if "scales" in name else 32)
+
+
+@pytest.mark.parametrize("tokens,max_rows,want", [
+    (2 ** 30 - 1, 0, h3qk.ERR_INVALID_ARG), (2 ** 30 - 127, 0, h3qk.ERR_INVALID_ARG), (2 ** 30 - 128, 0, h3qk.ERR_CUDA),
+    (2 ** 30 - 1, 2 ** 30 - 128, h3qk.ERR_CUDA), (2 ** 30 - 1, 1, h3qk.ERR_CUDA),
+])
+def test_rows_of_a_sequence_fit_31_bits_to_full_tiles(no_gpu, tokens, max_rows, want):  # noqa: F811
+    """The kernel counts a sequence's rows times the heads of a K/V head, rounded up to tiles of 256, in 31 bits."""
+    call = dict(tokens=tokens, max_rows=max_rows, heads=2, q=1 << 44, out=1 << 45, lse=1 << 46, qt=128, ot=128,
+                offsets=1 << 47)
+    assert checks.c_attend(call, kv_heads=1) == want

@@ -86,7 +86,8 @@ h3qk_status check_call(const h3qk_cache& c, const h3qk_cache_attn& a, int64_t* r
     if (!a.q_offsets && a.tokens % c.batch) return H3QK_ERR_INVALID_ARG;
     *rows = a.q_offsets ? a.tokens : a.tokens / c.batch;
     if (a.max_rows > 0 && a.max_rows < *rows) *rows = a.max_rows;
-    // packed rows, and the join's grid, fit 31 bits
+    // packed rows to full tiles, all heads' rows, and the join's grid fit 31 bits
+    if (*rows * (a.heads / c.kv_heads) > INT32_MAX + INT64_C(1) - h3qk_core::kRowTile) return H3QK_ERR_INVALID_ARG;
     if (a.tokens * a.heads > INT32_MAX || static_cast<double>(a.heads) * c.batch * kFew > INT32_MAX) return H3QK_ERR_INVALID_ARG;
     return H3QK_OK;
 }
