@@ -580,9 +580,10 @@ int64_t h3qk_attention_stuck(void);
  *   Codes are rows of head_dim / 2 bytes, scales rows of head_dim / 16 bytes,
  *   without gaps between a page's rows; their page and head strides are in
  *   bytes, multiples of 16.  From a group's 16-bit values y:
- *     g = e4m3(max|y| / (6 k_scale)), at least 2^-9, at most 448,
+ *     g = e4m3(max|y| * r), at least 2^-9, at most 448, r = 1 / (6 k_scale),
  *     code = e2m1(y * (1 / (g k_scale))), both to nearest even, saturating;
- *   a group with an infinite or NaN value gets a NaN scale.  code * g is exact
+ *   r is the quotient rounded to binary32, and each product and the reciprocal
+ *   is rounded to it once.  A group with an infinite or NaN value gets a NaN scale.  code * g is exact
  *   in either 16-bit type, so with a k_scale of 1 no reader rounds.
  */
 typedef struct h3qk_cache {
@@ -666,8 +667,8 @@ h3qk_status h3qk_cache_attention(const h3qk_cache* cache, const h3qk_cache_attn*
 /*
  * h3qk_cache_read: rows [starts[b], kv_lens[b]) of each sequence, at most
  * `rows` of them, as dense 16-bit out_k, out_v [batch, kv_heads, rows,
- * head_dim] (contiguous, 16-byte aligned, of dtype: a 16-bit cache's own; what
- * 4 bits stand for, rounded once), with zeros after them.  starts NULL: from
+ * head_dim] (contiguous, 16-byte aligned, of dtype: a 16-bit cache's own; of
+ * 4 bits code * g times k_scale in binary32, rounded), with zeros after them.  starts NULL: from
  * row 0.  The result serves h3qk_attention and its gradient, or another cache.
  * batch * kv_heads is at most 65535.
  */

@@ -1,6 +1,7 @@
 """The paged cache's operators where their documentation allows more than
 ordinary calls make: rows that are not finite beside rows that are,
-sequences that are longer than their table, and the largest and smallest scales."""
+sequences that are longer than their table, the largest and smallest scales,
+and what the 4-bit format's roundings are."""
 import math
 
 import block_util as bu
@@ -146,3 +147,30 @@ def test_append_to_a_pool_with_k_and_v_beside_each_other_in_a_row(monkeypatch, s
     out, _ = cache_attention(q, cache, table, lens)
     want, _ = cu.attention(q, cache, table, [s[1] for s in seqs], list(range(len(seqs) + 1)))
     bu.assert_within(out, want["out"], want["out_bound"], "out")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("scale,maximum", [(1.0, None), (0.37, None), (0.1, 0.0087890625), (0.05, 0.00439453125)])
+def test_every_maximum_gets_the_group_scale_that_the_header_states(scale, maximum, dtype):
+    """max|y| times the binary32 value of 1 / (6 v_scale), rounded to binary32 and then to e4m3: for a few maxima and
+    scales the neighbour of the quotient's."""
+    top = torch.arange(0x7C00 if dtype == F16 else 0x7F80, dtype=torch.int16, device="cuda").view(dtype)
+    rows = top.numel() // 8
+    y = torch.zeros(rows, 8, 16, dtype=dtype, device="cuda")
+    y[:, :, 5] = -top.view(rows, 8)
+    cache = Cache.empty(rows // 256 + 1, 1, 128, page_size=256, dtype="e2m1", v_scale=scale)
+    table = torch.arange(cache.pages, dtype=torch.int32, device="cuda")[None]
+    w = torch.ones(128, device="cuda")
+    qkv = torch.zeros(rows, 3 * 128, dtype=dtype, device="cuda")
+    qkv[:, 256:] = y.view(rows, 128)
+    cache_append(qkv, w, w, cache, table, torch.tensor([rows], dtype=torch.int32, device="cuda"), heads=1, rotary_dim=0)
+    got = cache.v_scales.view(torch.uint8).view(-1, 8)[:rows].flatten()
+    held = float(torch.tensor(scale))  # what binary32 holds of it
+
+    def e4m3(x):
+        return x.float().clamp(2.0 ** -9, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+
+    r = torch.tensor(1.0 / (6.0 * held), dtype=torch.float64, device="cuda").float()
+    assert torch.equal(got, e4m3(top.float() * r))
+    if maximum:  # the quotient is just below the middle of codes 7 and 8, the product on it
+        assert maximum / (6.0 * held) < 7.5 * 2.0 ** -9 and got[top == maximum].tolist() == [8]
