@@ -639,7 +639,9 @@ h3qk_status h3qk_cache_append(const h3qk_cache* cache, const void* qkv, const fl
  * as they were.  A non-finite key reaches the rows that see it, a non-finite
  * value may reach all rows of a sequence that sees it, and rows of the cache
  * that no row sees reach none.  Scores, sums and outputs are binary32.  p is rounded for its
- * product with v: to the type of q, over 4-bit caches always to binary16.  The same call gives the same bits every time.
+ * product with v: to the type of q, over 4-bit caches always to binary16.  Over
+ * those, bfloat16 rows of q are kept to 2^-39 of their largest magnitude: channels
+ * more than 2^31 below it lose digits.  The same call gives the same bits every time.
  * Fill the struct from zeros.
  */
 typedef struct h3qk_cache_attn {

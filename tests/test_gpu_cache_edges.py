@@ -174,3 +174,22 @@ def test_every_maximum_gets_the_group_scale_that_the_header_states(scale, maximu
     assert torch.equal(got, e4m3(top.float() * r))
     if maximum:  # the quotient is just below the middle of codes 7 and 8, the product on it
         assert maximum / (6.0 * held) < 7.5 * 2.0 ** -9 and got[top == maximum].tolist() == [8]
+
+
+@pytest.mark.parametrize("rows", [3, 70])
+@pytest.mark.parametrize("exponent", [0, 20, 28, 36, 40])
+def test_channels_far_below_a_rows_largest_over_4_bits(exponent, rows):
+    """bfloat16 rows with one channel of 2^exponent, which meets zeros: the others are kept to 2^-39 of it."""
+    lens = [300, 200]
+    cache, table, kv_lens = cu.build(lens, 1, 64, 64, "e2m1", v_scale=0.5)
+    cache.k[..., 3] &= 0xF0  # channel 6 of every key: code 0
+    q = torch.randn(2 * rows, 4, 64, device="cuda").to(BF16)
+    q[..., 6] = 2.0 ** exponent
+    out, lse = cache_attention(q, cache, table, kv_lens)
+    want, _ = cu.attention(q, cache, table, lens, [0, rows, 2 * rows])
+    k = torch.nan_to_num(cu.values(cache)[0], nan=0.0).abs().sum(-1).amax()
+    off = 2.0 ** -39 * 2.0 ** exponent * float(k) / 8  # of a score, in binary64
+    bu.assert_within(lse.t(), want["lse"], want["lse_bound"] + off, "lse")
+    if off < 2.0 ** -8:  # scores and lse off by e each move a weight by a factor of exp(2 e), below 1 + 2.01 e
+        spread = 2.01 * off * torch.nan_to_num(cu.values(cache)[1], nan=0.0).abs().amax()
+        bu.assert_within(out, want["out"], want["out_bound"] + spread, "out")

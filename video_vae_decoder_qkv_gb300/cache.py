@@ -262,7 +262,8 @@ def cache_attention(q, cache, block_table, kv_lens, *, q_offsets=None, max_rows:
 
     Returns (out, lse): out like q, lse float32 [heads, tokens].  Rows that
     see nothing have out = 0 and lse = -inf; rows of no sequence are left as
-    they were (uninitialised without ``out``).  The same call gives the same
+    they were (uninitialised without ``out``).  Over 4 bits, bfloat16 rows are
+    kept to 2^-39 of their largest magnitude.  The same call gives the same
     bits every time."""
     dtype, dev = q.dtype, cache.device
     if dtype not in (torch.float16, torch.bfloat16):

@@ -39,8 +39,8 @@
 // 4 bits: e2m1 codes become binary16 in one conversion for two, times their
 // group's scale, exactly.  The products are binary16's whatever the type of
 // q: bfloat16 rows are first scaled by a power of two so that their largest
-// value is near 2^14, which loses nothing that binary32 sums would keep, and P
-// is held 2^11 larger.  V's codes of two neighbouring keys are interleaved by
+// value is near 2^14, which keeps every channel to 2^-39 of that value
+// (raise_of), and P is held 2^11 larger.  V's codes of two neighbouring keys are interleaved by
 // nibbles before their conversion, which makes the pairs that the product
 // takes.
 #include <type_traits>
