@@ -256,8 +256,13 @@ def cache_attention(q, cache, block_table, kv_lens, *, q_offsets=None, max_rows:
     ``kv_lens`` and ``block_table`` as for ``cache_append``: a sequence's
     rows are its last ones, and each sees, with ``causal``, the keys up to its
     own and the first ``prefix_lens`` (int32 [batch]); else all of the
-    sequence's.  ``max_rows``: no sequence has more rows than that (with
-    q_offsets the host does not know; it saves the launch for longer ones).
+    sequence's.  ``max_rows``: no sequence has more rows than that (default:
+    q's rows, without q_offsets those of a sequence).  It chooses the kernel,
+    which up to 32 packed rows (max_rows times heads per K/V head) is the one for
+    few rows: with q_offsets the host does not know the longest sequence, and
+    single tokens of a batch take three times as long without it.  The choice
+    also goes by the table's width: short ones (8,192 rows) of few sequences
+    take one launch, whatever their lengths.
     ``scale``, ``softcap`` and ``slopes`` are ``attention``'s.
 
     Returns (out, lse): out like q, lse float32 [heads, tokens].  Rows that

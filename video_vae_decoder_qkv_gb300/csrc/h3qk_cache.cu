@@ -23,17 +23,19 @@ using h3qk_detail::range_of;
 // offsets, and their angles, once, and walks a slice of the heads, kAhead head
 // rows of copies ahead of itself (in shared memory: loads ahead in
 // registers were waited for together).  13,000 rows of 40 + 2 x 8 heads of 128
-// in 16 bits: 68 us, 5.7 TB/s; 107 with the rows ahead in registers.
+// in 16 bits: 67 us, 5.7 TB/s; 107 with the rows ahead in registers.
 //
 // 4 bits: a group of 16 channels is two neighbouring lanes.  The largest
 // magnitude of its 16-bit values is an integer maximum of their bits (exact,
 // and any infinity or NaN wins it), one exchange joins the lanes, and a lane's
-// 8 codes are one 4-byte store.
+// 8 codes are one 4-byte store.  There the instructions count as much as the
+// bytes: 32,640 rows of 40 + 2 x 8 heads of 128 take 172 us, 4.9 TB/s, with three
+// issue slots of four in use (in 16 bits 155).
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8, kBlocks = 3;  // of a block; of an SM
 // Head rows of copies ahead: the 4-bit form's longer arithmetic hides them
-// behind less (32,640 rows of 40 + 2 x 8 heads of 128, read back: 212 us with 2,
-// 224 with 3; in 16 bits 13,000 rows 70 us with 2, 67 with 3).
+// behind less (32,640 rows of 40 + 2 x 8 heads of 128: 172 us with 2, 192 with
+// 3; in 16 bits 13,000 rows 70 us with 2, 67 with 3).
 constexpr int kAhead4 = 2, kAhead16 = 3;
 
 struct AppendArgs {
@@ -239,8 +241,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const __gr
 // Reading back: a thread takes 8 channels of kReadRows rows of a head at a
 // time, `turns` times, the next turn's rows on their way; K in one half of the
 // grid and V in the other.  Small calls spread over the GPU in one turn.  Four
-// caches of up to 32,768 keys, 8 K/V heads of 128, 4 bits to bf16: 106 us, 6.0
-// TB/s; 116 in one turn a thread.  Bound by HBM: mostly
+// caches of up to 32,768 keys, 8 K/V heads of 128, 4 bits to bf16: 104 us, 6.1
+// TB/s; 157 in one turn a thread.  Bound by HBM: mostly
 // the dense rows' 2 bytes a value on their way out.
 // ---------------------------------------------------------------------------
 constexpr int kReadRows = 3, kReadTurns = 8;

@@ -23,8 +23,9 @@ constexpr int kMostUnits = 16;
 // rows, which reads (and converts) their keys once for 8 or 16 of them; others
 // to the tiles of 256, of which even a row costs a whole softmax.  24 caches of
 // up to 8,192 keys in 4 bits, 20 packed rows, capped scores: 69 us in two tiles
-// of 16, 176 in tiles of 256.  A call that mixes long chunks with single tokens
-// stays in one kernel: two kernels one after the other each left SMs idle.
+// of 16, 152 in tiles of 256.  A call that mixes long chunks with single tokens
+// stays in one kernel, whose equal shares end together, and its tokens take
+// tiles of 256.
 constexpr int kFew = 32;
 
 // How a call is cut, from its sizes alone.

@@ -3,7 +3,7 @@
 //
 // Bound by reading the cache once: 144 bytes a key and K/V head of 128 in
 // 4 bits, 512 in 16.  16 bits reach it: 16 uneven caches of up to 32,768 keys
-// take 210 us, 6.5 TB/s.  4 bits leave a multiprocessor 6.5 cycles a key and
+// take 209 us, 6.5 TB/s.  4 bits leave a multiprocessor 6.5 cycles a key and
 // head, in which its four schedulers issue some 18 instructions (four
 // conversions, five products with scales and P, and what they need): 32 such
 // caches take 130 us, 5.5 TB/s, one of 524,288 keys 112 us.  Twelve warps with
@@ -20,8 +20,10 @@
 //
 // Short caches of few sequences (a token's latency) take one launch: a cluster
 // of kCluster blocks shares a run, and joins its parts through the blocks'
-// shared memory.  One token over 4,896 keys, 4 K/V heads of 64: 6.8 us (with
-// blocks of three warps 7.6, and then with the line and its join 10.7).
+// shared memory.  One token over 4,896 keys, 4 K/V heads of 64: 7.0 us (with
+// blocks of three warps 7.6, and then with the line and its join 10.7); over
+// 8,192 keys, the most that a table may have room for here, 8.5, and with the
+// line over 8,256 11.7.
 //
 // Inside a share the block's warps take turns of keys in round robin, each
 // with its own copies in flight (cp.async into a ring of its own: no barrier

@@ -34,8 +34,8 @@
 //
 // Bound, 16-bit pages: the groups' chains of products and softmax, as in the
 // dense kernel.  40 heads on 8 of 128, bf16, 1,024 rows behind 16,384 keys: 237
-// us, 1.41 PFLOP/s (the dense kernel's tiles of single heads: 323).  4 bits: the
-// same, with the conversions taking issue slots from the softmax: 272 us, 1.22
+// us, 1.40 PFLOP/s (the dense kernel's tiles of single heads: 321).  4 bits: the
+// same, with the conversions taking issue slots from the softmax: 271 us, 1.23
 // PFLOP/s.  Four uneven chunks: 0.67 ms; with the products and barriers alone
 // 0.52, with the softmax alone 0.54.  A warp takes whole blocks of 16 rows, which
 // lie on one page: their page is looked up once and their scales come in one
