@@ -1,5 +1,6 @@
 """The paged cache's operators, without a GPU, where one call could spoil the
 next or a value or layout lies at the edge of what is allowed."""
+import copy
 import math
 import random
 
@@ -155,15 +156,35 @@ def test_tensors_that_are_changed_in_place(packed_calls, fmt, change):
         was = called(packed_calls, cache)
         t = getattr(cache, name)
         CHANGES[change](t)
-        if change in ("set", "data", "part"):
+        moved = t.data_ptr() != was[5 + ("k", "v", "k_scales", "v_scales").index(name)]
+        assert moved or change not in ("set", "data", "part", "more")
+        if moved:
             with pytest.raises(ValueError, match="other memory"):
                 called(packed_calls, cache)
             assert not packed_calls
             continue
-        now = called(packed_calls, cache)
-        assert now[:5] == was[:5] and now[9:] == was[9:]  # all but the addresses
-        at = 5 + ("k", "v", "k_scales", "v_scales").index(name)
-        assert now[at] == t.data_ptr() and t.untyped_storage().nbytes() >= 9 * 2 * 64 * (4 if "scales" in name else 32)
+        assert called(packed_calls, cache) == was
+        assert t.untyped_storage().nbytes() >= 9 * 2 * 64 * (4 if "scales" in name else 32)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", F16])
+def test_copies_of_a_cache_can_be_called(packed_calls, fmt):
+    cache = Cache.empty(9, 2, 64, device="cpu", dtype=fmt)
+    was = called(packed_calls, cache)
+    assert called(packed_calls, copy.copy(cache)) == was
+    other = copy.deepcopy(cache)
+    now = called(packed_calls, other)
+    assert now[:5] == was[:5] and now[9:] == was[9:] and now[5] == other.k.data_ptr() != was[5]
+
+
+def test_the_memory_of_a_cache_stays_its_own(packed_calls):
+    """A tensor that lost its memory and is given a smaller one: that cannot lie at the old address."""
+    cache = Cache.empty(64, 2, 64, device="cpu", dtype=F16)
+    for _ in range(20):
+        cache.k.set_()
+        cache.k.set_(torch.empty(1, 2, 64, 64, dtype=F16))
+        with pytest.raises(ValueError, match="other memory"):
+            called(packed_calls, cache)
 
 
 @pytest.mark.parametrize("tokens,max_rows,want", [

@@ -49,11 +49,12 @@ class Cache:
     times its group's scale times ``k_scale`` (``v_scale``; 2^-117 to 2^117).  page_size is a
     power of two from 16 on.  ``Cache.empty`` allocates one.  What a cache is made
     of stays: other tensors or scales are another Cache.  A tensor that is given
-    other memory in place (``set_``, ``data``) is refused at the next call; one
-    that is only given another shape leaves the cache as it was made."""
+    other memory in place (``set_``, ``data``, a ``resize_`` that grows) is
+    refused at the next call; one that is only given another shape leaves the
+    cache as it was made."""
 
     __slots__ = ("k", "v", "k_scales", "v_scales", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim",
-                 "dtype", "device", "_held", "_head", "_tail")
+                 "dtype", "device", "_held", "_at", "_head", "_tail")
 
     def __init__(self, k, v, k_scales=None, v_scales=None, *, k_scale: float = 1.0, v_scale: float = 1.0):
         if k.dim() != 4:
@@ -89,8 +90,10 @@ class Cache:
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.dtype, self.device = ("e2m1" if codes else k.dtype), k.device
-        # Views of our own, whose shapes and strides nobody else can change in place.
+        # The memory that the strides describe, kept by views of our own: whatever becomes of a tensor in
+        # place, nothing else comes to lie at these addresses.
         self._held = tuple(t if t is None else t.detach() for t in (k, v, k_scales, v_scales))
+        self._at = _addresses(self)
         # h3qk_cache but for the addresses, which each call takes anew
         packed = _POOL.pack(E2M1 if codes else _DTYPES[k.dtype], heads, dim, page, pages, 0, 0, 0, 0, *strides, self.k_scale,
                             self.v_scale)
@@ -100,6 +103,11 @@ class Cache:
         if hasattr(self, "_tail"):
             raise AttributeError(f"{name} of a Cache is fixed: make another Cache")
         object.__setattr__(self, name, value)
+
+    def __reduce__(self):
+        """Copies are made of (copies of) the same tensors."""
+        return (functools.partial(Cache, k_scale=self.k_scale, v_scale=self.v_scale),
+                (self.k, self.v, self.k_scales, self.v_scales))
 
     @staticmethod
     def _need(t, name, shape, dtype, dev):
@@ -135,8 +143,9 @@ def _list(t, name, n, dev):
     return _need_lens(t, name, n, dev)  # says what is wrong
 
 
-def _addresses(k, v, ks, vs):
-    return k.data_ptr(), v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr()
+def _addresses(cache):
+    ks, vs = cache.k_scales, cache.v_scales
+    return (cache.k.data_ptr(), cache.v.data_ptr(), 0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr())
 
 
 def _pool(cache, block_table, kv_lens):
@@ -154,8 +163,8 @@ def _pool(cache, block_table, kv_lens):
         raise ValueError("block_table must hold at least one sequence, and fewer than 2^30 rows of each")
     if kv_lens is None:
         raise ValueError("kv_lens is required")
-    at = _addresses(*cache._held)
-    if at != _addresses(cache.k, cache.v, cache.k_scales, cache.v_scales):
+    at = _addresses(cache)
+    if at != cache._at:
         raise ValueError("a tensor of the Cache has other memory than when it was made: make another Cache")
     table = _TABLE.pack(batch, max_pages, block_table.data_ptr(), across if batch > 1 else 0,
                         _list(kv_lens, "kv_lens", batch, dev))
