@@ -106,7 +106,7 @@ class Cache:
 
     def __reduce__(self):
         """Copies are made of (copies of) the same tensors."""
-        return (functools.partial(Cache, k_scale=self.k_scale, v_scale=self.v_scale),
+        return (functools.partial(type(self), k_scale=self.k_scale, v_scale=self.v_scale),
                 (self.k, self.v, self.k_scales, self.v_scales))
 
     @staticmethod
